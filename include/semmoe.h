@@ -11,12 +11,15 @@
  * CUDA stream:
  *   semmoe_route            router GEMM, fp32 softmax, per-token top-k
  *   semmoe_route_hier       the same over sub-experts, by hierarchical gating
+ *   semmoe_route_select     the same by sigmoid or softmax scores, a choice bias and groups
  *   semmoe_affinity_lookup  token id -> predicted logical rank
  *   semmoe_remote_count     activations per (source rank, destination rank)
  *   semmoe_permute          stable sort of (token, expert) pairs by
  *                           (destination rank, expert) + row gather
  *   semmoe_grouped_ffn      per-expert SwiGLU FFN over the sorted rows
  *   semmoe_grouped_ffn_gather  the same, reading x through the permutation
+ *   semmoe_mx4_grouped_ffn  the same on 4-bit microscaled rows and weights
+ *                           (semmoe_mx4_quantize, _quantize_rows, _dequantize, _grouped_gemm)
  *   semmoe_shared_ffn       dense SwiGLU of the shared experts (optional)
  *   semmoe_combine          un-permute and gate-weighted sum
  * and, around the layer:
@@ -201,6 +204,48 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
                       float* logits_out, const float* sub_logw, int N, const int32_t* k_per_token, int k_uniform,
                       int T, int H, int Ep, int k_max, int32_t* topk_idx, float* topk_w,
                       int32_t* pair_counts, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * semmoe_route_select -- router product and expert choice by score: sigmoid or
+ * softmax scores, a bias that only chooses (load balance without a loss), and
+ * a first choice among groups of experts (experts that live together).  The
+ * pages have no counterpart: layers trained with such a router need it.
+ *
+ *   l = x . Wr^T  (fp32 accumulation, as semmoe_route)
+ *   s_e = 1 / (1 + exp(-l_e))          (SEMMOE_SCORE_SIGMOID)
+ *       = exp(l_e) / sum_i exp(l_i)    (SEMMOE_SCORE_SOFTMAX, over all E)
+ *   c_e = s_e + bias_e                 (fp32)
+ *   groups: experts [g E/n_group, (g+1) E/n_group); a group scores the sum of
+ *   its group_top (1 or 2) largest c; the topk_group best groups stay, equal
+ *   scores keeping the lower group first
+ *   slot j < k_t holds the expert of the j-th largest c among those groups'
+ *   experts, equal c keeping the lower index first; without a bias experts are
+ *   ordered by l (as s, without the ties that rounding s would make)
+ *   w_j = scale * s_j, over sum_{i < k_t} s_i if renorm
+ *
+ * A bias of -inf switches an expert off: it is never taken and adds nothing to
+ * its group's score (a group with every expert off comes last).  A token with
+ * fewer than k_t experts to take has padding (-1, weight 0) in the slots left;
+ * its live pairs are then fewer, which semmoe_permute and the FFN allow (P is
+ * an upper bound).  A bias of NaN or +inf switches its expert off and sets
+ * SEMMOE_DEVERR_NONFINITE; so does a non-finite logit, for its token.
+ *
+ * score       SEMMOE_SCORE_SIGMOID or SEMMOE_SCORE_SOFTMAX
+ * bias        [device] [E] fp32 or NULL
+ * n_group, topk_group  E % n_group == 0, 1 <= topk_group <= n_group (equal: no groups)
+ * group_top   1 or 2
+ * renorm      non-zero: weights sum to `scale`
+ * scale       finite
+ * other arguments as semmoe_route; ws of semmoe_route_select_workspace_size() bytes
+ * Limits: 1 <= E <= 256, 1 <= k_max <= topk_group * E / n_group.
+ */
+enum { SEMMOE_SCORE_SIGMOID = 0, SEMMOE_SCORE_SOFTMAX = 1 };
+size_t semmoe_route_select_workspace_size(int T, int H, int E, int x_dtype, int w_dtype);
+int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_dtype, const float* logits_in,
+                        float* logits_out, int score, const float* bias, int n_group, int topk_group, int group_top,
+                        int renorm, float scale, const int32_t* k_per_token, int k_uniform, int T, int H, int E,
+                        int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts, void* ws, size_t ws_bytes,
+                        void* stream);
 
 /*
  * semmoe_affinity_lookup -- predicted logical rank of each token from its id.
@@ -471,6 +516,87 @@ int semmoe_shared_ffn(const void* x, const void* ws13, const void* ws2, int dtyp
 int semmoe_combine(const void* y_perm, const int32_t* pair_to_sorted, const float* topk_w,
                    const void* y_shared, int dtype, int T, int H, int k_max, int P,
                    void* out, void* stream);
+
+/*
+ * 4-bit microscaled values ("mx4"): 32 consecutive values of a row share one
+ * power-of-two scale, and each is a 4-bit float (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and their negatives).  With a = the largest magnitude of the block,
+ *   scale = 2^max(floor(log2 a) - 2, -127),   value = round-to-nearest-even
+ *   (ties to the even code) of x / scale on that grid, at most 6 in magnitude;
+ * a block holding NaN or an infinity has scale code 255 and stands for 32 NaNs.
+ *
+ * codes   row-major [rows, K/2] bytes, two values each, the lower column in the
+ *         low four bits; code = sign (8) | index into the list above
+ * scales  one byte per block, exponent + 127, in tiles of 128 rows x 128 columns
+ *         (512 bytes): row r of a tile and its column block j at byte
+ *         16 (r % 32) + 4 (r / 32) + j.  ceil(K/128) tiles follow one another
+ *         along K, then the next 128 rows'.  Rows come in groups (the matrices of
+ *         E experts; an expert's sorted rows), and each group starts a row tile.
+ *         Column blocks past K hold 0.
+ * semmoe_mx4_scales_size(rows, K, groups) is enough for any split of `rows`
+ * rows into `groups` groups: (rows / 128 + groups) ceil(K/128) 512 bytes.
+ * Limits: K % 32 == 0; all pointers 16-byte aligned.
+ */
+size_t semmoe_mx4_scales_size(int rows, int K, int groups);
+
+/*
+ * semmoe_mx4_quantize -- codes and scales of x [groups * group_rows, K] (fp32 or
+ * bf16), `groups` groups of group_rows rows.  Expert weights: w2 [E,H,I] is E
+ * groups of H rows; w13 [E,2I,H] is 2E groups of I rows (gate and up halves).
+ * semmoe_mx4_dequantize -- the values they stand for (exact in fp32 and in bf16).
+ */
+int semmoe_mx4_quantize(const void* x, int dtype, int groups, int group_rows, int K, uint8_t* codes, uint8_t* scales,
+                        void* stream);
+int semmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int groups, int group_rows, int K, void* out,
+                          int out_dtype, void* stream);
+
+/*
+ * semmoe_mx4_quantize_rows -- token rows quantised straight into expert order
+ * (the row gather of semmoe_permute and the quantisation in one pass): sorted
+ * row q = pair_to_sorted[t*k_max + j] gets the codes and scales of x[t], scales
+ * in the groups of expert_offsets.  Each token row is read once.
+ *
+ * x              [device] [T,K] fp32 or bf16
+ * pair_to_sorted [device] [T*k_max] int32, expert_offsets [device] [E+1] int32,
+ *                P: from semmoe_permute (its x and x_perm may be NULL)
+ * codes          [device] [P,K/2] out;  scales [device] semmoe_mx4_scales_size(P, K, E) bytes out
+ * Rows outside every group or past P, and offsets that decrease or leave [0, P],
+ * set SEMMOE_DEVERR_PAIRS and are skipped.  Scales of a tile's unused rows keep
+ * what they held.  Limits: 1 <= E <= 256.
+ */
+int semmoe_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32_t* pair_to_sorted, int k_max, int P,
+                             const int32_t* expert_offsets, int E, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * semmoe_mx4_grouped_gemm -- 4-bit rows times their expert's 4-bit matrix: rows
+ * [expert_offsets[b], expert_offsets[b+1]) with expert e = phys_to_expert[b]:
+ *   out[q, n] = sum_k a[q, k] b[e, n, k]      (fp32 accumulation, stored in out_dtype)
+ *
+ * a, a_scales   [device] [P,K] quantised, groups of expert_offsets
+ * b, b_scales   [device] [E,N,K] quantised, E groups of N rows
+ * out           [device] [P,N] fp32 or bf16
+ * Limits: K % 32 == 0, N % 8 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn.
+ */
+int semmoe_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* expert_offsets,
+                            const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,
+                            int N, int K, void* out, int out_dtype, void* stream);
+
+/*
+ * semmoe_mx4_grouped_ffn -- semmoe_grouped_ffn on 4-bit rows and weights:
+ *   h = silu(x W1_e^T) * (x W3_e^T), quantised (from fp32) in blocks of 32;  y = h W2_e^T
+ *
+ * x, x_scales     [device] [P,H] quantised, groups of expert_offsets (semmoe_mx4_quantize_rows)
+ * w13, w13_scales [device] [E,2I,H] quantised as 2E groups of I rows
+ * w2, w2_scales   [device] [E,H,I] quantised as E groups of H rows
+ * y_perm          [device] [P,H] bf16 out (for semmoe_combine)
+ * ws              [device] workspace of semmoe_mx4_grouped_ffn_workspace_size() bytes (256-byte aligned)
+ * Limits: H % 32 == 0, I % 32 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn.
+ */
+size_t semmoe_mx4_grouped_ffn_workspace_size(int P, int E, int I);
+int semmoe_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int32_t* expert_offsets,
+                           const int32_t* phys_to_expert, const uint8_t* w13, const uint8_t* w13_scales,
+                           const uint8_t* w2, const uint8_t* w2_scales, int P, int E, int H, int I, void* y_perm,
+                           void* ws, size_t ws_bytes, void* stream);
 
 /*
  * semmoe_dp_schedule -- online inter-request scheduling of Attention-DP: a

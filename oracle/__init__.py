@@ -33,3 +33,5 @@ from .moe import (  # noqa: F401
 )
 from .scheduling import dp_schedule, transition_lookup  # noqa: F401
 from .prism import hier_route, split_expert_weights, sub_scores  # noqa: F401
+from .mx4 import mx4_encode, mx4_grouped_ffn, mx4_grouped_product, mx4_round, mx4_values  # noqa: F401
+from .select import choice_scores, route_select, scores  # noqa: F401

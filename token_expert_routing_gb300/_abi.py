@@ -22,6 +22,8 @@ SEMMOE_F32_SPLIT = 2   # router weight only: the output of semmoe_route_split_we
 # grouped-FFN kernel forms (semmoe_grouped_ffn_form)
 SEMMOE_FORM_DEFAULT, SEMMOE_FORM_SINGLE, SEMMOE_FORM_PAIR1, SEMMOE_FORM_PAIR, SEMMOE_FORM_SINGLE_TMA_GATHER, \
     SEMMOE_FORM_CUDA_CORE, SEMMOE_FORM_FUSED = range(7)
+# scores of semmoe_route_select
+SEMMOE_SCORE_SIGMOID, SEMMOE_SCORE_SOFTMAX = 0, 1
 # device error word bits (semmoe_check_errors)
 SEMMOE_DEVERR_EXPERT, SEMMOE_DEVERR_TOKEN_ID, SEMMOE_DEVERR_LUT, SEMMOE_DEVERR_K, SEMMOE_DEVERR_PAIRS, \
     SEMMOE_DEVERR_TIMEOUT, SEMMOE_DEVERR_NONFINITE, SEMMOE_DEVERR_OFFSETS, SEMMOE_DEVERR_RANK = \
@@ -29,7 +31,7 @@ SEMMOE_DEVERR_EXPERT, SEMMOE_DEVERR_TOKEN_ID, SEMMOE_DEVERR_LUT, SEMMOE_DEVERR_K
 
 _DTYPE = {torch.float32: SEMMOE_F32, torch.bfloat16: SEMMOE_BF16}
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
 # name -> (restype, argtypes), in the order of include/semmoe.h
 SIGNATURES = {
@@ -46,6 +48,9 @@ SIGNATURES = {
     "semmoe_route_hier_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "semmoe_route_hier": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                                _sz, _vp]),
+    "semmoe_route_select_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "semmoe_route_select": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _f, _vp, _i, _i, _i, _i, _i, _vp,
+                                 _vp, _vp, _vp, _sz, _vp]),
     "semmoe_affinity_lookup": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "semmoe_remote_count": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "semmoe_permute_workspace_size": (_sz, [_i, _i, _i]),
@@ -65,6 +70,13 @@ SIGNATURES = {
     "semmoe_shared_ffn_workspace_size": (_sz, [_i, _i, _i]),
     "semmoe_shared_ffn": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_combine": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
+    "semmoe_mx4_scales_size": (_sz, [_i, _i, _i]),
+    "semmoe_mx4_quantize": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "semmoe_mx4_dequantize": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp]),
+    "semmoe_mx4_quantize_rows": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp]),
+    "semmoe_mx4_grouped_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]),
+    "semmoe_mx4_grouped_ffn_workspace_size": (_sz, [_i, _i, _i]),
+    "semmoe_mx4_grouped_ffn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_selftest_bounded_wait": (_i, [_vp]),
     "semmoe_selftest_fused_ready_wait": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_dp_schedule": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -116,6 +128,12 @@ def _p(t) -> ctypes.c_void_p | None:
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _want(t, dtype, numel, what):
+    """Refuse a tensor of another type, or of fewer elements than the library will touch (None passes)."""
+    if t is not None and (t.dtype != dtype or t.numel() < numel):
+        raise ValueError(f"{what}: expected at least {numel} elements of {dtype}, got {t.numel()} of {t.dtype}")
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -205,6 +223,29 @@ def semmoe_route_hier(x, w_parent, logits_in, logits_out, sub_logw, N, k_per_tok
     _check(lib().semmoe_route_hier(_p(x), xd, _p(w_parent), wd, _p(logits_in), _p(logits_out), _p(sub_logw), N,
                                    _p(k_per_token), k_uniform, T, H, Ep, k_max, _p(topk_idx), _p(topk_w),
                                    _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def semmoe_route_select_workspace_size(T, H, E, x_dtype: int, w_dtype: int) -> int:
+    return lib().semmoe_route_select_workspace_size(T, H, E, x_dtype, w_dtype)
+
+
+def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_group, topk_group, group_top, renorm,
+                        scale, k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w, ws=None, stream=None,
+                        w_dtype=None, pair_counts=None):
+    """Router product and expert choice by score, bias and groups.  ``score`` is
+    SEMMOE_SCORE_SIGMOID or SEMMOE_SCORE_SOFTMAX, ``bias`` [E] fp32 or None; ``ws``
+    defaults to a fresh workspace of the size the library asks for; ``w_dtype``
+    and ``pair_counts`` as in semmoe_route."""
+    _want(bias, torch.float32, E, "bias")
+    xd = dtype_code(x) if x is not None else SEMMOE_F32
+    wd = w_dtype if w_dtype is not None else (dtype_code(w_router) if w_router is not None else SEMMOE_F32)
+    if ws is None:
+        n = semmoe_route_select_workspace_size(T, max(H, 1), E, xd, wd)
+        ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
+    _check(lib().semmoe_route_select(_p(x), xd, _p(w_router), wd, _p(logits_in), _p(logits_out), score, _p(bias),
+                                     n_group, topk_group, group_top, int(bool(renorm)), float(scale),
+                                     _p(k_per_token), k_uniform, T, H, E, k_max, _p(topk_idx), _p(topk_w),
+                                     _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_affinity_lookup(token_ids, lut, V, R, T, pred_rank, stream=None):
@@ -307,6 +348,61 @@ def semmoe_dp_schedule(pred_rank, req_offsets, T, n_req, R, hist, req_rank, req_
 def semmoe_transition_lookup(topk_idx, k_per_token, k_uniform, trans, T, k_max, E, R, pred_next, stream=None):
     _check(lib().semmoe_transition_lookup(_p(topk_idx), _p(k_per_token), k_uniform, _p(trans), T, k_max, E, R,
                                           _p(pred_next), _stream(stream)))
+
+
+def semmoe_mx4_scales_size(rows, K, groups) -> int:
+    return lib().semmoe_mx4_scales_size(rows, K, groups)
+
+
+def _mx4(codes, scales, rows, K, row_tiles, what):
+    """Codes and scales of ``rows`` rows of K values in ``row_tiles`` 128-row tiles."""
+    _want(codes, torch.uint8, rows * (K // 2), what)
+    _want(scales, torch.uint8, row_tiles * (-(-K // 128)) * 512, what + " scales")
+
+
+def semmoe_mx4_quantize(x, groups, group_rows, K, codes, scales, stream=None):
+    """x [groups * group_rows, K] (fp32 or bf16) to 4-bit codes [rows, K/2] and scales (uint8)."""
+    _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
+    _check(lib().semmoe_mx4_quantize(_p(x), dtype_code(x), groups, group_rows, K, _p(codes), _p(scales),
+                                     _stream(stream)))
+
+
+def semmoe_mx4_dequantize(codes, scales, groups, group_rows, K, out, stream=None):
+    """The values that codes and scales stand for, in out's type (fp32 or bf16; exact in both)."""
+    _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
+    _check(lib().semmoe_mx4_dequantize(_p(codes), _p(scales), groups, group_rows, K, _p(out), dtype_code(out),
+                                       _stream(stream)))
+
+
+def semmoe_mx4_quantize_rows(x, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes, scales, stream=None):
+    """Token rows x [T, K] quantised into expert order (see include/semmoe.h)."""
+    _mx4(codes, scales, P, K, P // 128 + E, "codes")
+    _check(lib().semmoe_mx4_quantize_rows(_p(x), dtype_code(x), T, K, _p(pair_to_sorted), k_max, P,
+                                          _p(expert_offsets), E, _p(codes), _p(scales), _stream(stream)))
+
+
+def semmoe_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream=None):
+    """4-bit rows [P, K] times their expert's 4-bit matrix [N, K] into out [P, N] (fp32 or bf16)."""
+    _mx4(a, a_scales, P, K, P // 128 + E, "a")
+    _mx4(b, b_scales, E * N, K, E * (-(-N // 128)), "b")
+    _check(lib().semmoe_mx4_grouped_gemm(_p(a), _p(a_scales), _p(expert_offsets), _p(phys_to_expert), _p(b),
+                                         _p(b_scales), P, E, N, K, _p(out), dtype_code(out), _stream(stream)))
+
+
+def semmoe_mx4_grouped_ffn_workspace_size(P, E, I) -> int:
+    return lib().semmoe_mx4_grouped_ffn_workspace_size(P, E, I)
+
+
+def semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I,
+                           y_perm, ws, stream=None):
+    """SwiGLU experts on 4-bit rows and weights, y_perm [P, H] bf16."""
+    _mx4(x, x_scales, P, H, P // 128 + E, "x")
+    _mx4(w13, w13_scales, 2 * E * I, H, 2 * E * (-(-I // 128)), "w13")
+    _mx4(w2, w2_scales, E * H, I, E * (-(-H // 128)), "w2")
+    _want(y_perm, torch.bfloat16, P * H, "y_perm")
+    _check(lib().semmoe_mx4_grouped_ffn(_p(x), _p(x_scales), _p(expert_offsets), _p(phys_to_expert), _p(w13),
+                                        _p(w13_scales), _p(w2), _p(w2_scales), P, E, H, I, _p(y_perm), _p(ws),
+                                        ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_selftest_bounded_wait(stream=None):

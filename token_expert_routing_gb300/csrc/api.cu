@@ -82,7 +82,8 @@ int semmoe_check_errors(void* stream, int* bits) {
   if (e != cudaSuccess) return cuda_status(e, "semmoe_check_errors");
   int b = 0;
   if (route_take_errors(s, &b) || permute_take_errors(s, &b) || ffn_take_errors(s, &b) ||
-      combine_take_errors(s, &b) || schedule_take_errors(s, &b) || selftest_take_errors(s, &b))
+      combine_take_errors(s, &b) || schedule_take_errors(s, &b) || selftest_take_errors(s, &b) ||
+      mx4_take_errors(s, &b) || mx4_gemm_take_errors(s, &b))
     return cuda_status(cudaGetLastError(), "semmoe_check_errors: reading the device error word");
   if (bits != nullptr) *bits = b;
   if (b & SEMMOE_DEVERR_TIMEOUT) return fail(SEMMOE_ERR_DEVICE_TIMEOUT, "a bounded in-kernel wait ran out (bits 0x%x)", b);
@@ -190,6 +191,54 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
                                        k_per_token, k_uniform, T, H, Ep, k_max, topk_idx, topk_w, pair_counts, ws,
                                        static_cast<cudaStream_t>(stream)),
                      "semmoe_route_hier");
+}
+
+size_t semmoe_route_select_workspace_size(int T, int H, int E, int x_dtype, int w_dtype) {
+  return semmoe_route_hier_workspace_size(T, H, E, x_dtype, w_dtype);  // logits for a selection kernel of their own
+}
+
+int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_dtype, const float* logits_in,
+                        float* logits_out, int score, const float* bias, int n_group, int topk_group, int group_top,
+                        int renorm, float scale, const int32_t* k_per_token, int k_uniform, int T, int H, int E,
+                        int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts, void* ws, size_t ws_bytes,
+                        void* stream) {
+  const char* fn = "semmoe_route_select";
+  REQUIRE(T >= 0, "%s: T = %d < 0", fn, T);
+  REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
+  REQUIRE(k_max >= 1 && k_max <= E, "%s: k_max = %d outside [1, E = %d]", fn, k_max, E);
+  REQUIRE((long long)T * E < (1LL << 31), "%s: T * E too large", fn);
+  REQUIRE(score == SEMMOE_SCORE_SIGMOID || score == SEMMOE_SCORE_SOFTMAX, "%s: bad score %d", fn, score);
+  REQUIRE(n_group >= 1 && E % n_group == 0, "%s: n_group = %d does not divide E = %d", fn, n_group, E);
+  REQUIRE(topk_group >= 1 && topk_group <= n_group, "%s: topk_group = %d outside [1, n_group = %d]", fn, topk_group,
+          n_group);
+  REQUIRE(group_top == 1 || group_top == 2, "%s: group_top = %d is neither 1 nor 2", fn, group_top);
+  REQUIRE(k_max <= (long long)topk_group * (E / n_group), "%s: k_max = %d exceeds the %d experts of %d groups", fn,
+          k_max, topk_group * (E / n_group), topk_group);
+  REQUIRE(scale == scale && scale - scale == 0.0f, "%s: scale is not finite", fn);
+  REQUIRE(k_per_token != nullptr || (k_uniform >= 1 && k_uniform <= k_max), "%s: k_uniform = %d outside [1, k_max = %d]",
+          fn, k_uniform, k_max);
+  if (T == 0) return SEMMOE_OK;
+  REQUIRE(topk_idx != nullptr && topk_w != nullptr, "%s: null output pointer", fn);
+  if (logits_in == nullptr) {
+    REQUIRE(x != nullptr && w_router != nullptr, "%s: null x or w_router without logits_in", fn);
+    REQUIRE(valid_dtype(x_dtype) && valid_router_dtype(w_dtype, x_dtype, H), "%s: bad dtype (%d, %d)", fn, x_dtype,
+            w_dtype);
+    REQUIRE(H >= 1, "%s: H = %d < 1", fn, H);
+    REQUIRE(aligned(x, 16) && aligned(w_router, 16), "%s: x and w_router must be 16-byte aligned", fn);
+    const size_t need = route_hier_ws_bytes(T, H, E, x_dtype, w_dtype);
+    REQUIRE(need == 0 || (ws != nullptr && aligned(ws, 256) && ws_bytes >= need),
+            "%s: workspace null, not 256-byte aligned or below %zu bytes", fn, need);
+  } else {
+    REQUIRE(aligned(logits_in, 4), "%s: misaligned logits_in", fn);
+  }
+  REQUIRE(aligned(topk_idx, 4) && aligned(topk_w, 4) && aligned(logits_out, 4) && aligned(k_per_token, 4) &&
+              aligned(bias, 4) && aligned(pair_counts, 16),
+          "%s: misaligned pointer", fn);
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_route_select(x, x_dtype, w_router, w_dtype, logits_in, logits_out, score, bias, n_group,
+                                         topk_group, group_top, renorm != 0, scale, k_per_token, k_uniform, T, H, E,
+                                         k_max, topk_idx, topk_w, pair_counts, ws, static_cast<cudaStream_t>(stream)),
+                     fn);
 }
 
 int semmoe_affinity_lookup(const int32_t* token_ids, const int32_t* lut, int V, int R, int T, int32_t* pred_rank,
@@ -474,6 +523,116 @@ int semmoe_transition_lookup(const int32_t* topk_idx, const int32_t* k_per_token
   return cuda_status(launch_transition_lookup(topk_idx, k_per_token, k_uniform, trans, T, k_max, E, R, pred_next,
                                               static_cast<cudaStream_t>(stream)),
                      "semmoe_transition_lookup");
+}
+
+size_t semmoe_mx4_scales_size(int rows, int K, int groups) {
+  if (rows < 0 || K < 32 || K % 32 != 0 || groups < 1) return 0;
+  return mx4_scale_bytes(rows, K, groups);
+}
+
+static int check_mx4_matrix(const char* fn, int groups, int group_rows, int K, const void* full, int dtype,
+                            const void* codes, const void* scales) {
+  REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
+  REQUIRE(groups >= 1 && group_rows >= 0, "%s: bad sizes groups=%d group_rows=%d", fn, groups, group_rows);
+  REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
+  REQUIRE((long long)groups * group_rows < (1LL << 31), "%s: groups * group_rows too large", fn);
+  if (group_rows == 0) return SEMMOE_OK;
+  REQUIRE(full && codes && scales, "%s: null pointer", fn);
+  REQUIRE(aligned(full, 16) && aligned(codes, 16) && aligned(scales, 16), "%s: pointers must be 16-byte aligned", fn);
+  return SEMMOE_OK;
+}
+
+int semmoe_mx4_quantize(const void* x, int dtype, int groups, int group_rows, int K, uint8_t* codes, uint8_t* scales,
+                        void* stream) {
+  const char* fn = "semmoe_mx4_quantize";
+  int rc = check_mx4_matrix(fn, groups, group_rows, K, x, dtype, codes, scales);
+  if (rc != SEMMOE_OK || group_rows == 0) return rc;
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_quantize(x, dtype, groups, group_rows, K, codes, scales,
+                                         static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+int semmoe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int groups, int group_rows, int K, void* out,
+                          int out_dtype, void* stream) {
+  const char* fn = "semmoe_mx4_dequantize";
+  int rc = check_mx4_matrix(fn, groups, group_rows, K, out, out_dtype, codes, scales);
+  if (rc != SEMMOE_OK || group_rows == 0) return rc;
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_dequantize(codes, scales, groups, group_rows, K, out, out_dtype,
+                                           static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+int semmoe_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32_t* pair_to_sorted, int k_max, int P,
+                             const int32_t* expert_offsets, int E, uint8_t* codes, uint8_t* scales, void* stream) {
+  const char* fn = "semmoe_mx4_quantize_rows";
+  REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
+  REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
+  REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
+  REQUIRE(T >= 0 && k_max >= 1 && (long long)T * k_max < (1LL << 31), "%s: bad sizes T=%d k_max=%d", fn, T, k_max);
+  REQUIRE(P >= 0 && P <= (long long)T * k_max, "%s: P = %d outside [0, T * k_max]", fn, P);
+  if (P == 0) return SEMMOE_OK;
+  REQUIRE(x && pair_to_sorted && expert_offsets && codes && scales, "%s: null pointer", fn);
+  REQUIRE(aligned(x, 16) && aligned(codes, 16) && aligned(scales, 16), "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(aligned(pair_to_sorted, 4) && aligned(expert_offsets, 4), "%s: misaligned table", fn);
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_quantize_rows(x, dtype, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes,
+                                              scales, static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+static int check_mx4_product(const char* fn, int P, int E, int N, int K, const void* a, const void* a_scales,
+                             const void* offsets, const void* experts, const void* b, const void* b_scales,
+                             const void* out) {
+  REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
+  REQUIRE(P >= 0, "%s: P = %d < 0", fn, P);
+  REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
+  REQUIRE(N >= 8 && N % 8 == 0, "%s: N = %d is not a positive multiple of 8", fn, N);
+  REQUIRE((long long)P / 128 + E < (1LL << 31) / ((N + 127) / 128), "%s: P * N too large", fn);
+  if (P == 0) return SEMMOE_OK;
+  REQUIRE(a && a_scales && offsets && experts && b && b_scales && out, "%s: null pointer", fn);
+  REQUIRE(aligned(a, 16) && aligned(a_scales, 16) && aligned(b, 16) && aligned(b_scales, 16) && aligned(out, 16),
+          "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(aligned(offsets, 4) && aligned(experts, 4), "%s: misaligned table", fn);
+  return SEMMOE_OK;
+}
+
+int semmoe_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* expert_offsets,
+                            const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,
+                            int N, int K, void* out, int out_dtype, void* stream) {
+  const char* fn = "semmoe_mx4_grouped_gemm";
+  REQUIRE(valid_dtype(out_dtype), "%s: bad dtype %d", fn, out_dtype);
+  int rc = check_mx4_product(fn, P, E, N, K, a, a_scales, expert_offsets, phys_to_expert, b, b_scales, out);
+  if (rc != SEMMOE_OK || P == 0) return rc;
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out,
+                                             out_dtype, static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+size_t semmoe_mx4_grouped_ffn_workspace_size(int P, int E, int I) {
+  if (P < 0 || E < 1 || I < 32 || I % 32 != 0) return 0;
+  return mx4_ffn_ws_bytes(P, E, I);
+}
+
+int semmoe_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int32_t* expert_offsets,
+                           const int32_t* phys_to_expert, const uint8_t* w13, const uint8_t* w13_scales,
+                           const uint8_t* w2, const uint8_t* w2_scales, int P, int E, int H, int I, void* y_perm,
+                           void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "semmoe_mx4_grouped_ffn";
+  REQUIRE(I >= 32 && I % 32 == 0, "%s: I = %d is not a positive multiple of 32", fn, I);
+  int rc = check_mx4_product(fn, P, E, H > I ? H : I, H, x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales,
+                             y_perm);
+  if (rc != SEMMOE_OK || P == 0) return rc;
+  REQUIRE(w2 && w2_scales, "%s: null pointer", fn);
+  REQUIRE(aligned(w2, 16) && aligned(w2_scales, 16), "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(ws != nullptr && aligned(ws, 256) && ws_bytes >= mx4_ffn_ws_bytes(P, E, I),
+          "%s: workspace null, not 256-byte aligned or below %zu bytes", fn, mx4_ffn_ws_bytes(P, E, I));
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2,
+                                            w2_scales, P, E, H, I, y_perm, ws, static_cast<cudaStream_t>(stream)),
+                     fn);
 }
 
 int semmoe_selftest_bounded_wait(void* stream) {

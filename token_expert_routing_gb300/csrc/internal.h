@@ -19,6 +19,8 @@ int ffn_take_errors(cudaStream_t s, int* bits);
 int combine_take_errors(cudaStream_t s, int* bits);
 int schedule_take_errors(cudaStream_t s, int* bits);
 int selftest_take_errors(cudaStream_t s, int* bits);
+int mx4_take_errors(cudaStream_t s, int* bits);
+int mx4_gemm_take_errors(cudaStream_t s, int* bits);
 cudaError_t launch_selftest_bounded_wait(cudaStream_t s);
 cudaError_t launch_selftest_fused_ready_wait(const void* x, const void* w13, const void* w2, int P, int H, int I,
                                              void* y, void* ws, cudaStream_t s);
@@ -59,6 +61,13 @@ cudaError_t launch_route_hier(const void* x, int x_dtype, const void* w, int w_d
                               float* logits_out, const float* sub_logw, int N, const int32_t* kpt, int k_uniform,
                               int T, int H, int Ep, int k_max, int32_t* topk_idx, float* topk_w,
                               int32_t* pair_counts, void* ws, cudaStream_t s);
+
+// Expert choice by score: sigmoid or softmax, a choice bias, groups.
+cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w_dtype, const float* logits_in,
+                                float* logits_out, int score, const float* bias, int n_group, int topk_group,
+                                int group_top, int renorm, float scale, const int32_t* kpt, int k_uniform, int T,
+                                int H, int E, int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts,
+                                void* ws, cudaStream_t s);
 
 cudaError_t launch_affinity_lookup(const int32_t* token_ids, const int32_t* lut, int V, int R,
                                    int T, int32_t* pred, cudaStream_t s);
@@ -122,5 +131,23 @@ cudaError_t launch_dp_schedule(const int32_t* pred, const int32_t* off, int T, i
 
 cudaError_t launch_transition_lookup(const int32_t* topk_idx, const int32_t* kpt, int ku, const float* trans, int T,
                                      int k_max, int E, int R, int32_t* pred_next, cudaStream_t s);
+
+// 4-bit microscaled values (mx4.cuh): quantisation (mx4.cu) and grouped products (mx4_gemm.cu).
+size_t mx4_scale_bytes(long long rows, int K, int groups);
+cudaError_t launch_mx4_quantize(const void* x, int dtype, int groups, int group_rows, int K, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32_t* pair_to_sorted, int k_max,
+                                     int P, const int32_t* expert_offsets, int E, uint8_t* codes, uint8_t* scales,
+                                     cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int groups, int group_rows, int K,
+                                  void* out, int dtype, cudaStream_t s);
+cudaError_t launch_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* offsets,
+                                    const int32_t* experts, const uint8_t* b, const uint8_t* b_scales, int P, int E,
+                                    int N, int K, void* out, int out_dtype, cudaStream_t s);
+size_t mx4_ffn_ws_bytes(int P, int E, int I);
+cudaError_t launch_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int32_t* offsets,
+                                   const int32_t* experts, const uint8_t* w13, const uint8_t* w13_scales,
+                                   const uint8_t* w2, const uint8_t* w2_scales, int P, int E, int H, int I, void* y,
+                                   void* ws, cudaStream_t s);
 
 }  // namespace semmoe
