@@ -10,11 +10,12 @@
 //               (128-byte rows, 128-byte swizzle) and their scales (512-byte tiles)
 //   warp 1      allocates TMEM; one thread copies the stage's scales to TMEM
 //               (tcgen05.cp) and issues the MMAs (K 64 each)
-//   warps 2..5  epilogue
-// A stage's scales have TMEM columns of their own (one set per stage), so they
-// are overwritten only after the MMAs that read them have completed: the copy
-// waits for the stage's operands, which the producer loads only after the
-// commit of those MMAs.
+//   warps 2..9  epilogue: two groups of four, each one half of the tile's columns
+// TMEM: two accumulators of 256 columns that share 48 of them, [0, 256) and
+// [208, 464), and two sets of scales in the 48 columns left, so that the epilogue
+// of a tile runs beside the next tile's MMAs: it loads the shared columns first
+// and then lets the MMAs go on.  A set of scales is overwritten only after the
+// commit of the MMAs that read it, two stages before.
 //
 // Every wait is bounded; a wait that runs out sets the timeout bit of the device
 // error word and an abort flag, after which every role stops, loads and MMAs in
@@ -40,14 +41,16 @@ constexpr int A_BYTES = BM * BK / 2;   // 16 KB
 constexpr int B_BYTES = BN * BK / 2;   // 32 KB
 constexpr int SC_BYTES = 6 * kTileBytes;  // two column tiles of A's and of B's two row tiles
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int THREADS = 192;
+constexpr int THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t SC_COL = 256;       // first column of the scales; the accumulator takes [0, 256)
-constexpr uint32_t SC_COLS = 24;       // columns of one stage's scales: 2 x (4 for A + 8 for B)
+constexpr uint32_t SC_COLS = 24;       // columns of one set of scales: 2 x (4 for A + 8 for B)
+constexpr uint32_t SC_COL = TMEM_COLS - 2 * SC_COLS;  // the scales' first column
+constexpr uint32_t ACC1_COL = SC_COL - BN;            // the second accumulator's first column (the first one's is 0)
+static_assert(BN - ACC1_COL <= 64, "the epilogue's first pieces hold the shared columns");
 constexpr int MAX_GROUPS = 256;
 
 struct Shared {
-  uint64_t full[STAGES], empty[STAGES], tfull, tempty, done;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty, done;
   uint32_t tmem_base;
   int abort_flag;
   int armed;  // stage positions the producer has armed
@@ -57,7 +60,7 @@ struct Shared {
   int tp[MAX_GROUPS + 1];
 };
 
-constexpr int OUT_STAGE_BYTES = 4 * 4096;  // 4 KB per epilogue warp
+constexpr int OUT_STAGE_BYTES = 8 * 2048;  // 2 KB per epilogue warp
 constexpr size_t kSmemBytes =
     1024 + (size_t)STAGES * (STAGE_BYTES + SC_BYTES) + OUT_STAGE_BYTES + sizeof(Shared);
 
@@ -111,26 +114,26 @@ __device__ __forceinline__ void decode_mtile(const Shared& sh, int G, int mu, in
   e = sh.pe[lo];
 }
 
-// Output of a 128-byte piece of an epilogue warp's 32 tile rows (w: the thread's
-// row, 32 words): transposed through the warp's 4 KB of shared memory (16-byte
-// piece v of row r at piece v ^ (r & 7)) so that eight lanes write one row's
-// 128 bytes.  orow0: the warp's first row at the piece's first column; bytes: row
+// Output of a 64-byte piece of an epilogue warp's 32 tile rows (w: the thread's
+// row, 16 words): transposed through the warp's 2 KB of shared memory (16-byte
+// piece v of row r at piece v ^ (r / 2 & 3)) so that four lanes write one row's
+// 64 bytes.  orow0: the warp's first row at the piece's first column; bytes: row
 // bytes left from there (a multiple of 16); rows: valid rows.
-__device__ __forceinline__ void emit(unsigned char* stage, const uint32_t (&w)[32], unsigned char* orow0, size_t stride,
+__device__ __forceinline__ void emit(unsigned char* stage, const uint32_t* w, unsigned char* orow0, size_t stride,
                                      int bytes, int rows, int lane) {
+  __syncwarp();
 #pragma unroll
-  for (int v = 0; v < 8; ++v)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+  for (int v = 0; v < 4; ++v)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
   __syncwarp();
-  const int v = lane & 7;
+  const int v = lane & 3;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + (lane >> 3);
-    const uint4 d = *reinterpret_cast<const uint4*>(stage + r * 128 + ((v ^ (r & 7)) << 4));
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 d = *reinterpret_cast<const uint4*>(stage + r * 64 + ((v ^ ((r >> 1) & 3)) << 4));
     if (r < rows && v * 16 < bytes) *reinterpret_cast<uint4*>(orow0 + (size_t)r * stride + v * 16) = d;
   }
-  __syncwarp();
 }
 
 // What a launch multiplies.
@@ -165,8 +168,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
-    mbar_init(&sh.tfull, 1);
-    mbar_init(&sh.tempty, 128);
+    for (int a = 0; a < 2; ++a) mbar_init(&sh.tfull[a], 1);
+    mbar_init(&sh.tempty, 256);
     mbar_init(&sh.done, 1);
     sh.abort_flag = 0;
     sh.armed = 0;
@@ -269,19 +272,26 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     if (lane == 0) {
       uint32_t it = 0, acc_it = 0;
       bool ok = true;
-      for (int tile = unit0; ok && tile < total; tile += units) {
-        if (!mbar_wait(&sh.tempty, (acc_it & 1) ^ 1, abort_flag, &g_err)) break;
+      for (int tile = unit0; ok && tile < total; tile += units, ++acc_it) {
+        // the epilogue of the tile before has left the shared columns (and that of two tiles before has ended)
+        if (acc_it > 0 && !mbar_wait(&sh.tempty, (acc_it - 1) & 1, abort_flag, &g_err)) break;
         fence_after();
+        const uint32_t d = tmem + (acc_it & 1) * ACC1_COL;
         for (int kb = 0; kb < kb_n; ++kb, ++it) {
           const int s = it % STAGES;
           if (!mbar_wait(&sh.full[s], (it / STAGES) & 1, abort_flag, &g_err)) {
             ok = false;
             break;
           }
+          // the MMAs of two stages before have read this set of scales
+          if (it >= 2 && !mbar_wait(&sh.empty[(it - 2) % STAGES], ((it - 2) / STAGES) & 1, abort_flag, &g_err)) {
+            ok = false;
+            break;
+          }
           fence_after();
           const uint32_t sa = smem_u32(stage_a + s * A_BYTES), sb = smem_u32(stage_b + s * B_BYTES);
           const uint32_t ss = smem_u32(stage_s + s * SC_BYTES);
-          const uint32_t ta = tmem + SC_COL + s * SC_COLS, tb = ta + 8;
+          const uint32_t ta = tmem + SC_COL + (it & 1) * SC_COLS, tb = ta + 8;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             copy_scales(ta + 4 * c, scale_desc(ss + c * kTileBytes));
@@ -292,93 +302,95 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 #pragma unroll
           for (int k = 0; k < BK / UK; ++k)
             if (k * UK < left)
-              mma_mx4(tmem, sw128_desc(sa + k * UK / 2), sw128_desc(sb + k * UK / 2),
+              mma_mx4(d, sw128_desc(sa + k * UK / 2), sw128_desc(sb + k * UK / 2),
                       idesc_mx4(BM, BN, (uint32_t)(k & 1) * 2), ta + 4 * (k / 2), tb + 8 * (k / 2), (kb | k) != 0);
           commit(&sh.empty[s]);
         }
         if (!ok) break;
-        commit(&sh.tfull);
-        ++acc_it;
+        commit(&sh.tfull[acc_it & 1]);
       }
       commit(&sh.done);
       mbar_drain(&sh.done, 0, &g_err);
     }
   } else {
-    const int q = warp & 3;
+    // Epilogue group w takes pieces (64 output columns; SwiGLU: 32) 3 - w and 1 - w
+    // of the first accumulator, w and 2 + w of the second: the shared columns are
+    // in the first pieces taken.
+    const int q = warp & 3, w = (warp - 2) >> 2;
     const int r = q * 32 + lane;
     uint32_t acc_it = 0;
-    unsigned char* stage = out_stage + q * 4096;
-    for (int tile = unit0; tile < total; tile += units) {
+    unsigned char* stage = out_stage + (warp - 2) * 2048;
+    for (int tile = unit0; tile < total; tile += units, ++acc_it) {
       const int mt = tile / n_tiles, nt = tile % n_tiles;
       int row0, rows, e;
       decode_mtile(sh, G, mt, row0, rows, e);
+      const uint32_t a = acc_it & 1;
       int ok = 1;
-      if (lane == 0) ok = mbar_wait(&sh.tfull, acc_it & 1, abort_flag, &g_err);
+      if (lane == 0) ok = mbar_wait(&sh.tfull[a], (acc_it >> 1) & 1, abort_flag, &g_err);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       fence_after();
-      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + a * ACC1_COL;
       const int wrows = rows - q * 32;  // valid rows of this warp
-      if (GLU) {
-        uint32_t sword = 0;
-        uint8_t* hrow = static_cast<uint8_t*>(pr.out) + (size_t)(row0 + (r < rows ? r : 0)) * (pr.N / 2) + nt * 64;
+      uint8_t* hrow = static_cast<uint8_t*>(pr.out) + (size_t)(row0 + (r < rows ? r : 0)) * (pr.N / 2) + nt * 64;
+      uint8_t* hs = GLU ? pr.out_scales + ((size_t)mt * n_tiles + nt) * kTileBytes + row_byte(r) : nullptr;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          if (nt * 128 + j * 32 >= pr.N) break;
-          uint32_t g[32], u[32];
-          tmem_ld32(t_row + j * 32, g);
-          tmem_ld32(t_row + 128 + j * 32, u);
-          tmem_ld_wait();
-          float h[32];
-          uint32_t a = 0;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            h[i] = swiglu(g[i], u[i]);
-            a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
-          }
-          const uint32_t b = scale_code(a);
-          const float f = inverse_scale(b);
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = encode8(h[8 * i] * f, h[8 * i + 1] * f, h[8 * i + 2] * f, h[8 * i + 3] * f, h[8 * i + 4] * f,
-                           h[8 * i + 5] * f, h[8 * i + 6] * f, h[8 * i + 7] * f);
-          sword |= b << (8 * j);
-          if (r < rows) *reinterpret_cast<uint4*>(hrow + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 2; ++i) {
+        const int j = a == 0 ? 3 - w - 2 * i : w + 2 * i;
+        uint32_t x0[32], x1[32];  // SwiGLU: gate and up values; else 64 columns
+        tmem_ld32(t_row + (GLU ? 32 * j : 64 * j), x0);
+        tmem_ld32(t_row + (GLU ? 128 + 32 * j : 64 * j + 32), x1);
+        tmem_ld_wait();
+        if (i == 0) {
+          fence_before();
+          mbar_arrive(&sh.tempty);
         }
-        if (r < rows)
-          *reinterpret_cast<uint32_t*>(pr.out_scales + ((size_t)mt * n_tiles + nt) * kTileBytes + row_byte(r)) = sword;
-      } else {
-        constexpr int COLS = 128 / (int)sizeof(OUT);  // columns of a 128-byte piece
-#pragma unroll 1
-        for (int c = 0; c < BN; c += COLS) {
-          const int col = nt * BN + c;
-          if (col >= pr.N) break;
-          uint32_t w[32];
-          if (sizeof(OUT) == 4) {
-            tmem_ld32(t_row + c, w);
-            tmem_ld_wait();
-          } else {
-            uint32_t y0[32], y1[32];
-            tmem_ld32(t_row + c, y0);
-            tmem_ld32(t_row + c + 32, y1);
-            tmem_ld_wait();
+        if (GLU) {
+          // a block past N is outside h: only its scale, 0, is kept
+          uint32_t b = 0;
+          if (nt * 128 + 32 * j < pr.N) {
+            uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(y0[2 * i]), __uint_as_float(y0[2 * i + 1]));
-              w[i] = *reinterpret_cast<uint32_t*>(&p);
-              p = __floats2bfloat162_rn(__uint_as_float(y1[2 * i]), __uint_as_float(y1[2 * i + 1]));
-              w[16 + i] = *reinterpret_cast<uint32_t*>(&p);
+            for (int i2 = 0; i2 < 32; ++i2) {
+              const float h = swiglu(x0[i2], x1[i2]);
+              x0[i2] = __float_as_uint(h);
+              m = max(m, x0[i2] & 0x7fffffffu);
+            }
+            b = scale_code(m);
+            const float f = inverse_scale(b);
+            uint32_t c[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              float h[8];
+#pragma unroll
+              for (int i2 = 0; i2 < 8; ++i2) h[i2] = __uint_as_float(x0[8 * v + i2]) * f;
+              c[v] = encode8(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7]);
+            }
+            if (r < rows) *reinterpret_cast<uint4*>(hrow + j * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+          }
+          if (r < rows) hs[j] = (uint8_t)b;
+        } else if (wrows > 0) {
+          constexpr int PIECE = 64 / (int)sizeof(OUT);  // columns of an emitted piece
+          uint32_t y[sizeof(OUT) == 4 ? 1 : 32];
+          if (sizeof(OUT) == 2) {
+#pragma unroll
+            for (int i2 = 0; i2 < 16; ++i2) {
+              __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(x0[2 * i2]), __uint_as_float(x0[2 * i2 + 1]));
+              y[i2] = *reinterpret_cast<uint32_t*>(&p);
+              p = __floats2bfloat162_rn(__uint_as_float(x1[2 * i2]), __uint_as_float(x1[2 * i2 + 1]));
+              y[16 + i2] = *reinterpret_cast<uint32_t*>(&p);
             }
           }
-          if (wrows > 0)
-            emit(stage, w, static_cast<unsigned char*>(pr.out) + ((size_t)(row0 + q * 32) * pr.N + col) * sizeof(OUT),
+#pragma unroll
+          for (int c = 0; c < 64; c += PIECE) {
+            const int col = nt * BN + 64 * j + c;
+            if (col >= pr.N) break;
+            const uint32_t* src = sizeof(OUT) == 2 ? y + c / 2 : (c < 32 ? x0 + c : x1 + c - 32);
+            emit(stage, src, static_cast<unsigned char*>(pr.out) + ((size_t)(row0 + q * 32) * pr.N + col) * sizeof(OUT),
                  (size_t)pr.N * sizeof(OUT), (pr.N - col) * (int)sizeof(OUT), wrows, lane);
+          }
         }
       }
-      fence_before();
-      mbar_arrive(&sh.tempty);
-      ++acc_it;
     }
   }
 
