@@ -169,6 +169,8 @@ def operands(rng, P, E, N, K, count, zero_fill=0):
 SHAPES = [  # counts per group, N, K
     ([1], 8, 32), ([5, 0, 3], 128, 256), ([127, 128, 129, 1], 264, 96), ([0, 0, 300], 520, 352),
     ([256, 257, 0, 40], 256, 1056), ([1, 0, 2, 0, 1, 700], 1000, 768),
+    # groups long enough on average for pairs of CTAs: one row, one past a row tile, one past a pair
+    ([600, 1, 129], 72, 32), ([1000], 264, 544), ([385, 257, 0, 513], 520, 352), ([2000, 128, 0, 0, 256], 128, 800),
 ]
 
 
@@ -225,7 +227,8 @@ def test_grouped_gemm_flags_bad_tables_and_skips_their_groups():
 
 @pytest.mark.parametrize("T,k_max,E,H,I,budgets", [(1, 1, 1, 32, 32, False), (1, 8, 128, 256, 96, False),
                                                    (200, 3, 7, 544, 352, True), (260, 4, 5, 1056, 160, False),
-                                                   (64, 6, 64, 256, 1408, True), (1500, 2, 4, 320, 256, False)])
+                                                   (64, 6, 64, 256, 1408, True), (1500, 2, 4, 320, 256, False),
+                                                   (900, 3, 3, 1056, 480, False)])
 def test_grouped_ffn_matches_oracle(T, k_max, E, H, I, budgets):
     rng = np.random.default_rng(T + H + I)
     order, back, off, count = routing(rng, T, k_max, E, budgets)

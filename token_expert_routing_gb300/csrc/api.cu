@@ -589,7 +589,10 @@ static int check_mx4_product(const char* fn, int P, int E, int N, int K, const v
   REQUIRE(P >= 0, "%s: P = %d < 0", fn, P);
   REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
   REQUIRE(N >= 8 && N % 8 == 0, "%s: N = %d is not a positive multiple of 8", fn, N);
+  // tile counts and the tensor maps' coordinates are 32-bit
   REQUIRE((long long)P / 128 + E < (1LL << 31) / ((N + 127) / 128), "%s: P * N too large", fn);
+  REQUIRE((long long)P / 128 + E < (1LL << 31) / ((K + 127) / 128), "%s: P * K too large", fn);
+  REQUIRE(2LL * E * ((N + 127) / 128) < (1LL << 31) / ((K + 127) / 128), "%s: E * N * K too large", fn);
   if (P == 0) return SEMMOE_OK;
   REQUIRE(a && a_scales && offsets && experts && b && b_scales && out, "%s: null pointer", fn);
   REQUIRE(aligned(a, 16) && aligned(a_scales, 16) && aligned(b, 16) && aligned(b_scales, 16) && aligned(out, 16),
@@ -625,6 +628,7 @@ int semmoe_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int3
   int rc = check_mx4_product(fn, P, E, H > I ? H : I, H, x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales,
                              y_perm);
   if (rc != SEMMOE_OK || P == 0) return rc;
+  REQUIRE((long long)P / 128 + E < (1LL << 31) / ((I + 127) / 128), "%s: P * I too large", fn);
   REQUIRE(w2 && w2_scales, "%s: null pointer", fn);
   REQUIRE(aligned(w2, 16) && aligned(w2_scales, 16), "%s: pointers must be 16-byte aligned", fn);
   REQUIRE(ws != nullptr && aligned(ws, 256) && ws_bytes >= mx4_ffn_ws_bytes(P, E, I),
