@@ -117,17 +117,15 @@ def _check(rc: int) -> None:
         raise SemMoEError(rc, lib().semmoe_last_error().decode())
 
 
-def _p(t) -> ctypes.c_void_p | None:
+def _p(t) -> int | None:
     """Device pointer of a contiguous CUDA tensor (None passes NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
+    if t is None or t.__class__ is int:
+        return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _want(t, dtype, numel, what):
@@ -136,9 +134,16 @@ def _want(t, dtype, numel, what):
         raise ValueError(f"{what}: expected at least {numel} elements of {dtype}, got {t.numel()} of {t.dtype}")
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+#: the current stream's handle without a Stream object (3 us of a call's host time on Grace), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def dtype_code(t: torch.Tensor) -> int:

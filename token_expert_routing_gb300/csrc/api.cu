@@ -235,9 +235,10 @@ int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_
               aligned(bias, 4) && aligned(pair_counts, 16),
           "%s: misaligned pointer", fn);
   CHECK_DEVICE(fn);
-  return cuda_status(launch_route_select(x, x_dtype, w_router, w_dtype, logits_in, logits_out, score, bias, n_group,
-                                         topk_group, group_top, renorm != 0, scale, k_per_token, k_uniform, T, H, E,
-                                         k_max, topk_idx, topk_w, pair_counts, ws, static_cast<cudaStream_t>(stream)),
+  return cuda_status(launch_route_select(x, x_dtype, w_router, w_dtype, logits_in, logits_out,
+                                         Select{score, bias, n_group, topk_group, group_top, renorm != 0, scale},
+                                         k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w, pair_counts, ws,
+                                         static_cast<cudaStream_t>(stream)),
                      fn);
 }
 

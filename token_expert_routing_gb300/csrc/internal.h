@@ -62,12 +62,24 @@ cudaError_t launch_route_hier(const void* x, int x_dtype, const void* w, int w_d
                               int T, int H, int Ep, int k_max, int32_t* topk_idx, float* topk_w,
                               int32_t* pair_counts, void* ws, cudaStream_t s);
 
-// Expert choice by score: sigmoid or softmax, a choice bias, groups.
+// Expert choice by score: sigmoid or softmax, a choice bias, groups (select.cuh).
+struct Select {
+  int score;                // SEMMOE_SCORE_*
+  const float* bias;        // [E] or NULL
+  int n_group, topk_group, group_top, renorm;
+  float scale;
+};
 cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w_dtype, const float* logits_in,
-                                float* logits_out, int score, const float* bias, int n_group, int topk_group,
-                                int group_top, int renorm, float scale, const int32_t* kpt, int k_uniform, int T,
+                                float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform, int T,
                                 int H, int E, int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts,
                                 void* ws, cudaStream_t s);
+// The product and the choice in one kernel, a cluster of CTAs per token tile
+// (route_tc.cu); route_select_cl_slices gives the slices of H (0: not applicable).
+int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype);
+cudaError_t launch_route_select_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int KS,
+                                   float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform,
+                                   int32_t* topk_idx, float* topk_w, int32_t* counts, int count_stride, void* split,
+                                   cudaStream_t s);
 
 cudaError_t launch_affinity_lookup(const int32_t* token_ids, const int32_t* lut, int V, int R,
                                    int T, int32_t* pred, cudaStream_t s);

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "select.cuh"
 
 namespace semmoe {
 namespace {
@@ -419,160 +420,26 @@ hier_topk_kernel(const float* __restrict__ logits, int ks, float* __restrict__ l
   }
 }
 
-// Expert choice by score (semmoe_route_select), one warp per token.  With the
-// logits l (summed over K slices) in registers, lane holding e = lane + 32 i:
-//   s_e = sigmoid(l_e), or the softmax of l;  c_e = s_e + bias_e  (fp32)
-// and experts are taken by c -- by l without a bias, which s never reorders and
-// which has no ties that rounding s would make.  Experts whose c is -inf are off.
-// Groups: `per_group` consecutive experts; L lanes share a group (L = 32 over
-// the next power of two of G, one lane per group and several groups per lane
-// past 32), each finds the two largest of its share of c and they are merged.
-// A group's rank is the number of groups with a larger score, or an equal one
-// and a lower index; ranks below topk_group stay.
-// Weights: s_j, or s_j over the sum of the picks' -- computed as exp(log s_j -
-// max log s) over its sum (log sigmoid(l) = min(l, 0) - log1p(exp(-|l|))), so that picks
-// whose scores all underflow still share one.
-struct Select {
-  int score;                // SEMMOE_SCORE_*
-  const float* bias;        // [E] or NULL
-  int n_group, topk_group, group_top, renorm;
-  float scale;
-};
-
-__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
-__device__ __forceinline__ float log_sigmoid_f32(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
-
-// (a, b) = the two largest of (a, b) and (c, d), each pair in descending order.
-__device__ __forceinline__ void merge_top2(float& a, float& b, float c, float d) {
-  const float lo = fminf(a, c);
-  a = fmaxf(a, c);
-  b = fmaxf(lo, fmaxf(b, d));
-}
-
+// Expert choice by score (select.cuh) of precomputed logits, the sum of ks
+// partial [T, E] slices: one warp per token.
 template <int NPER>  // experts per lane: E <= 32 * NPER
 __global__ void __launch_bounds__(kTopkWarps * 32)
 select_kernel(const float* __restrict__ logits, int ks, float* __restrict__ logits_out, Select sel,
               const int32_t* __restrict__ k_per_token, int k_uniform, int T, int E, int k_max,
               int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, PairCounts pc) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ unsigned long long sel_lists[kTopkWarps * sel_list_words(NPER)];
   pdl_trigger();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int G = sel.n_group;
-  float* base = reinterpret_cast<float*>(smem_raw) + warp * (2 * E + G + 2 * k_max);
-  float* lg = base;               // logits
-  float* ch = lg + E;             // choice scores
-  float* gs = ch + E;             // group scores
-  float* sel_v = gs + G;
-  int* sel_e = reinterpret_cast<int*>(sel_v + k_max);
+  const int warp = threadIdx.x / 32;
+  float* scratch = reinterpret_cast<float*>(smem_raw) + warp * select_scratch(E, sel.n_group, k_max);
   const int t = blockIdx.x * kTopkWarps + warp;
   if (t >= T) return;
   const int kt = warp_budget(k_per_token, k_uniform, k_max, t);
   float v[NPER];
   warp_load_logits<NPER>(logits + (size_t)t * E, ks, (size_t)T * E,
                          logits_out != nullptr ? logits_out + (size_t)t * E : nullptr, E, v);
-  const bool soft = sel.score == SEMMOE_SCORE_SOFTMAX;
-  const bool grouped = sel.topk_group < G;
-  float m = -INFINITY, z = 1.0f;  // the softmax's maximum and sum over all experts
-  if (soft) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) m = fmaxf(m, v[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.0f;  // no finite logit (flagged): nothing is taken
-    z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) z += expf(v[i] - m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  float c[NPER];  // what experts are taken by
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = v[i];
-    if (e < E) {
-      lg[e] = v[i];
-      if (sel.bias != nullptr || grouped) {
-        float s = v[i] == -INFINITY ? -INFINITY : soft ? expf(v[i] - m) / z : sigmoid_f32(v[i]);
-        if (sel.bias != nullptr) {
-          const float b = __ldg(sel.bias + e);
-          if (!(b < INFINITY)) flag(SEMMOE_DEVERR_NONFINITE);  // NaN or +inf: the expert is off
-          s = b < INFINITY ? s + b : -INFINITY;
-          c[i] = s;
-        }
-        ch[e] = s;
-      }
-    }
-  }
-  if (grouped) {
-    const int per_group = E / G;
-    int L = 1;  // lanes per group
-    if (G <= 32) {
-      int g2 = 1;
-      while (g2 < G) g2 <<= 1;
-      L = 32 / g2;
-    }
-    __syncwarp();
-    for (int g0 = 0; g0 < G; g0 += 32 / L) {
-      const int g = g0 + lane / L;
-      float a = -INFINITY, b = -INFINITY;
-      if (g < G)
-        for (int i = lane % L; i < per_group; i += L) merge_top2(a, b, ch[g * per_group + i], -INFINITY);
-      for (int o = L / 2; o > 0; o >>= 1) {
-        const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
-        merge_top2(a, b, a2, b2);
-      }
-      if (g < G && lane % L == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? a + b : a;
-    }
-    __syncwarp();
-    // experts of the groups that do not stay are off
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) {
-        const int g = e / per_group;
-        const float mine = gs[g];
-        int rank = 0;
-        for (int o = 0; o < G; ++o) rank += gs[o] > mine || (gs[o] == mine && o < g);
-        if (rank >= sel.topk_group) c[i] = -INFINITY;
-      }
-    }
-  }
-  warp_select<NPER>(c, E, kt, sel_v, sel_e, sel_lists + warp * sel_list_words(NPER));
-  // weights; a pick whose choice score is -inf is none
-  float top = -INFINITY;
-  if (sel.renorm) {
-    for (int j = lane; j < kt; j += 32)
-      if (sel_e[j] >= 0 && sel_v[j] > -INFINITY) {
-        const float l = lg[sel_e[j]];
-        top = fmaxf(top, soft ? l : log_sigmoid_f32(l));
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  float den = 0.0f;
-  for (int j = lane; j < kt; j += 32) {
-    if (sel_e[j] < 0 || sel_v[j] == -INFINITY) continue;
-    const float l = lg[sel_e[j]];
-    if (sel.renorm) den += expf((soft ? l : log_sigmoid_f32(l)) - top);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  for (int j = lane; j < k_max; j += 32) {
-    int e = -1;
-    float w = 0.0f;
-    if (j < kt && sel_e[j] >= 0 && sel_v[j] > -INFINITY) {
-      e = sel_e[j];
-      const float l = lg[e];
-      if (sel.renorm) w = expf((soft ? l : log_sigmoid_f32(l)) - top) / den;
-      else w = soft ? expf(l - m) / z : sigmoid_f32(l);
-      w *= sel.scale;
-      count_pick(pc, e, t);
-    }
-    topk_idx[(size_t)t * k_max + j] = e;
-    topk_w[(size_t)t * k_max + j] = w;
-  }
+  const int bad = warp_choose<NPER>(v, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max,
+                                    topk_w + (size_t)t * k_max, [&](int e) { count_pick(pc, e, t); });
+  if (bad) flag(bad);
 }
 
 __global__ void affinity_lookup_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ lut,
@@ -829,19 +696,25 @@ cudaError_t launch_route_hier(const void* x, int x_dtype, const void* w, int w_d
 }
 
 cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w_dtype, const float* logits_in,
-                                float* logits_out, int score, const float* bias, int n_group, int topk_group,
-                                int group_top, int renorm, float scale, const int32_t* kpt, int k_uniform, int T,
+                                float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform, int T,
                                 int H, int E, int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts,
                                 void* ws, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
+  cudaError_t e;
+  if (logits_in == nullptr && route_on_tensor_cores(x_dtype, H)) {  // product and choice in one kernel
+    const int ks = route_select_cl_slices(T, H, E, k_max, w_dtype);
+    if (ks >= 1)
+      return launch_route_select_cl(x, w, w_dtype, T, H, E, k_max, ks, logits_out, sel, kpt, k_uniform, topk_idx,
+                                    topk_w, pair_counts, pair_counts != nullptr ? pair_counts_stride(T) : 0,
+                                    static_cast<unsigned char*>(ws) + route_partials_bytes(T, H, E, w_dtype), s);
+  }
   int ks = 1;
-  cudaError_t e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s);
+  e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s);
   if (e != cudaSuccess) return e;
   PairCounts pc;
   e = pair_counts_begin(pair_counts, T, E, &pc, s);
   if (e != cudaSuccess) return e;
-  const Select sel{score, bias, n_group, topk_group, group_top, renorm, scale};
-  const size_t sm = (size_t)kTopkWarps * (2 * E + n_group + 2 * k_max) * sizeof(float);
+  const size_t sm = (size_t)kTopkWarps * select_scratch(E, sel.n_group, k_max) * sizeof(float);
   const dim3 grid((T + kTopkWarps - 1) / kTopkWarps), block(kTopkWarps * 32);
   auto run = [&](auto kern) {
     kern<<<grid, block, sm, s>>>(logits_in, ks, logits_out, sel, kpt, k_uniform, T, E, k_max, topk_idx, topk_w, pc);
@@ -849,13 +722,7 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
   if (E <= 32) run(select_kernel<1>);
   else if (E <= 64) run(select_kernel<2>);
   else if (E <= 128) run(select_kernel<4>);
-  else {
-    // E = n_group = k_max = 256 needs 40 KB beside 16 KB of static selection lists
-    static std::atomic<unsigned long long> smem_set{0};
-    e = ensure_smem_limit(select_kernel<8>, kTopkWarps * 5 * kRouteMaxE * (int)sizeof(float), smem_set);
-    if (e != cudaSuccess) return e;
-    run(select_kernel<8>);
-  }
+  else run(select_kernel<8>);  // at most 40 KB of scratch (E = n_group = k_max = 256)
   count_launches(1);
   return cudaGetLastError();
 }

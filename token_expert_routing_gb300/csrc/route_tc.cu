@@ -19,6 +19,7 @@
 // the grouped-FFN kernel.
 #include "common.cuh"
 #include "internal.h"
+#include "select.cuh"
 #include "tc_common.cuh"
 
 namespace semmoe {
@@ -472,13 +473,13 @@ route_topk_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 // ---------------------------------------------------------------------------
 constexpr int kClThreads = 64 + 4 * 128;  // producer, MMA, 16 epilogue / selection warps
 
-template <int S, int NPER>  // NPER experts per lane in the selection: E <= 32 * NPER
+template <int S, int NPER, bool SEL = false>  // NPER experts per lane in the selection: E <= 32 * NPER; SEL: choice by score
 __global__ void __launch_bounds__(kClThreads, 1)
 route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, int T,
                      int H, int E, int EC, int KS, int CS, int stages, int kb_slice, float* __restrict__ logits_out,
                      const int32_t* __restrict__ k_per_token, int k_uniform, int k_max,
                      int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, int32_t* __restrict__ counts,
-                     int count_stride) {
+                     int count_stride, const Select sel) {
   pdl_trigger();  // the kernel after it may start its setup
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -631,6 +632,28 @@ route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                                           : recv + ((size_t)qc * rpc + (row - rank * rpc)) * pstride;
             l[i] = sk == 0 ? src[c] : l[i] + src[c];
           }
+      }
+      if constexpr (SEL) {  // choice by score (select.cuh), scratch past the received rows
+        if (t >= T) continue;
+        int bits = 0;
+        if (kt < 1 || kt > k_max) {
+          bits = SEMMOE_DEVERR_K;
+          kt = kt < 1 ? 1 : k_max;
+        }
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) {
+          const int e = lane + 32 * i;
+          if (e < E) {
+            if (logits_out != nullptr) logits_out[(size_t)t * E + e] = l[i];
+            if (!isfinite(l[i])) bits |= SEMMOE_DEVERR_NONFINITE;
+          }
+          if (e >= E || !isfinite(l[i])) l[i] = -INFINITY;
+        }
+        float* scratch = recv + (size_t)(CS > 1 ? BM : 0) * pstride + (warp - 2) * select_scratch(E, sel.n_group, k_max);
+        bits |= warp_choose<NPER>(l, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max,
+                                  topk_w + (size_t)t * k_max, [&](int e) { atomicAdd(&hist[e], 1); });
+        if (bits) atomicOr(&g_err, bits);
+        continue;
       }
       bool nonfinite = false;
       uint32_t key[NPER];
@@ -922,12 +945,14 @@ int route_topk_cl_slices(int T, int H, int E, int k_max, int w_dtype) {
   return ks;
 }
 
-cudaError_t launch_route_topk_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int KS,
-                                 float* logits_out, const int32_t* kpt, int k_uniform, int32_t* topk_idx,
-                                 float* topk_w, int32_t* counts, int count_stride, void* split, cudaStream_t s) {
+// Launches the cluster router on passes of EC experts; sel: choice by score, or NULL for the plain top-k.
+static cudaError_t launch_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int EC, int KS,
+                             float* logits_out, const Select* sel, const int32_t* kpt, int k_uniform,
+                             int32_t* topk_idx, float* topk_w, int32_t* counts, int count_stride, void* split,
+                             cudaStream_t s) {
   const int S = w_dtype == SEMMOE_BF16 ? 1 : 3;
   const int E16 = (E + 15) / 16 * 16;
-  const int EC = experts_per_pass(E, S), n_pass = (E + EC - 1) / EC, CS = n_pass * KS;
+  const int n_pass = (E + EC - 1) / EC, CS = n_pass * KS;
   const void* wb = w;
   int w_rows = E;
   if (S == 3) {
@@ -952,20 +977,24 @@ cudaError_t launch_route_topk_cl(const void* x, const void* w, int w_dtype, int 
     if (!make_map_bf16(&mw, wb, 2, dims, str, box)) return cudaErrorInvalidValue;
   }
   const int kb_all = (H + BK - 1) / BK, kb_slice = (kb_all + KS - 1) / KS;
-  if (CS < 2 || CS > 8 || (KS - 1) * kb_slice >= kb_all) return cudaErrorInvalidValue;  // every slice holds k-blocks
+  if (CS < 1 || CS > 8 || (KS - 1) * kb_slice >= kb_all) return cudaErrorInvalidValue;  // every slice holds k-blocks
   const size_t stage_bytes = A_BYTES + (size_t)S * EC * BK * 2;
   int stages = (int)(stage_budget(1) / stage_bytes);
   if (stages > MAX_STAGES) stages = MAX_STAGES;
   using K = void (*)(CUtensorMap, CUtensorMap, int, int, int, int, int, int, int, int, float*, const int32_t*, int,
-                     int, int32_t*, float*, int32_t*, int);
+                     int, int32_t*, float*, int32_t*, int, Select);
   // experts per lane in the selection (E <= 32 NPER)
   const int np = E16 <= 32 ? 1 : (E16 <= 64 ? 2 : (E16 <= 128 ? 4 : 8));
-  const int ki = (S == 1 ? 0 : 4) + (np == 1 ? 0 : (np == 2 ? 1 : (np == 4 ? 2 : 3)));
-  static const K kerns[8] = {route_topk_cl_kernel<1, 1>, route_topk_cl_kernel<1, 2>, route_topk_cl_kernel<1, 4>,
-                             route_topk_cl_kernel<1, 8>, route_topk_cl_kernel<3, 1>, route_topk_cl_kernel<3, 2>,
-                             route_topk_cl_kernel<3, 4>, route_topk_cl_kernel<3, 8>};
+  const int ki = (sel != nullptr ? 8 : 0) + (S == 1 ? 0 : 4) + (np == 1 ? 0 : (np == 2 ? 1 : (np == 4 ? 2 : 3)));
+  static const K kerns[16] = {
+      route_topk_cl_kernel<1, 1>,       route_topk_cl_kernel<1, 2>,       route_topk_cl_kernel<1, 4>,
+      route_topk_cl_kernel<1, 8>,       route_topk_cl_kernel<3, 1>,       route_topk_cl_kernel<3, 2>,
+      route_topk_cl_kernel<3, 4>,       route_topk_cl_kernel<3, 8>,       route_topk_cl_kernel<1, 1, true>,
+      route_topk_cl_kernel<1, 2, true>, route_topk_cl_kernel<1, 4, true>, route_topk_cl_kernel<1, 8, true>,
+      route_topk_cl_kernel<3, 1, true>, route_topk_cl_kernel<3, 2, true>, route_topk_cl_kernel<3, 4, true>,
+      route_topk_cl_kernel<3, 8, true>};
   const K kern = kerns[ki];
-  static std::atomic<unsigned long long> smem_set[8];
+  static std::atomic<unsigned long long> smem_set[16];
   cudaError_t e = ensure_smem_limit(kern, (int)smem_bytes(1), smem_set[ki]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -981,10 +1010,50 @@ cudaError_t launch_route_topk_cl(const void* x, const void* w, int w_dtype, int 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, mx, mw, T, H, E, EC, KS, CS, stages, kb_slice, logits_out, kpt, k_uniform,
-                         k_max, topk_idx, topk_w, counts, count_stride);
+                         k_max, topk_idx, topk_w, counts, count_stride, sel != nullptr ? *sel : Select{});
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
+}
+
+cudaError_t launch_route_topk_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int KS,
+                                 float* logits_out, const int32_t* kpt, int k_uniform, int32_t* topk_idx,
+                                 float* topk_w, int32_t* counts, int count_stride, void* split, cudaStream_t s) {
+  return launch_cl(x, w, w_dtype, T, H, E, k_max, experts_per_pass(E, w_dtype == SEMMOE_BF16 ? 1 : 3), KS, logits_out,
+                   nullptr, kpt, k_uniform, topk_idx, topk_w, counts, count_stride, split, s);
+}
+
+// The choice by score in the cluster router: passes of at most 128 experts (bf16
+// weight; 64 for an fp32 one, as its split has them), so that the partial and
+// received logits leave room for the selection's scratch in the operand ring.
+static int select_pass(int E, int w_dtype) {
+  const int e16 = (E + 15) / 16 * 16, cap = w_dtype == SEMMOE_BF16 ? 128 : 64;
+  return e16 < cap ? e16 : cap;
+}
+
+// Slices of H for the choice by score, 0 where the split-K product and a
+// selection kernel take the call: the largest KS in {1, 2, 4, 8} with one CTA per SM for
+// every (tile, pass, slice), at most 8 CTAs per cluster and at least 2 k-blocks per slice.
+int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype) {
+  const int EC = select_pass(E, w_dtype), n_pass = (E + EC - 1) / EC;
+  const long long tiles = (T + BM - 1) / BM;
+  const int kb_all = (H + BK - 1) / BK;
+  const size_t words = 2 * (size_t)BM * (EC + 4) + (size_t)(kClThreads / 32 - 2) * select_scratch(E, E, k_max);
+  if (words * 4 > stage_budget(1)) return 0;
+  int ks = 0;
+  for (int c = 1; c <= 8; c *= 2)
+    if (c * n_pass <= 8 && BM % (c * n_pass) == 0 && tiles * c * n_pass <= sm_count() && (c == 1 || kb_all >= 2 * c) &&
+        (c - 1) * ((kb_all + c - 1) / c) < kb_all)  // every slice holds k-blocks
+      ks = c;
+  return ks;
+}
+
+cudaError_t launch_route_select_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int KS,
+                                   float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform,
+                                   int32_t* topk_idx, float* topk_w, int32_t* counts, int count_stride, void* split,
+                                   cudaStream_t s) {
+  return launch_cl(x, w, w_dtype, T, H, E, k_max, select_pass(E, w_dtype), KS, logits_out, &sel, kpt, k_uniform,
+                   topk_idx, topk_w, counts, count_stride, split, s);
 }
 
 }  // namespace semmoe

@@ -1,0 +1,186 @@
+// Expert choice by score (semmoe_route_select) of one token by one warp, lane l
+// holding the experts l + 32 i.
+//   s_e = sigmoid(l_e), or the softmax of l;  c_e = s_e + bias_e  (fp32)
+// and experts are taken by c -- by l without a bias, which s never reorders and
+// which has no ties that rounding s would make.  Experts whose c is -inf are off.
+// Groups: `per_group` consecutive experts; L lanes share a group (L = 32 over
+// the next power of two of G, one lane per group and several groups per lane
+// past 32), each finds the two largest of its share of c and they are merged.
+// A group's rank is the number of groups with a larger score, or an equal one
+// and a lower index; ranks below topk_group stay.
+// Picks: k_t rounds of a warp maximum over order-preserving keys (key 0: not to
+// be taken), ties to the lowest index holding it.
+// Weights: s_j, or s_j over the sum of the picks' -- computed as exp(log s_j -
+// max log s) over its sum (log sigmoid(l) = min(l, 0) - log1p(exp(-|l|))), so that
+// picks whose scores all underflow still share one.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace semmoe {
+
+// Words of scratch per warp: logits, choice scores, group scores, picks.
+__host__ __device__ constexpr int select_scratch(int E, int G, int k_max) { return 2 * E + G + k_max; }
+
+__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float log_sigmoid_f32(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
+
+// (a, b) = the two largest of (a, b) and (c, d), each pair in descending order.
+__device__ __forceinline__ void merge_top2(float& a, float& b, float c, float d) {
+  const float lo = fminf(a, c);
+  a = fmaxf(a, c);
+  b = fmaxf(lo, fmaxf(b, d));
+}
+
+// v: the token's logits, -inf where not finite and past E.  idx / w: its k_max output
+// slots; picked(e) is called once for each expert taken.  Returns this lane's device
+// error bits.  Every lane of the warp calls.
+template <int NPER, typename F>
+__device__ __forceinline__ int warp_choose(const float (&v)[NPER], int E, int kt, int k_max, const Select& sel,
+                                           float* scratch, int32_t* __restrict__ idx, float* __restrict__ w,
+                                           F&& picked) {
+  const int lane = threadIdx.x & 31;
+  const int G = sel.n_group;
+  const bool soft = sel.score == SEMMOE_SCORE_SOFTMAX, grouped = sel.topk_group < G;
+  float* lg = scratch;
+  float* ch = lg + E;
+  float* gs = ch + E;
+  int* pick = reinterpret_cast<int*>(gs + G);
+  int bad = 0;
+  float m = -INFINITY, z = 1.0f;  // the softmax's maximum and sum over all experts
+  if (soft) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) m = fmaxf(m, v[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;  // no finite logit (flagged): nothing is taken
+    z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) z += expf(v[i] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  float c[NPER];  // what experts are taken by
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const int e = lane + 32 * i;
+    c[i] = v[i];
+    if (e < E) {
+      lg[e] = v[i];
+      if (sel.bias != nullptr || grouped) {
+        float s = v[i] == -INFINITY ? -INFINITY : soft ? expf(v[i] - m) / z : sigmoid_f32(v[i]);
+        if (sel.bias != nullptr) {
+          const float b = __ldg(sel.bias + e);
+          if (!(b < INFINITY)) bad |= SEMMOE_DEVERR_NONFINITE;  // NaN or +inf: the expert is off
+          s = b < INFINITY ? s + b : -INFINITY;
+          c[i] = s;
+        }
+        if (grouped) ch[e] = s;
+      }
+    }
+  }
+  if (grouped) {
+    const int per_group = E / G;
+    int L = 1;  // lanes per group
+    if (G <= 32) L = 32 >> (32 - __clz(G - 1));
+    __syncwarp();
+    for (int g0 = 0; g0 < G; g0 += 32 / L) {
+      const int g = g0 + lane / L;
+      float a = -INFINITY, b = -INFINITY;
+      if (g < G)
+        for (int i = lane % L; i < per_group; i += L) merge_top2(a, b, ch[g * per_group + i], -INFINITY);
+      for (int o = L / 2; o > 0; o >>= 1) {
+        const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+        merge_top2(a, b, a2, b2);
+      }
+      if (g < G && lane % L == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? a + b : a;
+    }
+    __syncwarp();
+    if (G <= 32) {  // lane g ranks group g
+      const float mine = lane < G ? gs[lane] : 0.0f;
+      int rank = 0;
+      for (int o = 0; o < G; ++o) {
+        const float other = __shfl_sync(0xffffffffu, mine, o);
+        rank += other > mine || (other == mine && o < lane);
+      }
+      const unsigned keep = __ballot_sync(0xffffffffu, lane < G && rank < sel.topk_group);
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E && !((keep >> (e / per_group)) & 1u)) c[i] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E) {
+          const int g = e / per_group;
+          const float mine = gs[g];
+          int rank = 0;
+          for (int o = 0; o < G; ++o) rank += gs[o] > mine || (gs[o] == mine && o < g);
+          if (rank >= sel.topk_group) c[i] = -INFINITY;
+        }
+      }
+    }
+  }
+  uint32_t key[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const uint32_t b = __float_as_uint(__fadd_rn(c[i], 0.0f));  // -0.0 -> +0.0
+    key[i] = c[i] == -INFINITY ? 0u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  }
+  int taken = 0;
+  for (; taken < kt; ++taken) {
+    uint32_t mk = key[0];
+#pragma unroll
+    for (int i = 1; i < NPER; ++i) mk = max(mk, key[i]);
+    mk = __reduce_max_sync(0xffffffffu, mk);
+    if (mk == 0u) break;  // none left to take
+    uint32_t first = 0xffffffffu;  // this lane's lowest index with that key
+#pragma unroll
+    for (int i = NPER - 1; i >= 0; --i)
+      if (key[i] == mk) first = (uint32_t)(lane + 32 * i);
+    const int e = (int)__reduce_min_sync(0xffffffffu, first);
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      if (e == lane + 32 * i) key[i] = 0u;
+    if (lane == (taken & 31)) pick[taken] = e;
+  }
+  __syncwarp();
+  float top = -INFINITY, den = 0.0f;
+  if (sel.renorm) {
+    for (int j = lane; j < taken; j += 32) {
+      const float l = lg[pick[j]];
+      top = fmaxf(top, soft ? l : log_sigmoid_f32(l));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int j = lane; j < taken; j += 32) {
+      const float l = lg[pick[j]];
+      den += expf((soft ? l : log_sigmoid_f32(l)) - top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  }
+  for (int j = lane; j < k_max; j += 32) {
+    int e = -1;
+    float g = 0.0f;
+    if (j < taken) {
+      e = pick[j];
+      const float l = lg[e];
+      if (sel.renorm) g = expf((soft ? l : log_sigmoid_f32(l)) - top) / den;
+      else g = soft ? expf(l - m) / z : sigmoid_f32(l);
+      g *= sel.scale;
+      picked(e);
+    }
+    idx[j] = e;
+    w[j] = g;
+  }
+  __syncwarp();  // the scratch may be written again
+  return bad;
+}
+
+}  // namespace semmoe
