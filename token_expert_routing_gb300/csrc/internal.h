@@ -33,7 +33,7 @@ size_t route_split_size(int H, int E);
 cudaError_t launch_route_split(const float* w, int H, int E, void* split, cudaStream_t s);
 int route_tc_k_slices(int T, int H, int E, int w_dtype);
 cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, float* partials,
-                                   int ks, void* split, cudaStream_t s);
+                                   int ks, void* split, cudaStream_t s, bool rotate = false);
 // The router GEMM and the top-k in one tensor-core kernel (route_tc.cu), for
 // routers whose experts fit one MMA (route_topk_tc_ok); writes the count table
 // (counts, row stride count_stride) in full when counts is not null.

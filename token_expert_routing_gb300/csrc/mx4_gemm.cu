@@ -115,17 +115,6 @@ __device__ __forceinline__ RowTile decode_mtile(const Shared& sh, int& g, int mt
   return RowTile{row0, left < BM ? left : BM, sh.pe[g]};
 }
 
-// One lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // mbar_wait (same bounds), polling a few times before it looks at the clock, whose
 // reading takes longer than most of the waits here.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {

@@ -433,13 +433,15 @@ select_kernel(const float* __restrict__ logits, int ks, float* __restrict__ logi
   float* scratch = reinterpret_cast<float*>(smem_raw) + warp * select_scratch(E, sel.n_group, k_max);
   const int t = blockIdx.x * kTopkWarps + warp;
   if (t >= T) return;
+  pdl_wait();
   const int kt = warp_budget(k_per_token, k_uniform, k_max, t);
-  float v[NPER];
+  float bias[NPER], v[NPER];
+  const int bits = load_bias<NPER>(sel, E, bias);
+  if (bits) flag(bits);
   warp_load_logits<NPER>(logits + (size_t)t * E, ks, (size_t)T * E,
                          logits_out != nullptr ? logits_out + (size_t)t * E : nullptr, E, v);
-  const int bad = warp_choose<NPER>(v, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max,
-                                    topk_w + (size_t)t * k_max, [&](int e) { count_pick(pc, e, t); });
-  if (bad) flag(bad);
+  warp_choose<NPER>(v, bias, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max, topk_w + (size_t)t * k_max,
+                    [&](int e) { count_pick(pc, e, t); });
 }
 
 __global__ void affinity_lookup_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ lut,
@@ -550,12 +552,12 @@ size_t route_ws_bytes(int T, int H, int E, int x_dtype, int w_dtype) {
 // Tensor-core logits into the workspace: fp32 partial sums over *ks K slices,
 // laid out [ks][T][E].
 static cudaError_t route_partials_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, void* ws,
-                                     const float** partials, int* ks, cudaStream_t s) {
+                                     const float** partials, int* ks, cudaStream_t s, bool rotate = false) {
   unsigned char* w8 = static_cast<unsigned char*>(ws);
   float* p = reinterpret_cast<float*>(w8);
   void* split = w8 + route_partials_bytes(T, H, E, w_dtype);
   int k = route_tc_k_slices(T, H, E, w_dtype);
-  cudaError_t e = launch_route_logits_tc(x, w, w_dtype, T, H, E, p, k, split, s);
+  cudaError_t e = launch_route_logits_tc(x, w, w_dtype, T, H, E, p, k, split, s, rotate);
   if (e != cudaSuccess) return e;
   const int kb_all = (H + 63) / 64, per = (kb_all + k - 1) / k;
   *ks = (kb_all + per - 1) / per;  // the slices the launcher actually used
@@ -643,13 +645,14 @@ size_t route_hier_ws_bytes(int T, int H, int Ep, int x_dtype, int w_dtype) {
 // Logits for a selection kernel of their own: *logits_in stays when given (and a
 // copy onto itself is dropped), else they go to the workspace as *ks partial sums.
 static cudaError_t route_logits(const void* x, int x_dtype, const void* w, int w_dtype, int T, int H, int E, void* ws,
-                                const float** logits_in, float** logits_out, int* ks, cudaStream_t s) {
+                                const float** logits_in, float** logits_out, int* ks, cudaStream_t s,
+                                bool rotate = false) {
   *ks = 1;
   if (*logits_in != nullptr) {
     if (*logits_out == *logits_in) *logits_out = nullptr;
     return cudaSuccess;
   }
-  if (route_on_tensor_cores(x_dtype, H)) return route_partials_tc(x, w, w_dtype, T, H, E, ws, logits_in, ks, s);
+  if (route_on_tensor_cores(x_dtype, H)) return route_partials_tc(x, w, w_dtype, T, H, E, ws, logits_in, ks, s, rotate);
   unsigned char* w8 = static_cast<unsigned char*>(ws);
   float* lg = reinterpret_cast<float*>(w8);
   unsigned char* rest = w8 + align_up((size_t)T * E * sizeof(float), 256);
@@ -709,7 +712,7 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
                                     static_cast<unsigned char*>(ws) + route_partials_bytes(T, H, E, w_dtype), s);
   }
   int ks = 1;
-  e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s);
+  e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s, true);
   if (e != cudaSuccess) return e;
   PairCounts pc;
   e = pair_counts_begin(pair_counts, T, E, &pc, s);
@@ -717,14 +720,13 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
   const size_t sm = (size_t)kTopkWarps * select_scratch(E, sel.n_group, k_max) * sizeof(float);
   const dim3 grid((T + kTopkWarps - 1) / kTopkWarps), block(kTopkWarps * 32);
   auto run = [&](auto kern) {
-    kern<<<grid, block, sm, s>>>(logits_in, ks, logits_out, sel, kpt, k_uniform, T, E, k_max, topk_idx, topk_w, pc);
+    return launch_kernel(kern, grid, block, sm, s, 1, true, logits_in, ks, logits_out, sel, kpt, k_uniform, T, E, k_max,
+                         topk_idx, topk_w, pc);
   };
-  if (E <= 32) run(select_kernel<1>);
-  else if (E <= 64) run(select_kernel<2>);
-  else if (E <= 128) run(select_kernel<4>);
-  else run(select_kernel<8>);  // at most 40 KB of scratch (E = n_group = k_max = 256)
+  // at most 32 KB of scratch (E = n_group = k_max = 256)
+  e = E <= 32 ? run(select_kernel<1>) : E <= 64 ? run(select_kernel<2>) : E <= 128 ? run(select_kernel<4>) : run(select_kernel<8>);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_affinity_lookup(const int32_t* ids, const int32_t* lut, int V, int R, int T, int32_t* pred,

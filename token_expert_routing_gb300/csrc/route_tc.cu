@@ -79,7 +79,7 @@ __global__ void split_router_kernel(const float* __restrict__ w, int E, int H, i
 template <int S, int CPS>  // CPS: resident CTAs per SM the ring is sized for
 __global__ void __launch_bounds__(THREADS, CPS)
 route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, int T, int H,
-                int E, int EC, int stages, int kb_per_slice, float* __restrict__ partials) {
+                int E, int EC, int stages, int kb_per_slice, int rotate, float* __restrict__ partials) {
   pdl_trigger();  // the kernel after it may start its setup
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -87,7 +87,7 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
   Shared& sh = *reinterpret_cast<Shared*>(ring + stage_budget(CPS));
   volatile int* abort_flag = &sh.abort_flag;
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int NB = S * EC;
   const uint32_t b_bytes = (uint32_t)NB * BK * 2;
   const uint32_t stage_bytes = A_BYTES + b_bytes;  // a multiple of 1024 (NB % 16 == 0)
@@ -96,6 +96,8 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
   const int kb0 = slice * kb_per_slice;
   const int kb_n = kb_all - kb0 < kb_per_slice ? kb_all - kb0 : kb_per_slice;  // >= 1 by construction
   float* logits = partials + (size_t)slice * T * E;  // this K slice's partial sums
+  // rotate: tiles start at different k-blocks, so that they do not all read the same weight lines at once
+  const int kb_first = rotate ? (int)(blockIdx.x % (unsigned)kb_n) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -115,42 +117,48 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
   fence_after();
   const uint32_t tmem = sh.tmem_base;
 
-  if (warp == 0) {
-    if (lane == 0) {  // TMA producer
-      int it = 0;
-      for (int kb = 0; kb < kb_n; ++kb) {
-        const int s = kb % stages;
-        const uint32_t ph = (kb / stages) & 1;
-        if (!mbar_wait(&sh.empty[s], ph ^ 1, abort_flag, &g_err)) break;
+  if (warp == 0) {  // TMA producer
+    int it = 0;
+    for (int i = 0; i < kb_n; ++i) {
+      const int kb = kb_first + i < kb_n ? kb_first + i : kb_first + i - kb_n;
+      const int s = i % stages;
+      const uint32_t ph = (i / stages) & 1;
+      if (!mbar_wait(&sh.empty[s], ph ^ 1, abort_flag, &g_err)) break;
+      if (elect_one()) {
         unsigned char* st = ring + (size_t)s * stage_bytes;
         mbar_expect_tx(&sh.full[s], stage_bytes);
         tma_load_2d(st, &map_x, &sh.full[s], (kb0 + kb) * BK, t0);
         tma_load_2d(st + A_BYTES, &map_w, &sh.full[s], (kb0 + kb) * BK, pass * NB);
-        ++it;
       }
-      if (*abort_flag)
-        for (int j = it > stages ? it - stages : 0; j < it; ++j)
-          mbar_drain(&sh.full[j % stages], (j / stages) & 1, &g_err);
+      __syncwarp();
+      ++it;
     }
-  } else if (warp == 1) {
-    if (lane == 0) {  // MMA issuer
-      const uint32_t idesc = idesc_bf16_f32(BM, NB);
-      bool ok = true;
-      for (int kb = 0; kb < kb_n; ++kb) {
-        const int s = kb % stages;
-        const uint32_t ph = (kb / stages) & 1;
-        if (!mbar_wait(&sh.full[s], ph, abort_flag, &g_err)) { ok = false; break; }
-        fence_after();
-        const uint32_t sa = smem_u32(ring + (size_t)s * stage_bytes), sb = sa + A_BYTES;
+    if (*abort_flag && lane == 0)
+      for (int j = it > stages ? it - stages : 0; j < it; ++j)
+        mbar_drain(&sh.full[j % stages], (j / stages) & 1, &g_err);
+  } else if (warp == 1) {  // MMA issuer
+    const uint32_t idesc = idesc_bf16_f32(BM, NB), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    for (int kb = 0; kb < kb_n; ++kb) {
+      const int s = kb % stages;
+      const uint32_t ph = (kb / stages) & 1;
+      if (!mbar_wait(&sh.full[s], ph, abort_flag, &g_err)) { ok = false; break; }
+      fence_after();
+      const uint32_t sa = smem_u32(ring) + (uint32_t)s * stage_bytes, sb = sa + A_BYTES;
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < BK / UK; ++k)
-          mma_bf16(tmem, sw128_desc(sa + k * UK * 2), sw128_desc(sb + k * UK * 2), idesc, (kb | k) != 0);
+          mma_bf16(tm, sw128_desc(sa + k * UK * 2), sw128_desc(sb + k * UK * 2), idesc, (kb | k) != 0);
         commit(&sh.empty[s]);
       }
+      __syncwarp();
+    }
+    if (elect_one()) {
       if (ok) commit(&sh.tfull);
       commit(&sh.done);
-      mbar_drain(&sh.done, 0, &g_err);
     }
+    __syncwarp();
+    if (lane == 0) mbar_drain(&sh.done, 0, &g_err);
   } else {  // epilogue: thread = one token row of the accumulator
     const int q = warp & 3;
     int ok = 1;
@@ -614,6 +622,11 @@ route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
   // slices in slice order; k_t rounds of a warp argmax (the largest key, then
   // the lowest expert holding it, which is taken out)
   if (warp >= 2) {
+    float bias[NPER];
+    if constexpr (SEL) {
+      const int bits = load_bias<NPER>(sel, E, bias);
+      if (bits) atomicOr(&g_err, bits);
+    }
     const bool got = mbar_wait(&recv_bar, 0, abort_flag, &g_err);  // every lane: acquire the copies
     for (int row = rank * rpc + (warp - 2); got && row < (rank + 1) * rpc; row += kClThreads / 32 - 2) {
       const int t = t0 + row;
@@ -650,8 +663,8 @@ route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
           if (e >= E || !isfinite(l[i])) l[i] = -INFINITY;
         }
         float* scratch = recv + (size_t)(CS > 1 ? BM : 0) * pstride + (warp - 2) * select_scratch(E, sel.n_group, k_max);
-        bits |= warp_choose<NPER>(l, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max,
-                                  topk_w + (size_t)t * k_max, [&](int e) { atomicAdd(&hist[e], 1); });
+        warp_choose<NPER>(l, bias, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max,
+                          topk_w + (size_t)t * k_max, [&](int e) { atomicAdd(&hist[e], 1); });
         if (bits) atomicOr(&g_err, bits);
         continue;
       }
@@ -808,12 +821,12 @@ cudaError_t launch_route_split(const float* w, int H, int E, void* split, cudaSt
 
 template <int S, int CPS>
 static cudaError_t launch_k(dim3 grid, const CUtensorMap& mx, const CUtensorMap& mw, int T, int H, int E, int EC,
-                            int stages, int kb_per_slice, float* partials, cudaStream_t s) {
+                            int stages, int kb_per_slice, int rotate, float* partials, cudaStream_t s) {
   static std::atomic<unsigned long long> smem_set{0};
   cudaError_t e = ensure_smem_limit(route_tc_kernel<S, CPS>, (int)smem_bytes(CPS), smem_set);
   if (e != cudaSuccess) return e;
   route_tc_kernel<S, CPS><<<grid, THREADS, smem_bytes(CPS), s>>>(mx, mw, T, H, E, EC, stages, kb_per_slice,
-                                                                 partials);
+                                                                 rotate, partials);
   return cudaSuccess;
 }
 
@@ -822,7 +835,7 @@ static cudaError_t launch_k(dim3 grid, const CUtensorMap& mx, const CUtensorMap&
 // route_tc_k_slices(); the logits are their sum in slice order); split:
 // workspace of route_tc_split_bytes() (fp32 weight only).
 cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, float* partials,
-                                   int ks, void* split, cudaStream_t s) {
+                                   int ks, void* split, cudaStream_t s, bool rotate) {
   const int S = w_dtype == SEMMOE_BF16 ? 1 : 3;
   const int EC = experts_per_pass(E, S), n_pass = (E + EC - 1) / EC;
   const int kb_all = (H + BK - 1) / BK;
@@ -857,10 +870,10 @@ cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, in
   int stages = (int)(stage_budget(cps) / stage_bytes);
   if (stages > MAX_STAGES) stages = MAX_STAGES;
   cudaError_t e;
-  if (S == 3 && cps == 1) e = launch_k<3, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, partials, s);
-  else if (S == 3) e = launch_k<3, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, partials, s);
-  else if (cps == 1) e = launch_k<1, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, partials, s);
-  else e = launch_k<1, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, partials, s);
+  if (S == 3 && cps == 1) e = launch_k<3, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
+  else if (S == 3) e = launch_k<3, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
+  else if (cps == 1) e = launch_k<1, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
+  else e = launch_k<1, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
@@ -1038,6 +1051,11 @@ int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype) {
   const int EC = select_pass(E, w_dtype), n_pass = (E + EC - 1) / EC;
   const long long tiles = (T + BM - 1) / BM;
   const int kb_all = (H + BK - 1) / BK;
+  // Up to 8 tiles and 2 passes of experts.  Measured (H 2048, device us a call, here and by
+  // the split-K product): 128 experts, bf16: 12.4 / 16.7 at 1024 tokens, 23.6 / 14.4 at
+  // 2048 (16 clusters of 8 CTAs do not fit at once); 256, bf16: 17.2 / 21.6 at 1024; four
+  // passes (256, fp32): 30.0 / 30.3 at 256, 30.1 / 26.9 at 1024.
+  if (tiles > 8 || n_pass > 2) return 0;
   const size_t words = 2 * (size_t)BM * (EC + 4) + (size_t)(kClThreads / 32 - 2) * select_scratch(E, E, k_max);
   if (words * 4 > stage_budget(1)) return 0;
   int ks = 0;

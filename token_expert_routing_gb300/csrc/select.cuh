@@ -8,11 +8,12 @@
 // past 32), each finds the two largest of its share of c and they are merged.
 // A group's rank is the number of groups with a larger score, or an equal one
 // and a lower index; ranks below topk_group stay.
-// Picks: k_t rounds of a warp maximum over order-preserving keys (key 0: not to
-// be taken), ties to the lowest index holding it.
-// Weights: s_j, or s_j over the sum of the picks' -- computed as exp(log s_j -
-// max log s) over its sum (log sigmoid(l) = min(l, 0) - log1p(exp(-|l|))), so that
-// picks whose scores all underflow still share one.
+// Picks: each lane sorts the keys of its experts (order-preserving, 0: not to be
+// taken; equal keys by index), then k_t rounds take the largest head of any lane; only
+// when several lanes hold it does a second reduction find the lowest index.
+// Weights: s_j, or s_j over the sum of the picks'; where that sum is close to
+// underflow, exp(log s_j - max log s) over its sum (log sigmoid(l) = min(l, 0) -
+// log1p(exp(-|l|))), so that picks whose scores all underflow still share one.
 #pragma once
 
 #include <math.h>
@@ -25,7 +26,8 @@ namespace semmoe {
 // Words of scratch per warp: logits, choice scores, group scores, picks.
 __host__ __device__ constexpr int select_scratch(int E, int G, int k_max) { return 2 * E + G + k_max; }
 
-__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
+// Within 3 ulp: the quotient of numbers at most 1 apart in magnitude needs no slow path (0 for l < -88).
+__device__ __forceinline__ float sigmoid_f32(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 __device__ __forceinline__ float log_sigmoid_f32(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
 
 // (a, b) = the two largest of (a, b) and (c, d), each pair in descending order.
@@ -35,11 +37,26 @@ __device__ __forceinline__ void merge_top2(float& a, float& b, float c, float d)
   b = fmaxf(lo, fmaxf(b, d));
 }
 
+// The lane's biases, loaded once per warp (0 without a bias); bits: what is not finite.
+template <int NPER>
+__device__ __forceinline__ int load_bias(const Select& sel, int E, float (&bias)[NPER]) {
+  int bits = 0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const int e = (threadIdx.x & 31) + 32 * i;
+    bias[i] = sel.bias != nullptr && e < E ? __ldg(sel.bias + e) : 0.0f;
+    if (!(bias[i] < INFINITY)) {  // NaN or +inf: the expert is off
+      bits = SEMMOE_DEVERR_NONFINITE;
+      bias[i] = -INFINITY;
+    }
+  }
+  return bits;
+}
+
 // v: the token's logits, -inf where not finite and past E.  idx / w: its k_max output
-// slots; picked(e) is called once for each expert taken.  Returns this lane's device
-// error bits.  Every lane of the warp calls.
+// slots; picked(e) is called once for each expert taken.  Every lane of the warp calls.
 template <int NPER, typename F>
-__device__ __forceinline__ int warp_choose(const float (&v)[NPER], int E, int kt, int k_max, const Select& sel,
+__device__ __forceinline__ void warp_choose(const float (&v)[NPER], const float (&bias)[NPER], int E, int kt, int k_max, const Select& sel,
                                            float* scratch, int32_t* __restrict__ idx, float* __restrict__ w,
                                            F&& picked) {
   const int lane = threadIdx.x & 31;
@@ -49,7 +66,6 @@ __device__ __forceinline__ int warp_choose(const float (&v)[NPER], int E, int kt
   float* ch = lg + E;
   float* gs = ch + E;
   int* pick = reinterpret_cast<int*>(gs + G);
-  int bad = 0;
   float m = -INFINITY, z = 1.0f;  // the softmax's maximum and sum over all experts
   if (soft) {
 #pragma unroll
@@ -66,20 +82,24 @@ __device__ __forceinline__ int warp_choose(const float (&v)[NPER], int E, int kt
   float c[NPER];  // what experts are taken by
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
-    const int e = lane + 32 * i;
+    if (lane + 32 * i < E) lg[lane + 32 * i] = v[i];
     c[i] = v[i];
-    if (e < E) {
-      lg[e] = v[i];
-      if (sel.bias != nullptr || grouped) {
-        float s = v[i] == -INFINITY ? -INFINITY : soft ? expf(v[i] - m) / z : sigmoid_f32(v[i]);
-        if (sel.bias != nullptr) {
-          const float b = __ldg(sel.bias + e);
-          if (!(b < INFINITY)) bad |= SEMMOE_DEVERR_NONFINITE;  // NaN or +inf: the expert is off
-          s = b < INFINITY ? s + b : -INFINITY;
-          c[i] = s;
-        }
-        if (grouped) ch[e] = s;
-      }
+  }
+  if (sel.bias != nullptr || grouped) {
+    float s[NPER];
+    if (soft) {
+      const float r = 1.0f / z;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) s[i] = expf(v[i] - m) * r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) s[i] = sigmoid_f32(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const float b = v[i] == -INFINITY ? -INFINITY : s[i] + bias[i];
+      if (lane + 32 * i < E && grouped) ch[lane + 32 * i] = b;
+      if (sel.bias != nullptr) c[i] = b;
     }
   }
   if (grouped) {
@@ -126,61 +146,96 @@ __device__ __forceinline__ int warp_choose(const float (&v)[NPER], int E, int kt
       }
     }
   }
-  uint32_t key[NPER];
+  uint32_t key[NPER];  // descending once sorted
+  int at[NPER];        // the experts' indices
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     const uint32_t b = __float_as_uint(__fadd_rn(c[i], 0.0f));  // -0.0 -> +0.0
     key[i] = c[i] == -INFINITY ? 0u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    at[i] = lane + 32 * i;
   }
+#pragma unroll
+  for (int i = 1; i < NPER; ++i)
+#pragma unroll
+    for (int j = i; j > 0; --j) {  // strictly larger keys move ahead: equal ones stay in index order
+      const bool up = key[j] > key[j - 1];
+      const uint32_t hi = up ? key[j] : key[j - 1], lo = up ? key[j - 1] : key[j];
+      const int ih = up ? at[j] : at[j - 1], il = up ? at[j - 1] : at[j];
+      key[j - 1] = hi, key[j] = lo;
+      at[j - 1] = ih, at[j] = il;
+    }
   int taken = 0;
   for (; taken < kt; ++taken) {
-    uint32_t mk = key[0];
-#pragma unroll
-    for (int i = 1; i < NPER; ++i) mk = max(mk, key[i]);
-    mk = __reduce_max_sync(0xffffffffu, mk);
+    const uint32_t mk = __reduce_max_sync(0xffffffffu, key[0]);
     if (mk == 0u) break;  // none left to take
-    uint32_t first = 0xffffffffu;  // this lane's lowest index with that key
+    bool won = key[0] == mk;
+    const unsigned holders = __ballot_sync(0xffffffffu, won);
+    if (holders & (holders - 1)) won = at[0] == (int)__reduce_min_sync(0xffffffffu, won ? (unsigned)at[0] : 0xffffffffu);
+    if (won) pick[taken] = at[0];
 #pragma unroll
-    for (int i = NPER - 1; i >= 0; --i)
-      if (key[i] == mk) first = (uint32_t)(lane + 32 * i);
-    const int e = (int)__reduce_min_sync(0xffffffffu, first);
-#pragma unroll
-    for (int i = 0; i < NPER; ++i)
-      if (e == lane + 32 * i) key[i] = 0u;
-    if (lane == (taken & 31)) pick[taken] = e;
+    for (int i = 0; i < NPER; ++i) {  // the next head
+      key[i] = won ? (i + 1 < NPER ? key[i + 1] : 0u) : key[i];
+      at[i] = won && i + 1 < NPER ? at[i + 1] : at[i];
+    }
   }
   __syncwarp();
-  float top = -INFINITY, den = 0.0f;
+  // the pick of this lane, and the sum of the first 32 (the rest are added below)
+  float mine = 0.0f, den = soft ? z : 1.0f, top = 0.0f;
+  bool logs = false;
+  if (lane < taken) {
+    const float l = lg[pick[lane]];
+    mine = soft ? expf(l - m) : sigmoid_f32(l);
+  }
   if (sel.renorm) {
-    for (int j = lane; j < taken; j += 32) {
+    den = mine;
+    for (int j = lane + 32; j < taken; j += 32) {
       const float l = lg[pick[j]];
-      top = fmaxf(top, soft ? l : log_sigmoid_f32(l));
+      den += soft ? expf(l - m) : sigmoid_f32(l);
     }
+    if (taken <= 8) {
+      den += __shfl_xor_sync(0xffffffffu, den, 4);
+      den += __shfl_xor_sync(0xffffffffu, den, 2);
+      den += __shfl_xor_sync(0xffffffffu, den, 1);
+      den = __shfl_sync(0xffffffffu, den, 0);
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int j = lane; j < taken; j += 32) {
-      const float l = lg[pick[j]];
-      den += expf((soft ? l : log_sigmoid_f32(l)) - top);
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     }
+    logs = !(den > 1e-30f);
+    if (logs) {
+      top = -INFINITY;
+      for (int j = lane; j < taken; j += 32) {
+        const float l = lg[pick[j]];
+        top = fmaxf(top, soft ? l : log_sigmoid_f32(l));
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      den = 0.0f;
+      for (int j = lane; j < taken; j += 32) {
+        const float l = lg[pick[j]];
+        den += expf((soft ? l : log_sigmoid_f32(l)) - top);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
   }
   for (int j = lane; j < k_max; j += 32) {
     int e = -1;
     float g = 0.0f;
     if (j < taken) {
       e = pick[j];
-      const float l = lg[e];
-      if (sel.renorm) g = expf((soft ? l : log_sigmoid_f32(l)) - top) / den;
-      else g = soft ? expf(l - m) / z : sigmoid_f32(l);
-      g *= sel.scale;
+      g = mine;
+      if (logs || j >= 32) {
+        const float l = lg[e];
+        g = logs ? expf((soft ? l : log_sigmoid_f32(l)) - top) : soft ? expf(l - m) : sigmoid_f32(l);
+      }
+      g = g / den * sel.scale;  // a single pick's renormalised weight is exactly the scale
       picked(e);
     }
     idx[j] = e;
     w[j] = g;
   }
   __syncwarp();  // the scratch may be written again
-  return bad;
 }
 
 }  // namespace semmoe
