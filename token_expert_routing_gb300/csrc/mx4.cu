@@ -1,7 +1,7 @@
 // Quantisation to 4-bit microscaled values and back (format and layouts:
 // mx4.cuh).  Pure data movement: per value 2 or 4 bytes in and 17/32 of a byte
-// out, so the bound is HBM bandwidth; a lane takes 8 values of a row (one
-// 16-byte load of bf16), four lanes share a block, sixteen one 128-column tile.
+// out, so the bound is HBM bandwidth; a lane takes 16 values of a row (two
+// 16-byte loads of bf16), two lanes share a block, eight one 128-column tile.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
@@ -14,37 +14,58 @@ using namespace mx4;
 __device__ int g_err;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSpan = 256;  // columns a warp takes at once, 8 per lane
+constexpr int kSpan = 512;  // columns a warp takes at once, 16 per lane
 
-// Eight consecutive values of a row as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// Sixteen consecutive values of a row, as loaded and as fp32.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 a, b;
+};
+template <> struct Raw<float> {
+  float4 a, b, c, d;
+};
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+  r.a = __ldg(reinterpret_cast<const uint4*>(p));
+  r.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+}
+__device__ __forceinline__ void load16(const float* p, Raw<float>& r) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+  r.a = __ldg(q), r.b = __ldg(q + 1), r.c = __ldg(q + 2), r.d = __ldg(q + 3);
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&v)[16]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(a[i] << 16);
-    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&v)[16]) {
+  const float w[16] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w,
+                       r.c.x, r.c.y, r.c.z, r.c.w, r.d.x, r.d.y, r.d.z, r.d.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = w[i];
 }
 
-// The lane's eight codes, and in every lane of a 16-lane half the half's four
+// The lane's sixteen codes, and in every lane of an 8-lane group the group's four
 // scales as one word (block j at byte j).  Whole warp.
-__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], uint32_t& scales) {
+template <typename T>
+__device__ __forceinline__ uint2 quantise16(const Raw<T>& raw, uint32_t& scales) {
+  float v[16];
+  widen(raw, v);
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
   const uint32_t b = scale_code(a);
   const float f = inverse_scale(b);
-  uint32_t w = b << (8 * ((threadIdx.x >> 2) & 3));
-  w |= __shfl_xor_sync(0xffffffffu, w, 4);
-  scales = w | __shfl_xor_sync(0xffffffffu, w, 8);
-  return encode8(v[0] * f, v[1] * f, v[2] * f, v[3] * f, v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+  uint32_t w = b << (8 * ((threadIdx.x >> 1) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 2);
+  scales = w | __shfl_xor_sync(0xffffffffu, w, 4);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= f;
+  return make_uint2(encode8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]),
+                    encode8(v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]));
 }
 
 // Groups of group_rows rows.  A warp takes rows r, r + 32, r + 64, r + 96 of a
@@ -65,26 +86,22 @@ mx4_quantize_kernel(const T* __restrict__ x, int groups, int group_rows, int K, 
     const int in_group = (int)(tile % tiles) * kTileRows + r0;
     const size_t row = (size_t)g * group_rows + in_group;
     for (int c0 = 0; c0 < K; c0 += kSpan) {
-      const int c = c0 + lane * 8;
-      float v[4][8];
+      const int c = c0 + lane * 16;
+      Raw<T> v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (c < K && in_group + 32 * i < group_rows) {
-          load8(x + (row + 32 * i) * K + c, v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        v[i] = Raw<T>{};
+        if (c < K && in_group + 32 * i < group_rows) load16(x + (row + 32 * i) * K + c, v[i]);
       }
       uint32_t s[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w = quantise8(v[i], s[i]);
+        const uint2 w = quantise16(v[i], s[i]);
         if (c < K && in_group + 32 * i < group_rows)
-          *reinterpret_cast<uint32_t*>(codes + ((row + 32 * i) * K + c) / 2) = w;
+          *reinterpret_cast<uint2*>(codes + ((row + 32 * i) * K + c) / 2) = w;
       }
       const int ct = c / kTileCols;
-      if ((lane & 15) == 0 && ct < kc)
+      if ((lane & 7) == 0 && ct < kc)
         *reinterpret_cast<uint4*>(scales + ((size_t)tile * kc + ct) * kTileBytes + 16 * r0) =
             make_uint4(s[0], s[1], s[2], s[3]);
     }
@@ -94,7 +111,7 @@ mx4_quantize_kernel(const T* __restrict__ x, int groups, int group_rows, int K, 
 // Token rows into expert order: one warp per token quantises its row once and
 // writes the codes and scales to each of its pairs' sorted rows.
 constexpr int kMaxE = 256;
-constexpr int kBatch = 8;  // column spans held in registers: 2048 columns
+constexpr int kBatch = 4;  // column spans held in registers: 2048 columns
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -128,20 +145,17 @@ mx4_quantize_rows_kernel(const T* __restrict__ x, int n_tok, int K, const int32_
   const int max_tiles = P / kTileRows + E;  // what the caller's scales hold
   for (int t = blockIdx.x * kWarps + threadIdx.x / 32; t < n_tok; t += gridDim.x * kWarps) {
     for (int c0 = 0; c0 < K; c0 += kBatch * kSpan) {
-      float v[kBatch][8];
+      Raw<T> v[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int c = c0 + i * kSpan + lane * 8;
-        if (c < K) {
-          load8(x + (size_t)t * K + c, v[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        const int c = c0 + i * kSpan + lane * 16;
+        v[i] = Raw<T>{};
+        if (c < K) load16(x + (size_t)t * K + c, v[i]);
       }
-      uint32_t w[kBatch], s[kBatch];
+      uint2 w[kBatch];
+      uint32_t s[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) w[i] = quantise8(v[i], s[i]);
+      for (int i = 0; i < kBatch; ++i) w[i] = quantise16(v[i], s[i]);
       for (int j0 = 0; j0 < k_max; j0 += 32) {
         int q = j0 + lane < k_max ? pair_to_sorted[(size_t)t * k_max + j0 + lane] : -1;
         int at = 0;  // byte of the row's scales in its tile, and its row tile
@@ -170,9 +184,9 @@ mx4_quantize_rows_kernel(const T* __restrict__ x, int n_tok, int K, const int32_
           uint8_t* sc = scales + (size_t)rj * kc * kTileBytes + aj;
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            const int c = c0 + i * kSpan + lane * 8;
-            if (c < K) *reinterpret_cast<uint32_t*>(row + c / 2) = w[i];
-            if ((lane & 15) == 0 && c < K) *reinterpret_cast<uint32_t*>(sc + (size_t)(c / kTileCols) * kTileBytes) = s[i];
+            const int c = c0 + i * kSpan + lane * 16;
+            if (c < K) *reinterpret_cast<uint2*>(row + c / 2) = w[i];
+            if ((lane & 7) == 0 && c < K) *reinterpret_cast<uint32_t*>(sc + (size_t)(c / kTileCols) * kTileBytes) = s[i];
           }
         }
       }
@@ -180,19 +194,20 @@ mx4_quantize_rows_kernel(const T* __restrict__ x, int n_tok, int K, const int32_
   }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 w;
-  uint32_t* a = &w.x;
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    a[i] = *reinterpret_cast<uint32_t*>(&h);
+    w[i] = *reinterpret_cast<uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = w;
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // Value of one e2m1 code: the two exponent bits and the mantissa bit are fp32's
@@ -219,27 +234,32 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
     const long long g = tile / tiles;
     const int in_group = (int)(tile % tiles) * kTileRows + r0;
     const size_t row = (size_t)g * group_rows + in_group;
-    for (int c = lane * 8; c < K; c += kSpan) {
+    for (int c = lane * 16; c < K; c += kSpan) {
       const uint4 sw = __ldg(reinterpret_cast<const uint4*>(
           scales + ((size_t)tile * kc + c / kTileCols) * kTileBytes + 16 * r0));
       const uint32_t s[4] = {sw.x, sw.y, sw.z, sw.w};
+      uint2 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (in_group + 32 * i < group_rows)
+          w[i] = __ldg(reinterpret_cast<const uint2*>(codes + ((row + 32 * i) * K + c) / 2));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (in_group + 32 * i >= group_rows) break;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + ((row + 32 * i) * K + c) / 2));
         const float f = scale_value((s[i] >> (8 * ((c / kBlock) & 3))) & 255u);
-        float v[8];
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = decode(w >> (4 * j)) * f;
-        store8(out + (row + 32 * i) * K + c, v);
+        for (int j = 0; j < 16; ++j) v[j] = decode((j < 8 ? w[i].x : w[i].y) >> (4 * (j & 7))) * f;
+        store16(out + (row + 32 * i) * K + c, v);
       }
     }
   }
 }
 
-// One warp per unit until every SM holds eight CTAs, then a grid-stride loop.
+// CTAs for `units` warps' work, each warp a few units at most (a grid that fills the GPU
+// once left the last units to a few warps: 8% on 45056 units of 2048 columns).
 int grid_for(long long units) {
-  const long long blocks = (units + kWarps - 1) / kWarps, cap = 8LL * sm_count();
+  const long long blocks = (units + kWarps - 1) / kWarps, cap = 1 << 20;
   return (int)(blocks < cap ? blocks : cap);
 }
 
@@ -266,7 +286,8 @@ cudaError_t launch_mx4_quantize(const void* x, int dtype, int groups, int group_
 cudaError_t launch_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32_t* pair_to_sorted, int k_max,
                                      int P, const int32_t* expert_offsets, int E, uint8_t* codes, uint8_t* scales,
                                      cudaStream_t s) {
-  const int grid = grid_for(T);
+  const long long cap = 8LL * sm_count();  // each CTA first scans the offsets
+  const int grid = (int)(ceil_div(T, kWarps) < cap ? ceil_div(T, kWarps) : cap);
   cudaError_t e;
   if (dtype == SEMMOE_BF16)
     e = launch_kernel(mx4_quantize_rows_kernel<__nv_bfloat16>, dim3(grid), dim3(kThreads), 0, s, 1, true,
