@@ -151,6 +151,9 @@ struct Product {
   const int32_t* offsets;
   const int32_t* experts;
   int G, P, E, N, K, n_tiles;
+  // early: launched as the dependent of a kernel of this file that triggers after its own wait (so that everything
+  // before that kernel is complete): tables and B are read before this kernel's wait, only A is its output
+  int early;
   void* out;             // plain: [P, N]; SwiGLU: the packed h [P, N / 2]
   uint8_t* out_scales;   // SwiGLU: h's scales
 };
@@ -160,7 +163,6 @@ template <bool GLU, typename OUT>
 __global__ void __launch_bounds__(THREADS, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_as,
                 const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_bs, Product pr) {
-  pdl_trigger();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   unsigned char* ring = smem_raw + pad;  // stage s: A, B, the scales (A's two tiles, then B's by row tile, column tile)
@@ -189,7 +191,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     prefetch_map(&map_bs);
   }
   if (warp == 1) tmem_alloc(&sh.tmem_base, TMEM_COLS);
-  pdl_wait();
+  if (!pr.early) pdl_wait();
+  pdl_trigger();
   for (int g = threadIdx.x; g <= G; g += blockDim.x) sh.off[g] = pr.offsets[g];
   for (int g = threadIdx.x; g < G; g += blockDim.x) sh.pe[g] = pr.experts[g];
   __syncthreads();
@@ -243,43 +246,68 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   // stay in uniform registers, and one elected lane issues.  With loops of one lane alone
   // K = 2048 products took 83 us instead of 54 (32768 rows x 1536).
   if (warp == 0) {
-    uint32_t it = 0;
-    int g = 0;
-    bool ok = true;
     const int b_tiles = row_tiles(pr.N);  // scale row tiles of one matrix (or of its gate half)
-    for (int tile = unit0; ok && tile < total; tile += units) {
-      const int mt = tile / n_tiles, nt = tile % n_tiles;
-      const RowTile rt = decode_mtile(sh, g, mt);
-      const int e = rt.expert;
+    // Positions: the producer's place in the (tile, k-block) list.
+    struct Place {
+      int tile, kb, g;
+      RowTile rt;
+    };
+    auto begin = [&](Place& p) {
+      if (p.tile < total) p.rt = decode_mtile(sh, p.g, p.tile / n_tiles);
+    };
+    auto next = [&](Place& p) {
+      if (++p.kb == kb_n) {
+        p.kb = 0;
+        p.tile += units;
+        begin(p);
+      }
+    };
+    auto load_a = [&](const Place& p, int s) {
+      unsigned char* a = ring + (size_t)s * STAGE_BYTES;
+      tma_load_2d(a, &map_a, &sh.full[s], p.kb * (BK / 2), p.rt.row0);
+      // two column tiles (of the next row tile, or past the end, where K has only one more: not used)
+      tma_load_2d(a + A_BYTES + B_BYTES, &map_as, &sh.full[s], 0, p.tile / n_tiles * kc + 2 * p.kb);
+    };
+    auto load_b = [&](const Place& p, int s) {
+      const int nt = p.tile % n_tiles, e = p.rt.expert, x = p.kb * (BK / 2);
       const int b0 = GLU ? 2 * e * b_tiles + nt : e * b_tiles + 2 * nt;  // row tiles of B's two halves
       const int b1 = GLU ? b0 + b_tiles : b0 + 1;
-      for (int kb = 0; kb < kb_n; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!wait_for(&sh.empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          uint64_t* bar = &sh.full[s];
-          mbar_expect_tx(bar, STAGE_BYTES);
-          unsigned char* a = ring + (size_t)s * STAGE_BYTES;
-          unsigned char* b = a + A_BYTES;
-          unsigned char* sc = b + B_BYTES;
-          const int x = kb * (BK / 2);
-          tma_load_2d(a, &map_a, bar, x, rt.row0);
-          if (GLU) {
-            tma_load_4d(b, &map_b, bar, x, nt * HN, 0, e);
-            tma_load_4d(b + B_BYTES / 2, &map_b, bar, x, nt * HN, 1, e);
-          } else {
-            tma_load_3d(b, &map_b, bar, x, nt * BN, e);
-          }
-          // two column tiles each (of the next row tile, or past the end, where K has only one more: not used)
-          tma_load_2d(sc, &map_as, bar, 0, mt * kc + 2 * kb);
-          tma_load_2d(sc + 2 * kTileBytes, &map_bs, bar, 0, b0 * kc + 2 * kb);
-          tma_load_2d(sc + 4 * kTileBytes, &map_bs, bar, 0, b1 * kc + 2 * kb);
-        }
+      uint64_t* bar = &sh.full[s];
+      unsigned char* b = ring + (size_t)s * STAGE_BYTES + A_BYTES;
+      unsigned char* sc = b + B_BYTES;
+      mbar_expect_tx(bar, STAGE_BYTES);
+      if (GLU) {
+        tma_load_4d(b, &map_b, bar, x, nt * HN, 0, e);
+        tma_load_4d(b + B_BYTES / 2, &map_b, bar, x, nt * HN, 1, e);
+      } else {
+        tma_load_3d(b, &map_b, bar, x, nt * BN, e);
+      }
+      tma_load_2d(sc + 2 * kTileBytes, &map_bs, bar, 0, b0 * kc + 2 * p.kb);
+      tma_load_2d(sc + 4 * kTileBytes, &map_bs, bar, 0, b1 * kc + 2 * p.kb);
+    };
+    Place p{unit0, 0, 0, {}};
+    begin(p);
+    uint32_t it = 0;
+    if (pr.early) {  // the ring's first turn: B while the kernel before ends, then A
+      Place q = p;
+      for (uint32_t s = 0; s < STAGES && q.tile < total; ++s, next(q)) {
+        if (elect_one()) load_b(q, s);
         __syncwarp();
       }
+      pdl_wait();
+      for (; it < STAGES && p.tile < total; ++it, next(p)) {
+        if (elect_one()) load_a(p, it);
+        __syncwarp();
+      }
+    }
+    for (; p.tile < total; ++it, next(p)) {
+      const int s = it % STAGES;
+      if (!wait_for(&sh.empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) break;
+      if (elect_one()) {
+        load_b(p, s);
+        load_a(p, s);
+      }
+      __syncwarp();
     }
     if (lane == 0) *reinterpret_cast<volatile int*>(&sh.armed) = (int)it;
   } else if (warp == 1) {
@@ -518,8 +546,8 @@ int mx4_gemm_take_errors(cudaStream_t s, int* bits) { return take_error_word(g_e
 
 cudaError_t launch_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* offsets,
                                     const int32_t* experts, const uint8_t* b, const uint8_t* b_scales, int P, int E,
-                                    int N, int K, void* out, int out_dtype, cudaStream_t s) {
-  const Product pr{offsets, experts, E, P, E, N, K, (N + BN - 1) / BN, out, nullptr};
+                                    int N, int K, void* out, int out_dtype, cudaStream_t s, bool early) {
+  const Product pr{offsets, experts, E, P, E, N, K, (N + BN - 1) / BN, early, out, nullptr};
   return out_dtype == SEMMOE_BF16 ? launch_one<false, __nv_bfloat16>(a, a_scales, b, b_scales, pr, s)
                                   : launch_one<false, float>(a, a_scales, b, b_scales, pr, s);
 }
@@ -535,10 +563,10 @@ cudaError_t launch_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, co
                                    void* ws, cudaStream_t s) {
   uint8_t* h = static_cast<uint8_t*>(ws);
   uint8_t* hs = h + align_up((size_t)P * (I / 2), 256);
-  const Product p1{offsets, experts, E, P, E, I, H, (I + 127) / 128, h, hs};
+  const Product p1{offsets, experts, E, P, E, I, H, (I + 127) / 128, 0, h, hs};
   cudaError_t e = launch_one<true, __nv_bfloat16>(x, x_scales, w13, w13_scales, p1, s);
   if (e != cudaSuccess) return e;
-  return launch_mx4_grouped_gemm(h, hs, offsets, experts, w2, w2_scales, P, E, H, I, y, SEMMOE_BF16, s);
+  return launch_mx4_grouped_gemm(h, hs, offsets, experts, w2, w2_scales, P, E, H, I, y, SEMMOE_BF16, s, true);
 }
 
 }  // namespace semmoe
