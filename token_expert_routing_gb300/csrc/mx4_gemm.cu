@@ -162,7 +162,8 @@ struct Product {
 template <bool GLU, typename OUT>
 __global__ void __launch_bounds__(THREADS, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_as,
-                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_bs, Product pr) {
+                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_bs,
+                const __grid_constant__ CUtensorMap map_out, Product pr) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   unsigned char* ring = smem_raw + pad;  // stage s: A, B, the scales (A's two tiles, then B's by row tile, column tile)
@@ -460,6 +461,22 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             const int col = nt * BN + HN * w + 64 * i + c;
             if (col >= pr.N) break;
             const uint32_t* src = sizeof(OUT) == 2 ? y + c / 2 : (c < 32 ? x0 + c : x1 + c - 32);
+            if (sizeof(OUT) == 2 && wrows >= 32) {  // whole rows: by TMA
+              if (lane == 0) bulk_wait_read<0>();  // the store before has read the buffer
+              __syncwarp();
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                *reinterpret_cast<uint4*>(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(src[4 * v], src[4 * v + 1], src[4 * v + 2], src[4 * v + 3]);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&map_out, stage, col, row0 + q * 32);
+                bulk_commit();
+              }
+              continue;
+            }
+            if (sizeof(OUT) == 2 && lane == 0) bulk_wait_read<0>();
             emit(stage, src, static_cast<unsigned char*>(pr.out) + ((size_t)(row0 + q * 32) * pr.N + col) * sizeof(OUT),
                  (size_t)pr.N * sizeof(OUT), (pr.N - col) * (int)sizeof(OUT), wrows, lane);
           }
@@ -468,6 +485,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     }
   }
 
+  if (!GLU && warp >= 2 && lane == 0) bulk_wait_all();  // this warp's stores are complete
   fence_before();
   __syncthreads();
   if (warp == 0 && lane == 0 && *abort_flag) {  // no TMA write may still be landing when the CTA exits
@@ -528,6 +546,12 @@ cudaError_t launch_one(const void* a, const void* a_scales, const void* b, const
   }
   ok = ok && map_scales(&mas, a_scales, (long long)pr.P / BM + pr.G, pr.K) &&
        map_scales(&mbs, b_scales, (long long)(GLU ? 2 : 1) * pr.E * row_tiles(pr.N), pr.K);
+  CUtensorMap mo = {};
+  if (!GLU && sizeof(OUT) == 2) {  // boxes of 32 rows x 32 columns, 64-byte swizzle
+    const cuuint64_t dims[2] = {(cuuint64_t)pr.N, (cuuint64_t)pr.P}, strides[1] = {(cuuint64_t)pr.N * 2};
+    const cuuint32_t box[2] = {32, 32};
+    ok = ok && make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (!ok) return cudaErrorInvalidValue;
   auto kern = mx4_gemm_kernel<GLU, OUT>;
   static std::atomic<unsigned long long> smem_set{0};
@@ -535,7 +559,7 @@ cudaError_t launch_one(const void* a, const void* a_scales, const void* b, const
   if (e != cudaSuccess) return e;
   const long long tiles = ((long long)pr.P / BM + pr.G) * pr.n_tiles;  // of any grouping, at most
   const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-  e = launch_kernel(kern, dim3(grid), dim3(THREADS), kSmemBytes, s, 1, true, ma, mas, mb, mbs, pr);
+  e = launch_kernel(kern, dim3(grid), dim3(THREADS), kSmemBytes, s, 1, true, ma, mas, mb, mbs, mo, pr);
   count_launches(1);
   return e;
 }
