@@ -225,9 +225,9 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
  *
  * A bias of -inf switches an expert off: it is never taken and adds nothing to
  * its group's score (a group with every expert off comes last).  A token with
- * fewer than k_t experts to take has padding (-1, weight 0) in the slots left;
- * its live pairs are then fewer, which semmoe_permute and the FFN allow (P is
- * an upper bound).  A bias of NaN or +inf switches its expert off and sets
+ * fewer than k_t experts to take has padding (-1, weight 0) in the slots left,
+ * and the live pairs, semmoe_permute's P, are fewer than the sum of k_t by as
+ * many.  A bias of NaN or +inf switches its expert off and sets
  * SEMMOE_DEVERR_NONFINITE; so does a non-finite logit, for its token.
  *
  * score       SEMMOE_SCORE_SIGMOID or SEMMOE_SCORE_SOFTMAX

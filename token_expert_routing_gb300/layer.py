@@ -8,6 +8,7 @@ step runs in the library's kernels, and nothing synchronises the host.
 """
 from __future__ import annotations
 
+import dataclasses
 from dataclasses import dataclass
 from typing import Optional
 
@@ -31,7 +32,7 @@ class LayerOutput:
     expert_counts: torch.Tensor
     sorted_to_pair: torch.Tensor
     pair_to_sorted: torch.Tensor
-    x_perm: Optional[torch.Tensor]   # None when GEMM1 gathers x through the permutation
+    x_perm: Optional[torch.Tensor]   # None when GEMM1 gathers x through the permutation, or the rows are 4-bit (mx4)
     y_perm: Optional[torch.Tensor]   # None when GEMM2 adds its rows into the token order (fused_combine)
     y_shared: Optional[torch.Tensor]
     schedule: Optional[dict] = None      # semmoe_dp_schedule outputs (when req_offsets is given)
@@ -62,6 +63,33 @@ def fuse_gather_default(I: int, dtype) -> bool:
     return I <= 384 and dtype == torch.bfloat16
 
 
+@dataclass(frozen=True)
+class RouteSelect:
+    """How a layer's router chooses experts by score (semmoe_route_select).
+
+    score "sigmoid" or "softmax"; bias [E] added for the choice only (-inf switches
+    an expert off; a forward in which tokens have fewer than k experts left needs
+    k_per_token and P, the pairs that are left); the topk_group best of n_group
+    groups, scored by their group_top (1 or 2) largest, stay; weights are
+    the picks' scores, over their sum if renorm, times scale.
+    """
+    score: str = "sigmoid"
+    bias: Optional[torch.Tensor] = None
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 2
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("sigmoid", "softmax"):
+            raise ValueError("score is 'sigmoid' or 'softmax'")
+
+    @property
+    def code(self) -> int:
+        return abi.SEMMOE_SCORE_SIGMOID if self.score == "sigmoid" else abi.SEMMOE_SCORE_SOFTMAX
+
+
 class MoELayer:
     """Weights and tables of one MoE layer, resident on a CUDA device.
 
@@ -71,12 +99,28 @@ class MoELayer:
     optional expert -> next-layer-rank transition table.  With ``sub_logw``
     [E] fp32 the layer routes by MoE-Prism's hierarchical gating: w_router is
     then the parent router [Ep,H] and each parent owns N = E / Ep sub-experts.
+    With ``select`` (a RouteSelect) it routes by score, with a choice bias and
+    groups.  ``mx4``: the experts' weights are quantised here to 4-bit
+    microscaled values (the originals are not kept) and forward quantises the
+    token rows into expert order and runs semmoe_mx4_grouped_ffn; bf16 layers
+    with H % 32 == 0 and I % 32 == 0 (shared experts stay bf16).
     """
 
     def __init__(self, w_router, w13, w2, expert_rank, lut, R: int, k_max: int, ws13=None, ws2=None,
                  trans=None, sub_logw=None, fused_gather: Optional[bool] = None,
                  fused_combine: Optional[bool] = None, overlap: bool = True,
-                 overlap_shared: bool = True, shared_at: str = "start", device="cuda"):
+                 overlap_shared: bool = True, shared_at: str = "start", device="cuda",
+                 select: Optional[RouteSelect] = None, mx4: bool = False):
+        if select is not None and sub_logw is not None:
+            raise ValueError("select and sub_logw are two ways to route: give one")
+        if mx4:
+            if w13.dtype != torch.bfloat16 or w2.dtype != torch.bfloat16:
+                raise ValueError("mx4 needs bf16 experts")
+            if w13.shape[2] % 32 or w2.shape[2] % 32:
+                raise ValueError("mx4 needs H and I in blocks of 32")
+            if fused_gather or fused_combine:
+                raise ValueError("mx4 quantises the rows into expert order: no fused_gather or fused_combine")
+            fused_gather, fused_combine = False, False
         dev = torch.device(device)
         c = lambda t: None if t is None else t.to(dev).contiguous()  # noqa: E731
         self.w_router, self.w13, self.w2 = c(w_router), c(w13), c(w2)
@@ -116,9 +160,16 @@ class MoELayer:
         self.Ep = self.w_router.shape[0]          # router rows: experts, or parents (hierarchical)
         if self.sub_logw is not None and (self.E % self.Ep or self.sub_logw.numel() != self.E):
             raise ValueError("hierarchical gating needs E = Ep * N and sub_logw of E values")
-        self.dtype = self.w13.dtype
+        self.dtype, self.dcode = self.w13.dtype, abi.dtype_code(self.w13)
         self.device = dev
         self._ws = {}
+        if select is not None and select.bias is not None:
+            select = dataclasses.replace(select, bias=c(select.bias).to(torch.float32))
+        self.select = select
+        self.mx4 = None  # codes and scales of w13 and w2
+        if mx4:
+            self.mx4 = (*self._quantised(self.w13, 2 * self.E, self.I, self.H), *self._quantised(self.w2, self.E, self.H, self.I))
+            self.w13 = self.w2 = None
         # An fp32 router weight meeting bf16 activations is split into its three
         # bf16 parts once here instead of on every call.
         self.w_route, self.w_route_dtype = self.w_router, abi.dtype_code(self.w_router)
@@ -127,6 +178,14 @@ class MoELayer:
             self.w_route = torch.empty(n, dtype=torch.uint8, device=dev)
             abi.semmoe_route_split_weight(self.w_router, self.H, self.Ep, self.w_route)
             self.w_route_dtype = abi.SEMMOE_F32_SPLIT
+
+    def _quantised(self, w, groups, rows, K):
+        """4-bit codes and scales of a weight of ``groups`` matrices [rows, K]."""
+        u8 = dict(dtype=torch.uint8, device=self.device)
+        codes = torch.empty(groups * rows, K // 2, **u8)
+        scales = torch.empty(abi.semmoe_mx4_scales_size(groups * rows, K, groups), **u8)
+        abi.semmoe_mx4_quantize(w, groups, rows, K, codes, scales)
+        return codes, scales
 
     def _router_weight(self, x):
         """The router weight to pass with x, and its type code (the pre-split
@@ -197,7 +256,7 @@ class MoELayer:
         T = x.shape[0]
         H, E, I, R, k_max = self.H, self.E, self.I, self.R, self.k_max
         dev = self.device
-        dcode = abi.dtype_code(self.w13)
+        dcode = self.dcode
         y_shared = None
         shared_side = self.ws13 is not None and self.overlap_shared
 
@@ -231,7 +290,14 @@ class MoELayer:
         topk_w = torch.empty(T, k_max, dtype=torch.float32, device=dev)
         # the router counts its picks per 128-token chunk; the permute starts from that table
         pair_counts = torch.empty(max(abi.semmoe_pair_counts_size(T, E) // 4, 4), **i32)
-        if self.sub_logw is None:
+        if self.select is not None:
+            sel = self.select
+            wr, wd = self._router_weight(x)
+            ws = self._workspace("route", abi.semmoe_route_select_workspace_size(T, H, E, abi.dtype_code(x), wd))
+            abi.semmoe_route_select(x, wr, logits_in, logits, sel.code, sel.bias, sel.n_group, sel.topk_group,
+                                    sel.group_top, sel.renorm, sel.scale, k_per_token, k or 0, T, H, E, k_max,
+                                    topk_idx, topk_w, ws, stream, w_dtype=wd, pair_counts=pair_counts)
+        elif self.sub_logw is None:
             wr, wd = self._router_weight(x)
             ws = self._workspace("route", abi.semmoe_route_workspace_size(T, H, E, abi.dtype_code(x), wd))
             abi.semmoe_route(x, wr, logits_in, logits, k_per_token, k or 0, T, H, E, k_max,
@@ -283,9 +349,10 @@ class MoELayer:
         expert_counts = torch.empty(E, **i32)
         sorted_to_pair = torch.empty(max(P, 1), **i32)
         pair_to_sorted = torch.empty(T * k_max, **i32)
-        x_perm = None if self.fused_gather else torch.empty(P, H, dtype=x.dtype, device=dev)
+        index_only = self.fused_gather or self.mx4 is not None  # the permute gathers no rows
+        x_perm = None if index_only else torch.empty(P, H, dtype=x.dtype, device=dev)
         ws = self._workspace("permute", abi.semmoe_permute_workspace_size(T, k_max, E))
-        abi.semmoe_permute(topk_idx, self.expert_rank, None if self.fused_gather else x, T, H, E, R, k_max, P,
+        abi.semmoe_permute(topk_idx, self.expert_rank, None if index_only else x, T, H, E, R, k_max, P,
                            expert_offsets, rank_offsets, phys_to_expert, expert_counts, sorted_to_pair,
                            pair_to_sorted, x_perm, ws, stream, pair_counts=pair_counts)
         mark("permute")
@@ -293,8 +360,17 @@ class MoELayer:
         acc = torch.empty(T, H, dtype=torch.float32, device=dev) if self.fused_combine else None
         if has_shared and self.shared_at == "permute":  # the shared experts beside the routed FFN
             run_shared()
-        ws = self._workspace("ffn", abi.semmoe_grouped_ffn_workspace_size(P, I, dcode))
-        if self.fused_combine:  # GEMM2 adds its rows into the token order
+        if self.mx4 is not None:
+            ws = self._workspace("ffn", abi.semmoe_mx4_grouped_ffn_workspace_size(P, E, I))
+        else:
+            ws = self._workspace("ffn", abi.semmoe_grouped_ffn_workspace_size(P, I, dcode))
+        if self.mx4 is not None:
+            xq = self._workspace("mx4_rows", P * (H // 2))
+            xs = self._workspace("mx4_scales", abi.semmoe_mx4_scales_size(P, H, E))
+            abi.semmoe_mx4_quantize_rows(x, T, H, pair_to_sorted, k_max, P, expert_offsets, E, xq, xs, stream)
+            mark("quantize")
+            abi.semmoe_mx4_grouped_ffn(xq, xs, expert_offsets, phys_to_expert, *self.mx4, P, E, H, I, y_perm, ws, stream)
+        elif self.fused_combine:  # GEMM2 adds its rows into the token order
             abi.semmoe_grouped_ffn_combine(x if self.fused_gather else x_perm, self.fused_gather, sorted_to_pair,
                                            k_max, T, expert_offsets, phys_to_expert, self.w13, self.w2, topk_w,
                                            P, E, H, I, acc, ws, stream)
