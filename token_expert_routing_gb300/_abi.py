@@ -1,6 +1,8 @@
-"""ctypes binding of libsemmoe.so: the C ABI declared in include/semmoe.h.
+"""Binding of libsemmoe.so: the C ABI declared in include/semmoe.h.
 
 Argument marshalling only -- every step runs in the library's CUDA kernels.
+Calls go through the compiled entry points (``_fast``, csrc/binding.cpp); the same
+symbols are declared for ctypes in ``SIGNATURES`` (``lib()``).
 Functions carry the C names and take torch tensors (device memory) or None
 for pointers; a non-zero status raises SemMoEError with the library's message.
 There is no fallback: if the library is missing, every call raises.
@@ -112,20 +114,27 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_fast = None
+
+
+def fast():
+    """The entry points compiled against the library (csrc/binding.cpp): the C
+    names, taking tensors, addresses or None for pointers, and returning the C status."""
+    global _fast
+    if _fast is None:
+        lib()   # says how to build what is missing
+        try:
+            from . import _fast as module
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is missing: build it with "
+                               "`python -m token_expert_routing_gb300.build`") from e
+        _fast = module
+    return _fast
+
+
 def _check(rc: int) -> None:
     if rc != SEMMOE_OK:
         raise SemMoEError(rc, lib().semmoe_last_error().decode())
-
-
-def _p(t) -> int | None:
-    """Device pointer of a contiguous CUDA tensor (None passes NULL)."""
-    if t is None or t.__class__ is int:
-        return t
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
 
 
 def _want(t, dtype, numel, what):
@@ -175,15 +184,15 @@ def semmoe_check_errors(stream=None) -> int:
 
 
 def semmoe_route_workspace_size(T, H, E, x_dtype: int, w_dtype: int) -> int:
-    return lib().semmoe_route_workspace_size(T, H, E, x_dtype, w_dtype)
+    return fast().semmoe_route_workspace_size(T, H, E, x_dtype, w_dtype)
 
 
 def semmoe_pair_counts_size(T, E) -> int:
-    return lib().semmoe_pair_counts_size(T, E)
+    return fast().semmoe_pair_counts_size(T, E)
 
 
 def semmoe_pair_counts_stride(T) -> int:
-    return lib().semmoe_pair_counts_stride(T)
+    return fast().semmoe_pair_counts_stride(T)
 
 
 def semmoe_route(x, w_router, logits_in, logits_out, k_per_token, k_uniform, T, H, E, k_max,
@@ -198,21 +207,21 @@ def semmoe_route(x, w_router, logits_in, logits_out, k_per_token, k_uniform, T, 
     if ws is None:
         n = semmoe_route_workspace_size(T, max(H, 1), E, xd, wd)
         ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
-    _check(lib().semmoe_route(_p(x), xd, _p(w_router), wd, _p(logits_in), _p(logits_out),
-                              _p(k_per_token), k_uniform, T, H, E, k_max, _p(topk_idx), _p(topk_w),
-                              _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _check(fast().semmoe_route(x, xd, w_router, wd, logits_in, logits_out,
+                              k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w,
+                              pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_route_split_size(H, E) -> int:
-    return lib().semmoe_route_split_size(H, E)
+    return fast().semmoe_route_split_size(H, E)
 
 
 def semmoe_route_split_weight(w, H, E, split, stream=None):
-    _check(lib().semmoe_route_split_weight(_p(w), H, E, _p(split), _stream(stream)))
+    _check(fast().semmoe_route_split_weight(w, H, E, split, _stream(stream)))
 
 
 def semmoe_route_hier_workspace_size(T, H, Ep, x_dtype: int, w_dtype: int) -> int:
-    return lib().semmoe_route_hier_workspace_size(T, H, Ep, x_dtype, w_dtype)
+    return fast().semmoe_route_hier_workspace_size(T, H, Ep, x_dtype, w_dtype)
 
 
 def semmoe_route_hier(x, w_parent, logits_in, logits_out, sub_logw, N, k_per_token, k_uniform, T, H, Ep, k_max,
@@ -225,13 +234,13 @@ def semmoe_route_hier(x, w_parent, logits_in, logits_out, sub_logw, N, k_per_tok
     if ws is None:
         n = semmoe_route_hier_workspace_size(T, max(H, 1), Ep, xd, wd)
         ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
-    _check(lib().semmoe_route_hier(_p(x), xd, _p(w_parent), wd, _p(logits_in), _p(logits_out), _p(sub_logw), N,
-                                   _p(k_per_token), k_uniform, T, H, Ep, k_max, _p(topk_idx), _p(topk_w),
-                                   _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _check(fast().semmoe_route_hier(x, xd, w_parent, wd, logits_in, logits_out, sub_logw, N,
+                                   k_per_token, k_uniform, T, H, Ep, k_max, topk_idx, topk_w,
+                                   pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_route_select_workspace_size(T, H, E, x_dtype: int, w_dtype: int) -> int:
-    return lib().semmoe_route_select_workspace_size(T, H, E, x_dtype, w_dtype)
+    return fast().semmoe_route_select_workspace_size(T, H, E, x_dtype, w_dtype)
 
 
 def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_group, topk_group, group_top, renorm,
@@ -247,23 +256,23 @@ def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_
     if ws is None:
         n = semmoe_route_select_workspace_size(T, max(H, 1), E, xd, wd)
         ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
-    _check(lib().semmoe_route_select(_p(x), xd, _p(w_router), wd, _p(logits_in), _p(logits_out), score, _p(bias),
+    _check(fast().semmoe_route_select(x, xd, w_router, wd, logits_in, logits_out, score, bias,
                                      n_group, topk_group, group_top, int(bool(renorm)), float(scale),
-                                     _p(k_per_token), k_uniform, T, H, E, k_max, _p(topk_idx), _p(topk_w),
-                                     _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                     k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w,
+                                     pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_affinity_lookup(token_ids, lut, V, R, T, pred_rank, stream=None):
-    _check(lib().semmoe_affinity_lookup(_p(token_ids), _p(lut), V, R, T, _p(pred_rank), _stream(stream)))
+    _check(fast().semmoe_affinity_lookup(token_ids, lut, V, R, T, pred_rank, _stream(stream)))
 
 
 def semmoe_remote_count(topk_idx, pred_rank, expert_rank, T, k_max, E, R, counts, remote, stream=None):
-    _check(lib().semmoe_remote_count(_p(topk_idx), _p(pred_rank), _p(expert_rank), T, k_max, E, R,
-                                     _p(counts), _p(remote), _stream(stream)))
+    _check(fast().semmoe_remote_count(topk_idx, pred_rank, expert_rank, T, k_max, E, R,
+                                     counts, remote, _stream(stream)))
 
 
 def semmoe_permute_workspace_size(T, k_max, E) -> int:
-    return lib().semmoe_permute_workspace_size(T, k_max, E)
+    return fast().semmoe_permute_workspace_size(T, k_max, E)
 
 
 def semmoe_permute(topk_idx, expert_rank, x, T, H, E, R, k_max, P, expert_offsets, rank_offsets,
@@ -272,10 +281,10 @@ def semmoe_permute(topk_idx, expert_rank, x, T, H, E, R, k_max, P, expert_offset
     """``pair_counts``: the router's count table for these topk_idx, or None
     (the permute then counts the pairs itself)."""
     d = dtype_code(x) if x is not None else SEMMOE_F32
-    _check(lib().semmoe_permute(_p(topk_idx), _p(expert_rank), _p(x), d, T, H, E, R, k_max, P,
-                                _p(expert_offsets), _p(rank_offsets), _p(phys_to_expert),
-                                _p(expert_counts), _p(sorted_to_pair), _p(pair_to_sorted), _p(x_perm),
-                                _p(pair_counts), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _check(fast().semmoe_permute(topk_idx, expert_rank, x, d, T, H, E, R, k_max, P,
+                                expert_offsets, rank_offsets, phys_to_expert,
+                                expert_counts, sorted_to_pair, pair_to_sorted, x_perm,
+                                pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_permute_noalloc(topk_idx, expert_rank, x, T, H, E, R, k_max, P, expert_offsets, rank_offsets,
@@ -284,118 +293,120 @@ def semmoe_permute_noalloc(topk_idx, expert_rank, x, T, H, E, R, k_max, P, exper
     """semmoe_permute without a workspace: for callers that cannot allocate
     device memory (the scratch is a static 96 KiB array inside the library)."""
     d = dtype_code(x) if x is not None else SEMMOE_F32
-    _check(lib().semmoe_permute_noalloc(_p(topk_idx), _p(expert_rank), _p(x), d, T, H, E, R, k_max, P,
-                                        _p(expert_offsets), _p(rank_offsets), _p(phys_to_expert),
-                                        _p(expert_counts), _p(sorted_to_pair), _p(pair_to_sorted),
-                                        _p(x_perm), _stream(stream)))
+    _check(fast().semmoe_permute_noalloc(topk_idx, expert_rank, x, d, T, H, E, R, k_max, P,
+                                        expert_offsets, rank_offsets, phys_to_expert,
+                                        expert_counts, sorted_to_pair, pair_to_sorted,
+                                        x_perm, _stream(stream)))
 
 
 def semmoe_grouped_ffn_workspace_size(P, I, dtype: int) -> int:
-    return lib().semmoe_grouped_ffn_workspace_size(P, I, dtype)
+    return fast().semmoe_grouped_ffn_workspace_size(P, I, dtype)
 
 
 def semmoe_grouped_ffn(x_perm, expert_offsets, phys_to_expert, w13, w2, P, E, H, I, y_perm, ws,
                        stream=None):
-    _check(lib().semmoe_grouped_ffn(_p(x_perm), _p(expert_offsets), _p(phys_to_expert), _p(w13),
-                                    _p(w2), dtype_code(w13), P, E, H, I, _p(y_perm), _p(ws),
+    _check(fast().semmoe_grouped_ffn(x_perm, expert_offsets, phys_to_expert, w13,
+                                    w2, dtype_code(w13), P, E, H, I, y_perm, ws,
                                     ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_grouped_ffn_gather(x, sorted_to_pair, k_max, T, expert_offsets, phys_to_expert, w13, w2, P, E, H, I,
                               y_perm, ws, stream=None):
-    _check(lib().semmoe_grouped_ffn_gather(_p(x), _p(sorted_to_pair), k_max, T, _p(expert_offsets),
-                                           _p(phys_to_expert), _p(w13), _p(w2), dtype_code(w13), P, E, H, I,
-                                           _p(y_perm), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _check(fast().semmoe_grouped_ffn_gather(x, sorted_to_pair, k_max, T, expert_offsets,
+                                           phys_to_expert, w13, w2, dtype_code(w13), P, E, H, I,
+                                           y_perm, ws, ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_grouped_ffn_form(x, sorted_to_pair, k_max, T, expert_offsets, phys_to_expert, w13, w2, P, E, H, I,
                             y_perm, ws, form1, form2, stream=None):
-    _check(lib().semmoe_grouped_ffn_form(_p(x), _p(sorted_to_pair), k_max, T, _p(expert_offsets),
-                                         _p(phys_to_expert), _p(w13), _p(w2), dtype_code(w13), P, E, H, I,
-                                         _p(y_perm), _p(ws), ws.numel() * ws.element_size(), form1, form2,
+    _check(fast().semmoe_grouped_ffn_form(x, sorted_to_pair, k_max, T, expert_offsets,
+                                         phys_to_expert, w13, w2, dtype_code(w13), P, E, H, I,
+                                         y_perm, ws, ws.numel() * ws.element_size(), form1, form2,
                                          _stream(stream)))
 
 
 def semmoe_grouped_ffn_combine(x, x_rows_are_tokens, sorted_to_pair, k_max, T, expert_offsets, phys_to_expert, w13,
                                w2, topk_w, P, E, H, I, acc, ws, stream=None):
-    _check(lib().semmoe_grouped_ffn_combine(_p(x), int(bool(x_rows_are_tokens)), _p(sorted_to_pair), k_max, T,
-                                            _p(expert_offsets), _p(phys_to_expert), _p(w13), _p(w2), _p(topk_w),
-                                            dtype_code(w13), P, E, H, I, _p(acc), _p(ws),
+    _check(fast().semmoe_grouped_ffn_combine(x, int(bool(x_rows_are_tokens)), sorted_to_pair, k_max, T,
+                                            expert_offsets, phys_to_expert, w13, w2, topk_w,
+                                            dtype_code(w13), P, E, H, I, acc, ws,
                                             ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_combine_finish(acc, y_shared, T, H, out, stream=None):
-    _check(lib().semmoe_combine_finish(_p(acc), _p(y_shared), dtype_code(out), T, H, _p(out), _stream(stream)))
+    _check(fast().semmoe_combine_finish(acc, y_shared, dtype_code(out), T, H, out, _stream(stream)))
 
 
 def semmoe_shared_ffn_workspace_size(T, I_s, dtype: int) -> int:
-    return lib().semmoe_shared_ffn_workspace_size(T, I_s, dtype)
+    return fast().semmoe_shared_ffn_workspace_size(T, I_s, dtype)
 
 
 def semmoe_shared_ffn(x, ws13, ws2, T, H, I_s, y_shared, ws, stream=None):
-    _check(lib().semmoe_shared_ffn(_p(x), _p(ws13), _p(ws2), dtype_code(ws13), T, H, I_s,
-                                   _p(y_shared), _p(ws), ws.numel() * ws.element_size(),
+    _check(fast().semmoe_shared_ffn(x, ws13, ws2, dtype_code(ws13), T, H, I_s,
+                                   y_shared, ws, ws.numel() * ws.element_size(),
                                    _stream(stream)))
 
 
 def semmoe_combine(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, out, stream=None):
-    _check(lib().semmoe_combine(_p(y_perm), _p(pair_to_sorted), _p(topk_w), _p(y_shared),
-                                dtype_code(out), T, H, k_max, P, _p(out), _stream(stream)))
+    _check(fast().semmoe_combine(y_perm, pair_to_sorted, topk_w, y_shared,
+                                dtype_code(out), T, H, k_max, P, out, _stream(stream)))
 
 
 def semmoe_dp_schedule(pred_rank, req_offsets, T, n_req, R, hist, req_rank, req_order, rank_req_offsets,
                        req_tok_start, tok_order, tok_rank, rank_tok_offsets, stream=None):
-    _check(lib().semmoe_dp_schedule(_p(pred_rank), _p(req_offsets), T, n_req, R, _p(hist), _p(req_rank),
-                                    _p(req_order), _p(rank_req_offsets), _p(req_tok_start), _p(tok_order),
-                                    _p(tok_rank), _p(rank_tok_offsets), _stream(stream)))
+    _check(fast().semmoe_dp_schedule(pred_rank, req_offsets, T, n_req, R, hist, req_rank,
+                                    req_order, rank_req_offsets, req_tok_start, tok_order,
+                                    tok_rank, rank_tok_offsets, _stream(stream)))
 
 
 def semmoe_transition_lookup(topk_idx, k_per_token, k_uniform, trans, T, k_max, E, R, pred_next, stream=None):
-    _check(lib().semmoe_transition_lookup(_p(topk_idx), _p(k_per_token), k_uniform, _p(trans), T, k_max, E, R,
-                                          _p(pred_next), _stream(stream)))
+    _check(fast().semmoe_transition_lookup(topk_idx, k_per_token, k_uniform, trans, T, k_max, E, R,
+                                          pred_next, _stream(stream)))
 
 
 def semmoe_mx4_scales_size(rows, K, groups) -> int:
-    return lib().semmoe_mx4_scales_size(rows, K, groups)
+    return fast().semmoe_mx4_scales_size(rows, K, groups)
 
 
 def _mx4(codes, scales, rows, K, row_tiles, what):
-    """Codes and scales of ``rows`` rows of K values in ``row_tiles`` 128-row tiles."""
-    _want(codes, torch.uint8, rows * (K // 2), what)
-    _want(scales, torch.uint8, row_tiles * (-(-K // 128)) * 512, what + " scales")
+    """Refuse codes and scales that do not hold ``rows`` rows of K values in ``row_tiles`` 128-row tiles."""
+    if codes.dtype is not torch.uint8 or codes.numel() < rows * (K // 2):
+        _want(codes, torch.uint8, rows * (K // 2), what)
+    if scales.dtype is not torch.uint8 or scales.numel() < row_tiles * ((K + 127) // 128) * 512:
+        _want(scales, torch.uint8, row_tiles * ((K + 127) // 128) * 512, what + " scales")
 
 
 def semmoe_mx4_quantize(x, groups, group_rows, K, codes, scales, stream=None):
     """x [groups * group_rows, K] (fp32 or bf16) to 4-bit codes [rows, K/2] and scales (uint8)."""
     _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
-    _check(lib().semmoe_mx4_quantize(_p(x), dtype_code(x), groups, group_rows, K, _p(codes), _p(scales),
+    _check(fast().semmoe_mx4_quantize(x, dtype_code(x), groups, group_rows, K, codes, scales,
                                      _stream(stream)))
 
 
 def semmoe_mx4_dequantize(codes, scales, groups, group_rows, K, out, stream=None):
     """The values that codes and scales stand for, in out's type (fp32 or bf16; exact in both)."""
     _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
-    _check(lib().semmoe_mx4_dequantize(_p(codes), _p(scales), groups, group_rows, K, _p(out), dtype_code(out),
+    _check(fast().semmoe_mx4_dequantize(codes, scales, groups, group_rows, K, out, dtype_code(out),
                                        _stream(stream)))
 
 
 def semmoe_mx4_quantize_rows(x, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes, scales, stream=None):
     """Token rows x [T, K] quantised into expert order (see include/semmoe.h)."""
     _mx4(codes, scales, P, K, P // 128 + E, "codes")
-    _check(lib().semmoe_mx4_quantize_rows(_p(x), dtype_code(x), T, K, _p(pair_to_sorted), k_max, P,
-                                          _p(expert_offsets), E, _p(codes), _p(scales), _stream(stream)))
+    _check(fast().semmoe_mx4_quantize_rows(x, dtype_code(x), T, K, pair_to_sorted, k_max, P,
+                                          expert_offsets, E, codes, scales, _stream(stream)))
 
 
 def semmoe_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream=None):
     """4-bit rows [P, K] times their expert's 4-bit matrix [N, K] into out [P, N] (fp32 or bf16)."""
     _mx4(a, a_scales, P, K, P // 128 + E, "a")
     _mx4(b, b_scales, E * N, K, E * (-(-N // 128)), "b")
-    _check(lib().semmoe_mx4_grouped_gemm(_p(a), _p(a_scales), _p(expert_offsets), _p(phys_to_expert), _p(b),
-                                         _p(b_scales), P, E, N, K, _p(out), dtype_code(out), _stream(stream)))
+    _check(fast().semmoe_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b,
+                                         b_scales, P, E, N, K, out, dtype_code(out), _stream(stream)))
 
 
 def semmoe_mx4_grouped_ffn_workspace_size(P, E, I) -> int:
-    return lib().semmoe_mx4_grouped_ffn_workspace_size(P, E, I)
+    return fast().semmoe_mx4_grouped_ffn_workspace_size(P, E, I)
 
 
 def semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I,
@@ -405,20 +416,20 @@ def semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13
     _mx4(w13, w13_scales, 2 * E * I, H, 2 * E * (-(-I // 128)), "w13")
     _mx4(w2, w2_scales, E * H, I, E * (-(-H // 128)), "w2")
     _want(y_perm, torch.bfloat16, P * H, "y_perm")
-    _check(lib().semmoe_mx4_grouped_ffn(_p(x), _p(x_scales), _p(expert_offsets), _p(phys_to_expert), _p(w13),
-                                        _p(w13_scales), _p(w2), _p(w2_scales), P, E, H, I, _p(y_perm), _p(ws),
+    _check(fast().semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13,
+                                        w13_scales, w2, w2_scales, P, E, H, I, y_perm, ws,
                                         ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def semmoe_selftest_bounded_wait(stream=None):
     """Launch the wait that can never complete (it gives up after 2 s and sets
     the timeout bit); see include/semmoe.h."""
-    _check(lib().semmoe_selftest_bounded_wait(_stream(stream)))
+    _check(fast().semmoe_selftest_bounded_wait(_stream(stream)))
 
 
 def semmoe_selftest_fused_ready_wait(x_perm, w13, w2, P, H, I, y_perm, ws, stream=None):
     """Run the one-launch grouped FFN with GEMM2's readiness waits made
     unreachable (each gives up after 2 s and sets the timeout bit); see
     include/semmoe.h."""
-    _check(lib().semmoe_selftest_fused_ready_wait(_p(x_perm), _p(w13), _p(w2), P, H, I, _p(y_perm), _p(ws),
+    _check(fast().semmoe_selftest_fused_ready_wait(x_perm, w13, w2, P, H, I, y_perm, ws,
                                                   ws.numel() * ws.element_size(), _stream(stream)))

@@ -3,7 +3,8 @@
     python -m token_expert_routing_gb300.build [-v]
 
 Each .cu file is compiled by its own nvcc process (in parallel) into
-``_build/``; the objects are linked into ``libsemmoe.so`` next to this file.
+``_build/``; the objects are linked into ``libsemmoe.so`` next to this file, and the
+Python entry points (binding.cpp) into ``_fast`` beside it.
 Objects are rebuilt when their source or a header is newer.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsemmoe.so")
+FAST = os.path.join(PKG, "_fast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))  # the Python entry points
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -70,6 +73,15 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    binding = os.path.join(CSRC, "binding.cpp")
+    if _stale(FAST, [binding, os.path.join(INCLUDE, "semmoe.h")]):
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", binding, "-o", FAST, "-I" + INCLUDE,
+               "-I" + sysconfig.get_paths()["include"], "-L" + PKG, "-l:libsemmoe.so", "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the binding did not build:\n{r.stdout}\n{r.stderr}")
     return LIB
 
 
