@@ -237,6 +237,7 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
  * renorm      non-zero: weights sum to `scale`
  * scale       finite
  * other arguments as semmoe_route; ws of semmoe_route_select_workspace_size() bytes
+ *             (may be NULL when that size is 256)
  * Limits: 1 <= E <= 256, 1 <= k_max <= topk_group * E / n_group.
  */
 enum { SEMMOE_SCORE_SIGMOID = 0, SEMMOE_SCORE_SOFTMAX = 1 };

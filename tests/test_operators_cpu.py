@@ -42,8 +42,9 @@ def test_select_refusals(lib, kw, word):
 
 def test_select_needs_its_workspace_and_nothing_for_no_tokens(lib):
     assert select(lib, T=0) == 0
-    need = lib.semmoe_route_select_workspace_size(64, 64, 16, 1, 1)
-    rc = lib.semmoe_route_select(P, 1, P, 1, None, None, 0, None, 1, 1, 1, 1, 1.0, None, 2, 64, 64, 16, 2, P, P, None, P,
+    assert lib.semmoe_route_select_workspace_size(64, 64, 300, 1, 1) == 0
+    need = lib.semmoe_route_select_workspace_size(6400, 64, 16, 1, 1)
+    rc = lib.semmoe_route_select(P, 1, P, 1, None, None, 0, None, 1, 1, 1, 1, 1.0, None, 2, 6400, 64, 16, 2, P, P, None, P,
                                  need - 1, None)
     assert rc == 1 and "workspace" in _err(lib)
 

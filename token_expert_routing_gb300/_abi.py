@@ -250,16 +250,21 @@ def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_
     SEMMOE_SCORE_SIGMOID or SEMMOE_SCORE_SOFTMAX, ``bias`` [E] fp32 or None; ``ws``
     defaults to a fresh workspace of the size the library asks for; ``w_dtype``
     and ``pair_counts`` as in semmoe_route."""
-    _want(bias, torch.float32, E, "bias")
+    if bias is not None:
+        _want(bias, torch.float32, E, "bias")
     xd = dtype_code(x) if x is not None else SEMMOE_F32
     wd = w_dtype if w_dtype is not None else (dtype_code(w_router) if w_router is not None else SEMMOE_F32)
-    if ws is None:
-        n = semmoe_route_select_workspace_size(T, max(H, 1), E, xd, wd)
-        ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
+    n = 0
+    if ws is not None:
+        n = ws.numel() * ws.element_size()
+    elif logits_in is None:
+        n = fast().semmoe_route_select_workspace_size(T, max(H, 1), E, xd, wd)
+        if n > 256:
+            ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
     _check(fast().semmoe_route_select(x, xd, w_router, wd, logits_in, logits_out, score, bias,
                                      n_group, topk_group, group_top, int(bool(renorm)), float(scale),
                                      k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w,
-                                     pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
+                                     pair_counts, ws, n, _stream(stream)))
 
 
 def semmoe_affinity_lookup(token_ids, lut, V, R, T, pred_rank, stream=None):

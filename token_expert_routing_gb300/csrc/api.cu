@@ -194,7 +194,9 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
 }
 
 size_t semmoe_route_select_workspace_size(int T, int H, int E, int x_dtype, int w_dtype) {
-  return semmoe_route_hier_workspace_size(T, H, E, x_dtype, w_dtype);  // logits for a selection kernel of their own
+  if (T < 0 || H < 1 || E < 1 || E > 256 || !valid_dtype(x_dtype) || !valid_router_dtype(w_dtype, x_dtype, H)) return 0;
+  const size_t b = route_select_ws_bytes(T, H, E, x_dtype, w_dtype);
+  return b > 0 ? b : 256;
 }
 
 int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_dtype, const float* logits_in,
@@ -225,7 +227,7 @@ int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_
             w_dtype);
     REQUIRE(H >= 1, "%s: H = %d < 1", fn, H);
     REQUIRE(aligned(x, 16) && aligned(w_router, 16), "%s: x and w_router must be 16-byte aligned", fn);
-    const size_t need = route_hier_ws_bytes(T, H, E, x_dtype, w_dtype);
+    const size_t need = route_select_ws_bytes(T, H, E, x_dtype, w_dtype);
     REQUIRE(need == 0 || (ws != nullptr && aligned(ws, 256) && ws_bytes >= need),
             "%s: workspace null, not 256-byte aligned or below %zu bytes", fn, need);
   } else {

@@ -69,13 +69,14 @@ struct Select {
   int n_group, topk_group, group_top, renorm;
   float scale;
 };
+size_t route_select_ws_bytes(int T, int H, int E, int x_dtype, int w_dtype);
 cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w_dtype, const float* logits_in,
                                 float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform, int T,
                                 int H, int E, int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts,
                                 void* ws, cudaStream_t s);
 // The product and the choice in one kernel, a cluster of CTAs per token tile
 // (route_tc.cu); route_select_cl_slices gives the slices of H (0: not applicable).
-int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype);
+int route_select_cl_slices(int T, int H, int E, int w_dtype);
 cudaError_t launch_route_select_cl(const void* x, const void* w, int w_dtype, int T, int H, int E, int k_max, int KS,
                                    float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform,
                                    int32_t* topk_idx, float* topk_w, int32_t* counts, int count_stride, void* split,

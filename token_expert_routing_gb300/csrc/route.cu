@@ -698,6 +698,13 @@ cudaError_t launch_route_hier(const void* x, int x_dtype, const void* w, int w_d
   return cudaGetLastError();
 }
 
+// The one-launch form keeps its logits in shared memory: only an fp32 weight's split is left.
+size_t route_select_ws_bytes(int T, int H, int E, int x_dtype, int w_dtype) {
+  if (route_on_tensor_cores(x_dtype, H) && route_select_cl_slices(T, H, E, w_dtype) >= 1)
+    return route_tc_split_bytes(H, E, w_dtype);
+  return route_hier_ws_bytes(T, H, E, x_dtype, w_dtype);
+}
+
 cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w_dtype, const float* logits_in,
                                 float* logits_out, const Select& sel, const int32_t* kpt, int k_uniform, int T,
                                 int H, int E, int k_max, int32_t* topk_idx, float* topk_w, int32_t* pair_counts,
@@ -705,11 +712,11 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
   if (T == 0) return cudaSuccess;
   cudaError_t e;
   if (logits_in == nullptr && route_on_tensor_cores(x_dtype, H)) {  // product and choice in one kernel
-    const int ks = route_select_cl_slices(T, H, E, k_max, w_dtype);
+    const int ks = route_select_cl_slices(T, H, E, w_dtype);
     if (ks >= 1)
       return launch_route_select_cl(x, w, w_dtype, T, H, E, k_max, ks, logits_out, sel, kpt, k_uniform, topk_idx,
                                     topk_w, pair_counts, pair_counts != nullptr ? pair_counts_stride(T) : 0,
-                                    static_cast<unsigned char*>(ws) + route_partials_bytes(T, H, E, w_dtype), s);
+                                    ws, s);
   }
   int ks = 1;
   e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s, true);

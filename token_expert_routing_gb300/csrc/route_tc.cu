@@ -1047,7 +1047,7 @@ static int select_pass(int E, int w_dtype) {
 // Slices of H for the choice by score, 0 where the split-K product and a
 // selection kernel take the call: the largest KS in {1, 2, 4, 8} with one CTA per SM for
 // every (tile, pass, slice), at most 8 CTAs per cluster and at least 2 k-blocks per slice.
-int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype) {
+int route_select_cl_slices(int T, int H, int E, int w_dtype) {
   const int EC = select_pass(E, w_dtype), n_pass = (E + EC - 1) / EC;
   const long long tiles = (T + BM - 1) / BM;
   const int kb_all = (H + BK - 1) / BK;
@@ -1056,7 +1056,7 @@ int route_select_cl_slices(int T, int H, int E, int k_max, int w_dtype) {
   // 2048 (16 clusters of 8 CTAs do not fit at once); 256, bf16: 17.2 / 21.6 at 1024; four
   // passes (256, fp32): 30.0 / 30.3 at 256, 30.1 / 26.9 at 1024.
   if (tiles > 8 || n_pass > 2) return 0;
-  const size_t words = 2 * (size_t)BM * (EC + 4) + (size_t)(kClThreads / 32 - 2) * select_scratch(E, E, k_max);
+  const size_t words = 2 * (size_t)BM * (EC + 4) + (size_t)(kClThreads / 32 - 2) * select_scratch(E, E, E);
   if (words * 4 > stage_budget(1)) return 0;
   int ks = 0;
   for (int c = 1; c <= 8; c *= 2)
