@@ -13,10 +13,10 @@
 //   warps 2..9  epilogue, two groups of four
 // A tile has two halves of 128 columns (SwiGLU: gate and up) with an accumulator
 // each, and TMEM holds three: the first half of a tile always finds one free, and the
-// second half the one that the epilogue of the tile before leaves first.  To give
-// that epilogue time, stages go in pairs: first half of both, then second half of
-// both.  (Two accumulators of 256 columns would leave no TMEM for the scales;
-// sharing some columns left the tensor cores idle for a round trip per tile.)
+// second half the one that the epilogue of the tile before leaves first; until it
+// has, the first halves of up to three stages go ahead.  (Two accumulators of 256 columns
+// would leave no TMEM for the scales; sharing some columns left the tensor cores idle
+// for a round trip per tile.)
 // A stage's scales have TMEM columns of their own, so they are overwritten only after
 // the commit of the MMAs that read them.
 //
@@ -314,58 +314,63 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   } else if (warp == 1) {
     uint32_t it = 0, half = 0;  // stage position; half tiles begun
     bool ok = true;
+    // descriptors of stage 0; their address field counts 16 bytes
+    const uint64_t desc_a = sw128_desc(smem_u32(ring)), desc_b = sw128_desc(smem_u32(ring) + A_BYTES),
+                   desc_s = scale_desc(smem_u32(ring) + A_BYTES + B_BYTES);
     auto stage_mma = [&](uint32_t pos, int kb, int h, uint32_t acc) {  // one half's MMAs of a stage
       const uint32_t s = pos % STAGES;
-      const uint32_t sa = smem_u32(ring) + s * STAGE_BYTES, sb = sa + A_BYTES + h * (B_BYTES / 2);
-      const uint32_t ta = tmem + SC_COL + s * SC_COLS, tb = ta + 8 + 8 * h;
+      const uint64_t da = desc_a + s * (STAGE_BYTES / 16), db = desc_b + s * (STAGE_BYTES / 16) + h * (B_BYTES / 32);
+      const uint32_t ta = tmem + SC_COL + s * SC_COLS, tb = ta + 8 + 8 * h, d = tmem + acc * HN;
       const int left = pr.K - kb * BK;  // columns past K are zeros, their scales undefined
 #pragma unroll
       for (int k = 0; k < BK / UK; ++k)
         if (k * UK < left)
-          mma_mx4(tmem + acc * HN, sw128_desc(sa + k * UK / 2), sw128_desc(sb + k * UK / 2),
-                  idesc_mx4(BM, HN, (uint32_t)(k & 1) * 2), ta + 4 * (k / 2), tb + 4 * (k / 2), (kb | k) != 0);
+          mma_mx4(d, da + k * (UK / 32), db + k * (UK / 32), idesc_mx4(BM, HN, (uint32_t)(k & 1) * 2), ta + 4 * (k / 2),
+                  tb + 4 * (k / 2), (kb | k) != 0);
     };
     for (int tile = unit0; ok && tile < total; tile += units, half += 2) {
       const uint32_t a0 = half % ACCS, a1 = (half + 1) % ACCS;
       // the epilogue has left the accumulator (three halves ago)
       if (half >= ACCS && !wait_for(&sh.tempty[a0], (half / ACCS - 1) & 1, abort_flag)) break;
-      for (int kb = 0; kb < kb_n; kb += 2, it += 2) {
-        const int n = kb_n - kb < 2 ? 1 : 2;  // the last pair may be one stage
-        for (int i = 0; ok && i < n; ++i) {
-          const uint32_t s = (it + i) % STAGES;
-          if (!wait_for(&sh.full[s], ((it + i) / STAGES) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          if (elect_one()) {
-            const uint32_t ss = smem_u32(ring) + s * STAGE_BYTES + A_BYTES + B_BYTES, ta = tmem + SC_COL + s * SC_COLS;
-#pragma unroll
-            for (int c = 0; c < 6; ++c) copy_scales(ta + 4 * c, scale_desc(ss + c * kTileBytes));
-            stage_mma(it + i, kb + i, 0, a0);
-            if (kb + i == kb_n - 1) commit(&sh.tfull[a0]);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (kb == 0 && half + 1 >= ACCS && !wait_for(&sh.tempty[a1], ((half + 1) / ACCS - 1) & 1, abort_flag)) {
+      int done1 = 0;                // stages whose second half is issued
+      bool free1 = half + 1 < ACCS; // the second half's accumulator is free
+      for (int kb = 0; kb < kb_n; ++kb) {
+        const uint32_t pos = it + kb, s = pos % STAGES;
+        if (!wait_for(&sh.full[s], (pos / STAGES) & 1, abort_flag)) {
           ok = false;
           break;
         }
         fence_after();
         if (elect_one()) {
-          for (int i = 0; i < n; ++i) {
-            stage_mma(it + i, kb + i, 1, a1);
-            commit(&sh.empty[(it + i) % STAGES]);
-          }
-          if (kb + n == kb_n) commit(&sh.tfull[a1]);
+          const uint64_t ds = desc_s + s * (STAGE_BYTES / 16);
+          const uint32_t ta = tmem + SC_COL + s * SC_COLS;
+#pragma unroll
+          for (int c = 0; c < 6; ++c) copy_scales(ta + 4 * c, ds + c * (kTileBytes / 16));
+          stage_mma(pos, kb, 0, a0);
+          if (kb == kb_n - 1) commit(&sh.tfull[a0]);
         }
         __syncwarp();
-        if (n == 1) {
-          it += 1;
-          break;
+        if (!free1) {  // first halves go on while the epilogue still reads it, as far as the ring reaches
+          const uint32_t ph = ((half + 1) / ACCS - 1) & 1;
+          if (kb + 1 < kb_n && kb + 1 < STAGES - 1) free1 = __any_sync(0xffffffffu, mbar_try_wait(&sh.tempty[a1], ph));
+          else free1 = ok = wait_for(&sh.tempty[a1], ph, abort_flag);
+          if (!free1) {
+            if (!ok) break;
+            continue;
+          }
+          fence_after();
         }
+        if (elect_one()) {
+          for (int i = done1; i <= kb; ++i) {
+            stage_mma(it + i, i, 1, a1);
+            commit(&sh.empty[(it + i) % STAGES]);
+          }
+          if (kb == kb_n - 1) commit(&sh.tfull[a1]);
+        }
+        done1 = kb + 1;
+        __syncwarp();
       }
+      it += kb_n;
     }
     if (elect_one()) commit(&sh.done);
     __syncwarp();

@@ -423,25 +423,40 @@ hier_topk_kernel(const float* __restrict__ logits, int ks, float* __restrict__ l
 // Expert choice by score (select.cuh) of precomputed logits, the sum of ks
 // partial [T, E] slices: one warp per token.
 template <int NPER>  // experts per lane: E <= 32 * NPER
-__global__ void __launch_bounds__(kTopkWarps * 32)
+__global__ void __launch_bounds__(kTopkWarps * 32, NPER <= 4 ? 6 : 4)
 select_kernel(const float* __restrict__ logits, int ks, float* __restrict__ logits_out, Select sel,
               const int32_t* __restrict__ k_per_token, int k_uniform, int T, int E, int k_max,
               int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, PairCounts pc) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   pdl_trigger();
-  const int warp = threadIdx.x / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float* scratch = reinterpret_cast<float*>(smem_raw) + warp * select_scratch(E, sel.n_group, k_max);
-  const int t = blockIdx.x * kTopkWarps + warp;
-  if (t >= T) return;
   pdl_wait();
-  const int kt = warp_budget(k_per_token, k_uniform, k_max, t);
-  float bias[NPER], v[NPER];
+  float bias[NPER];
   const int bits = load_bias<NPER>(sel, E, bias);
   if (bits) flag(bits);
-  warp_load_logits<NPER>(logits + (size_t)t * E, ks, (size_t)T * E,
-                         logits_out != nullptr ? logits_out + (size_t)t * E : nullptr, E, v);
-  warp_choose<NPER>(v, bias, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max, topk_w + (size_t)t * k_max,
-                    [&](int e) { count_pick(pc, e, t); });
+  for (int t = blockIdx.x * kTopkWarps + warp; t < T; t += gridDim.x * kTopkWarps) {
+    const int kt = warp_budget(k_per_token, k_uniform, k_max, t);
+    float v[NPER];
+    float* lo = logits_out != nullptr ? logits_out + (size_t)t * E : nullptr;
+    if (ks == 1 && lo == nullptr) {  // nothing to add or to copy
+      const float* row = logits + (size_t)t * E;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        v[i] = lane + 32 * i < E ? row[lane + 32 * i] : -INFINITY;
+        if (lane + 32 * i < E && !isfinite(v[i])) {
+          finite = false;
+          v[i] = -INFINITY;
+        }
+      }
+      if (!finite) flag(SEMMOE_DEVERR_NONFINITE);
+    } else {
+      warp_load_logits<NPER>(logits + (size_t)t * E, ks, (size_t)T * E, lo, E, v);
+    }
+    warp_choose<NPER>(v, bias, E, kt, k_max, sel, scratch, topk_idx + (size_t)t * k_max, topk_w + (size_t)t * k_max,
+                      [&](int e) { count_pick(pc, e, t); });
+  }
 }
 
 __global__ void affinity_lookup_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ lut,
@@ -725,7 +740,10 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
   e = pair_counts_begin(pair_counts, T, E, &pc, s);
   if (e != cudaSuccess) return e;
   const size_t sm = (size_t)kTopkWarps * select_scratch(E, sel.n_group, k_max) * sizeof(float);
-  const dim3 grid((T + kTopkWarps - 1) / kTopkWarps), block(kTopkWarps * 32);
+  // one warp per token until the GPU is full, then a few tokens each (the kernel is bound by
+  // instructions, and the setup is then shared)
+  const int full = 6 * sm_count(), need = (T + kTopkWarps - 1) / kTopkWarps;
+  const dim3 grid(need < full ? need : full), block(kTopkWarps * 32);
   auto run = [&](auto kern) {
     return launch_kernel(kern, grid, block, sm, s, 1, true, logits_in, ks, logits_out, sel, kpt, k_uniform, T, E, k_max,
                          topk_idx, topk_w, pc);
