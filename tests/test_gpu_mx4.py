@@ -266,3 +266,50 @@ def test_empty_inputs_enqueue_nothing():
     abi().semmoe_mx4_quantize(e32, 3, 0, 64, e8, e8)
     abi().semmoe_mx4_dequantize(e8, e8, 3, 0, 64, e32)
     assert abi().semmoe_kernel_launches() == n0
+
+
+def test_quantize_past_2_31_elements():
+    """Element offsets pass 32 bits: the last rows of 70000 x 32768 values."""
+    rows, K = 70000, 32768
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-130:] = torch.randn(130, K, device="cuda").to(torch.bfloat16)
+    codes = torch.empty(rows, K // 2, **u8)
+    scales = torch.empty(abi().semmoe_mx4_scales_size(rows, K, 1), **u8)
+    abi().semmoe_mx4_quantize(x, 1, rows, K, codes, scales)
+    ref_code, ref_e = oracle.mx4_encode(np_(x[-130:]))
+    np.testing.assert_array_equal(unpack(codes[-130:]), ref_code)
+    r, b = np.arange(rows - 130, rows)[:, None], np.arange(K // 32)[None, :]
+    at = torch.from_numpy(scale_at(0, r, b, K)).cuda()
+    np.testing.assert_array_equal(np_(scales[at]), ref_e)
+    assert not codes[:-130].any()
+    abi().semmoe_mx4_dequantize(codes, scales, 1, rows, K, x)
+    np.testing.assert_array_equal(np_(x[-130:]), oracle.mx4_values(ref_code, ref_e))
+
+
+def test_refuses_what_is_not_dense():
+    x = torch.zeros(8, 128, device="cuda")
+    codes, scales = torch.empty(8, 32, **u8), torch.empty(1024, **u8)
+    with pytest.raises(ValueError, match="contiguous"):
+        abi().semmoe_mx4_quantize(x[:, :64], 1, 8, 64, codes, scales)
+    with pytest.raises(ValueError, match="CUDA"):
+        abi().semmoe_mx4_quantize(x.cpu(), 1, 8, 64, codes, scales)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_grouped_gemm_random_groups(seed):
+    """Random tables: skewed, empty and one-row groups, experts in any order, ragged N and K."""
+    rng = np.random.default_rng(900 + seed)
+    E = int(rng.integers(1, 40))
+    count = np.maximum(rng.geometric(rng.uniform(0.005, 0.3), E) - 1, 0)
+    count[rng.random(E) < 0.3] = 0
+    count[rng.integers(E)] += 1
+    count = count.tolist()
+    N, K, P = 8 * int(rng.integers(1, 70)), 32 * int(rng.integers(1, 40)), sum(count)
+    (a, a_sc, b, b_sc), av, bv = operands(rng, P, E, N, K, count)
+    pe, off = rng.permutation(E), np.concatenate([[0], np.cumsum(count)])
+    y = torch.full((P + 1, N), 77.0, device="cuda")
+    abi().semmoe_mx4_grouped_gemm(a, a_sc, cuda(off, torch.int32), cuda(pe, torch.int32), b, b_sc, P, E, N, K, y[:P])
+    assert abi().semmoe_check_errors() == 0
+    size = oracle.mx4_grouped_product(np.abs(av), np.abs(bv), off, pe)
+    assert (np.abs(np_(y[:P]) - oracle.mx4_grouped_product(av, bv, off, pe)) <= K * 2.0 ** -23 * size).all()
+    assert (np_(y[P]) == 77.0).all()

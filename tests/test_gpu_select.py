@@ -187,3 +187,31 @@ def test_select_with_its_router_product(T, H, E, xd, wd):
     abi().semmoe_route_select(x, wr, None, None, abi().SEMMOE_SCORE_SIGMOID, b, 4, 2, 2, True, 1.0, None, k_max, T, H, E,
                               k_max, idx2, w2)
     assert torch.equal(idx, idx2) and torch.equal(w, w2)
+
+
+def test_select_on_another_stream_and_in_place_logits():
+    """The calls run on the stream they are given; logits routed as given may be written onto themselves."""
+    rng = np.random.default_rng(21)
+    T, E, k = 2000, 64, 4
+    l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    idx, w = torch.empty(T, k, **i32), torch.empty(T, k, device="cuda")
+    want = oracle.route_select(np_(l), "softmax", np.full(T, k), k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    before = l.clone()
+    abi().semmoe_route_select(None, None, l, l, abi().SEMMOE_SCORE_SOFTMAX, None, 1, 1, 1, True, 1.0, None, k, T, 0, E, k,
+                              idx, w, stream=side)
+    side.synchronize()
+    assert torch.equal(l, before)
+    np.testing.assert_array_equal(np_(idx), want[0])
+    np.testing.assert_allclose(np_(w), want[1], rtol=W_RTOL)
+
+
+def test_select_flags_a_budget_out_of_range():
+    from token_expert_routing_gb300 import SemMoEError
+    l = np.tile(np.arange(8, dtype=np.float32), (4, 1))
+    idx, _, _ = run(l, "sigmoid", [1, 0, 9, 2], 3)
+    with pytest.raises(SemMoEError) as e:
+        abi().semmoe_check_errors()
+    assert e.value.bits == abi().SEMMOE_DEVERR_K
+    assert idx.tolist() == [[7, -1, -1], [7, -1, -1], [7, 6, 5], [7, 6, -1]]

@@ -120,3 +120,26 @@ def test_binding_refuses_other_types_and_short_buffers():
         _abi.semmoe_mx4_dequantize(codes, scales[:100], 1, 4, 64, torch.zeros(4, 64))
     with pytest.raises(ValueError, match="codes"):
         _abi.semmoe_mx4_quantize(torch.zeros(4, 64), 1, 4, 64, codes.to(torch.int32), scales)
+
+
+def test_compiled_entry_points_cover_the_abi_and_check_their_arguments():
+    """Every enqueuing call has its compiled entry; host tensors, wrong argument counts and
+    integers past 32 bits are refused before the library is called."""
+    from token_expert_routing_gb300 import _abi
+    fast = _abi.fast()
+    left = {"semmoe_last_error", "semmoe_version", "semmoe_kernel_launches", "semmoe_check_errors"}
+    for name, (_, args) in _abi.SIGNATURES.items():
+        if name in left:
+            continue
+        with pytest.raises(TypeError, match=f"expected {len(args)} arguments, got 0"):
+            getattr(fast, name)()
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        fast.semmoe_mx4_quantize(torch.zeros(4, 64), 0, 1, 4, 64, None, None, None)
+    with pytest.raises(OverflowError):
+        fast.semmoe_mx4_scales_size(1 << 31, 64, 1)
+    with pytest.raises(TypeError):
+        fast.semmoe_mx4_scales_size(1.5, 64, 1)
+    with pytest.raises(AttributeError):
+        fast.semmoe_mx4_quantize("x", 0, 1, 4, 64, None, None, None)
+    assert fast.semmoe_mx4_scales_size(128, 128, 1) == 1024
+    assert fast.semmoe_mx4_quantize(None, 0, 1, 4, 48, 256, 256, None) == _abi.SEMMOE_ERR_INVALID_ARG
