@@ -2,6 +2,9 @@
 // mx4.cuh).  Pure data movement: per value 2 or 4 bytes in and 17/32 of a byte
 // out, so the bound is HBM bandwidth; a lane takes 16 values of a row (two
 // 16-byte loads of bf16), two lanes share a block, eight one 128-column tile.
+// Measured (GB300): 180224 x 2048 bf16 to 4 bits 131 us and back 143 us (934 MB each: 7.1 and
+// 6.5 TB/s, at the rate of a plain copy; with 8 values a lane and a grid that fills the
+// GPU once 178 and 228 us); 16384 rows of 2048 into 131072 sorted rows 38 us (210 MB, 5.5 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"

@@ -14,6 +14,10 @@
 // Weights: s_j, or s_j over the sum of the picks'; where that sum is close to
 // underflow, exp(log s_j - max log s) over its sum (log sigmoid(l) = min(l, 0) -
 // log1p(exp(-|l|))), so that picks whose scores all underflow still share one.
+// Bound by instructions where the GPU is full of tokens (16384 tokens, 128 experts, 8
+// picks: 69% of the issue slots, 690 instructions a token, 16 us beside 20 us of the
+// product) and by the latency of its steps where it is not (one token, 256 experts in 8
+// groups: about 5 us of the call's 14).
 #pragma once
 
 #include <math.h>
