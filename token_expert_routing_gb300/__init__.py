@@ -7,7 +7,7 @@ token-id affinity lookup and remote-activation count, stable permute by
 parallelism and MoE-Prism's per-request routing budgets; also a router that
 chooses by sigmoid or softmax score with a bias and groups, and experts on 4-bit
 microscaled weights and rows.  This package holds
-the library sources (``csrc/``), its build script, the ctypes binding
+the library sources (``csrc/``), its build script, the binding
 (``_abi``) and a thin layer driver (``layer``).
 """
 from . import _abi  # noqa: F401
