@@ -121,40 +121,56 @@ __global__ void __launch_bounds__(kThreads)
 mx4_quantize_rows_kernel(const T* __restrict__ x, int n_tok, int K, const int32_t* __restrict__ pair_to_sorted,
                          int k_max, int P, const int32_t* __restrict__ expert_offsets, int E,
                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  __shared__ int off[kMaxE + 1], first[kMaxE], scan[kThreads];
+  __shared__ int off[kMaxE + 1], first[kMaxE];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x % 32;
-  // row tile at which each expert's rows start
-  for (int e = threadIdx.x; e <= E; e += kThreads) off[e] = expert_offsets[e];
-  __syncthreads();
-  int mine = 0;
-  if ((int)threadIdx.x < E) {
-    const int lo = off[threadIdx.x], hi = off[threadIdx.x + 1];
-    if (lo < 0 || hi < lo || hi > P) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
-    else mine = row_tiles(hi - lo);
+  Raw<T> v[kBatch];
+  auto load = [&](int t, int c0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int c = c0 + i * kSpan + lane * 16;
+      v[i] = Raw<T>{};
+      if (c < K) load16(x + (size_t)t * K + c, v[i]);
+    }
+  };
+  const int t_first = blockIdx.x * kWarps + threadIdx.x / 32;
+  if (t_first < n_tok) load(t_first, 0);  // in flight beside the offsets
+  if (threadIdx.x < 32) {  // row tile at which each expert's rows start, 8 experts per lane
+    int o[9], cnt[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) o[i] = lane * 8 + i <= E ? expert_offsets[lane * 8 + i] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      cnt[i] = 0;
+      if (e < E) {
+        off[e] = o[i];
+        if (e == E - 1) off[E] = o[i + 1];
+        if (o[i] < 0 || o[i + 1] < o[i] || o[i + 1] > P) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
+        else cnt[i] = row_tiles(o[i + 1] - o[i]);
+      }
+      sum += cnt[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += u;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (lane * 8 + i < E) first[lane * 8 + i] = run;
+      run += cnt[i];
+    }
   }
-  scan[threadIdx.x] = mine;
-  __syncthreads();
-  for (int d = 1; d < kThreads; d <<= 1) {
-    const int v = (int)threadIdx.x >= d ? scan[threadIdx.x - d] : 0;
-    __syncthreads();
-    scan[threadIdx.x] += v;
-    __syncthreads();
-  }
-  if ((int)threadIdx.x < E) first[threadIdx.x] = scan[threadIdx.x] - mine;
   __syncthreads();
   const int kc = col_tiles(K);
   const int max_tiles = P / kTileRows + E;  // what the caller's scales hold
   for (int t = blockIdx.x * kWarps + threadIdx.x / 32; t < n_tok; t += gridDim.x * kWarps) {
     for (int c0 = 0; c0 < K; c0 += kBatch * kSpan) {
-      Raw<T> v[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int c = c0 + i * kSpan + lane * 16;
-        v[i] = Raw<T>{};
-        if (c < K) load16(x + (size_t)t * K + c, v[i]);
-      }
+      if (t != t_first || c0 > 0) load(t, c0);
       uint2 w[kBatch];
       uint32_t s[kBatch];
 #pragma unroll

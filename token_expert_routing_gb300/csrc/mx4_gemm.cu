@@ -119,9 +119,20 @@ __device__ __forceinline__ float swiglu(uint32_t gw, uint32_t uw) {
 struct RowTile {
   int row0, rows, expert;
 };
-// Tiles come in increasing order, so a role keeps the group `g` it is at.
-__device__ __forceinline__ RowTile decode_mtile(const Shared& sh, int& g, int mt) {
-  while (sh.tp[g + 1] <= mt) ++g;
+// Tiles come in increasing order, so a role keeps the group `g` it is at: the next tile
+// is a few groups on where groups are long, and anywhere after it where they are empty.
+__device__ __forceinline__ RowTile decode_mtile(const Shared& sh, int G, int& g, int mt) {
+  // the group: the first one with tp[g + 1] > mt
+  int steps = 4;
+  while (sh.tp[g + 1] <= mt && --steps) ++g;
+  if (steps == 0) {
+    int hi = G - 1;
+    while (g < hi) {
+      const int mid = (g + hi) >> 1;
+      if (sh.tp[mid + 1] > mt) hi = mid;
+      else g = mid + 1;
+    }
+  }
   const int row0 = sh.off[g] + (mt - sh.tp[g]) * BM, left = sh.off[g + 1] - row0;
   return RowTile{row0, left < BM ? left : BM, sh.pe[g]};
 }
@@ -205,17 +216,19 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   if (warp == 1) tmem_alloc(&sh.tmem_base, TMEM_COLS);
   if (!pr.early) pdl_wait();
   pdl_trigger();
-  for (int g = threadIdx.x; g <= G; g += blockDim.x) sh.off[g] = pr.offsets[g];
-  for (int g = threadIdx.x; g < G; g += blockDim.x) sh.pe[g] = pr.experts[g];
-  __syncthreads();
-  if (warp == 0) {  // exclusive prefix of row tiles per group, 8 groups per lane
-    int cnt[8], sum = 0;
+  if (warp == 0) {  // the tables, and the exclusive prefix of row tiles per group: 8 groups per lane
+    int off[9], cnt[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) off[i] = lane * 8 + i <= G ? pr.offsets[lane * 8 + i] : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
       int c = 0;
       if (g < G) {
-        const int lo = sh.off[g], hi = sh.off[g + 1], e = sh.pe[g];
+        const int lo = off[i], hi = off[i + 1], e = pr.experts[g];
+        sh.off[g] = lo;
+        sh.pe[g] = e;
+        if (g == G - 1) sh.off[G] = hi;
         if (lo < 0 || hi < lo || hi > pr.P) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
         else if (e < 0 || e >= pr.E) atomicOr(&g_err, SEMMOE_DEVERR_EXPERT);
         else c = row_tiles(hi - lo);
@@ -265,7 +278,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       RowTile rt;
     };
     auto begin = [&](Place& p) {
-      if (p.tile < total) p.rt = decode_mtile(sh, p.g, p.tile / n_tiles);
+      if (p.tile < total) p.rt = decode_mtile(sh, G, p.g, p.tile / n_tiles);
     };
     auto next = [&](Place& p) {
       if (++p.kb == kb_n) {
@@ -405,7 +418,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
     for (int tile = unit0; tile < total; tile += units, half += 2) {
       const int mt = tile / n_tiles, nt = tile % n_tiles;
-      const RowTile rt = decode_mtile(sh, g, mt);
+      const RowTile rt = decode_mtile(sh, G, g, mt);
       const int row0 = rt.row0, rows = rt.rows;
       if (GLU) {  // group w takes blocks w and w + 2 of 32 columns
         if (!wait_acc(half) || !wait_acc(half + 1)) break;
