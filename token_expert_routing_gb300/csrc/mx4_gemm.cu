@@ -26,7 +26,7 @@
 // 2048 x 1536: 53 us, 3.9 PFLOP/s; 45 us with no output stored, 42 with nothing loaded either.
 // 131072 rows x 768 x 2048 (537 MB of bf16 out): 130 us, 5.4 TB/s.  Pairs of CTAs
 // (cta_group::2, M256, 35 KB a stage and CTA, five in flight) were built and measured
-// slower, 61 us on the first and 177 us on the second: a stage's round trip between two
+// slower, 61 us on the first and 178 us on the second: a stage's round trip between two
 // SMs costs more than its smaller copies save.  Three stages of this form: 68 and 146 us.
 // Few rows per group: the weights' bytes, 64 experts of 2048 x 1408 and 384 rows in 22 us
 // (98 MB, 4.4 TB/s, of which some 7 us are the launch, the first loads and the last tiles).
