@@ -313,3 +313,44 @@ def test_grouped_gemm_random_groups(seed):
     size = oracle.mx4_grouped_product(np.abs(av), np.abs(bv), off, pe)
     assert (np.abs(np_(y[:P]) - oracle.mx4_grouped_product(av, bv, off, pe)) <= K * 2.0 ** -23 * size).all()
     assert (np_(y[P]) == 77.0).all()
+
+
+def test_rows_past_the_last_group_are_left_alone():
+    """P may be more than the groups hold: the rows past them are not written, here and by the quantisation."""
+    rng = np.random.default_rng(6)
+    count, N, K, P = [70, 0, 60], 136, 96, 150
+    (a, a_sc, b, b_sc), av, bv = operands(rng, P, 3, N, K, count + [20])
+    off = np.array([0, 70, 70, 130])
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((P, N), 77.0, dtype=dtype, device="cuda")
+        abi().semmoe_mx4_grouped_gemm(a, a_sc, cuda(off, torch.int32), cuda(np.arange(3), torch.int32), b, b_sc, P, 3, N, K, y)
+        assert (np_(y[130:]) == 77.0).all()
+        assert max_rel(np_(y[:130]), oracle.mx4_grouped_product(av[:130], bv, off, np.arange(3))) < 1e-2
+    x = torch.randn(P, 64, device="cuda")
+    codes, scales = torch.full((P, 32), 0x77, **u8), torch.empty(abi().semmoe_mx4_scales_size(P, 64, 3), **u8)
+    back = np.where(np.arange(P) < 130, np.arange(P), -1)
+    abi().semmoe_mx4_quantize_rows(x, P, 64, cuda(back, torch.int32), 1, P, cuda(off, torch.int32), 3, codes, scales)
+    assert abi().semmoe_check_errors() == 0
+    assert (np_(codes[130:]) == 0x77).all()
+    np.testing.assert_array_equal(unpack(codes[:130]), oracle.mx4_encode(np_(x[:130]))[0])
+
+
+def test_grouped_ffn_with_a_non_finite_row():
+    """A NaN or an infinity in a token's row makes that row's output NaN and no other's."""
+    rng = np.random.default_rng(12)
+    T, H, I, E = 140, 256, 96, 2
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    x[3, 7], x[139, 200] = float("nan"), float("inf")
+    w13, w2 = torch.randn(E, 2 * I, H, device="cuda").to(torch.bfloat16), torch.randn(E, H, I, device="cuda").to(torch.bfloat16)
+    size = abi().semmoe_mx4_scales_size
+    q13, s13, q2, s2 = (torch.empty(E * 2 * I * H // 2, **u8), torch.empty(size(2 * E * I, H, 2 * E), **u8),
+                        torch.empty(E * H * I // 2, **u8), torch.empty(size(E * H, I, E), **u8))
+    abi().semmoe_mx4_quantize(w13, 2 * E, I, H, q13, s13)
+    abi().semmoe_mx4_quantize(w2, E, H, I, q2, s2)
+    off = cuda(np.array([0, 130, 140]), torch.int32)
+    xq, xs, y = torch.empty(T, H // 2, **u8), torch.empty(size(T, H, E), **u8), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(abi().semmoe_mx4_grouped_ffn_workspace_size(T, E, I), **u8)
+    abi().semmoe_mx4_quantize_rows(x, T, H, cuda(np.arange(T), torch.int32), 1, T, off, E, xq, xs)
+    abi().semmoe_mx4_grouped_ffn(xq, xs, off, cuda(np.arange(E), torch.int32), q13, s13, q2, s2, T, E, H, I, y, ws)
+    bad = np.isnan(np_(y))
+    assert bad[[3, 139]].all() and not np.delete(bad, [3, 139], axis=0).any()

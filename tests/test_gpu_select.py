@@ -215,3 +215,23 @@ def test_select_flags_a_budget_out_of_range():
         abi().semmoe_check_errors()
     assert e.value.bits == abi().SEMMOE_DEVERR_K
     assert idx.tolist() == [[7, -1, -1], [7, -1, -1], [7, 6, 5], [7, 6, -1]]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_select_biases_of_the_lowest_float(score):
+    """The type's lowest value as a bias puts an expert last without switching it off: it is taken
+    when nothing else is left, before a group that is off, ties by index."""
+    l = np.tile(np.linspace(-2, 2, 16, dtype=np.float32), (3, 1))
+    low = np.finfo(np.float32).min
+    b = np.full(16, low, dtype=np.float32)
+    b[:4] = -np.inf                       # group 0 off; groups 1 to 3 at the lowest value
+    idx, w, _ = run(l, score, [6] * 3, 6, b, 4, 2, 2)
+    assert (idx == np.arange(4, 10)).all() and np.isfinite(w).all() and (w > 0).all()
+    b[13] = 0.0                           # one ordinary expert: its group's sum is the lowest value's alone
+    idx, _, _ = run(l, score, [6] * 3, 6, b, 4, 2, 1)
+    assert (idx == [13, 4, 5, 6, 7, 12]).all()
+    b[4:] = -np.inf
+    b[13] = low
+    idx, w, _ = run(l, score, [2] * 3, 2, b, 4, 1, 2)
+    assert (idx == [13, -1]).all() and (w == [1.0, 0.0]).all()
+    assert abi().semmoe_check_errors() == 0

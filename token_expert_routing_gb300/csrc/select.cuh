@@ -20,6 +20,7 @@
 // groups: about 5 us of the call's 14).
 #pragma once
 
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -120,7 +121,8 @@ __device__ __forceinline__ void warp_choose(const float (&v)[NPER], const float 
         const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
         merge_top2(a, b, a2, b2);
       }
-      if (g < G && lane % L == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? a + b : a;
+      // a sum past the lowest float (biases of the type's lowest value) still beats a group that is off
+      if (g < G && lane % L == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? fmaxf(a + b, -FLT_MAX) : a;
     }
     __syncwarp();
     if (G <= 32) {  // lane g ranks group g
