@@ -128,6 +128,7 @@ def fast():
         except ImportError as e:
             raise RuntimeError("the compiled binding is missing: build it with "
                                "`python -m token_expert_routing_gb300.build`") from e
+        module.set_raise(_check)
         _fast = module
     return _fast
 
@@ -135,12 +136,6 @@ def fast():
 def _check(rc: int) -> None:
     if rc != SEMMOE_OK:
         raise SemMoEError(rc, lib().semmoe_last_error().decode())
-
-
-def _want(t, dtype, numel, what):
-    """Refuse a tensor of another type, or of fewer elements than the library will touch (None passes)."""
-    if t is not None and (t.dtype != dtype or t.numel() < numel):
-        raise ValueError(f"{what}: expected at least {numel} elements of {dtype}, got {t.numel()} of {t.dtype}")
 
 
 #: the current stream's handle without a Stream object (3 us of a call's host time on Grace), where torch has it
@@ -250,21 +245,13 @@ def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_
     SEMMOE_SCORE_SIGMOID or SEMMOE_SCORE_SOFTMAX, ``bias`` [E] fp32 or None; ``ws``
     defaults to a fresh workspace of the size the library asks for; ``w_dtype``
     and ``pair_counts`` as in semmoe_route."""
-    if bias is not None:
-        _want(bias, torch.float32, E, "bias")
-    xd = dtype_code(x) if x is not None else SEMMOE_F32
-    wd = w_dtype if w_dtype is not None else (dtype_code(w_router) if w_router is not None else SEMMOE_F32)
-    n = 0
-    if ws is not None:
-        n = ws.numel() * ws.element_size()
-    elif logits_in is None:
-        n = fast().semmoe_route_select_workspace_size(T, max(H, 1), E, xd, wd)
+    if ws is None and logits_in is None and x is not None and w_router is not None:
+        wd = w_dtype if w_dtype is not None else dtype_code(w_router)
+        n = fast().semmoe_route_select_workspace_size(T, max(H, 1), E, dtype_code(x), wd)
         if n > 256:
             ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
-    _check(fast().semmoe_route_select(x, xd, w_router, wd, logits_in, logits_out, score, bias,
-                                     n_group, topk_group, group_top, int(bool(renorm)), float(scale),
-                                     k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w,
-                                     pair_counts, ws, n, _stream(stream)))
+    fast().route_select(x, w_router, logits_in, logits_out, score, bias, n_group, topk_group, group_top, renorm, scale,
+                        k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w, pair_counts, ws, w_dtype, stream)
 
 
 def semmoe_affinity_lookup(token_ids, lut, V, R, T, pred_rank, stream=None):
@@ -373,41 +360,24 @@ def semmoe_mx4_scales_size(rows, K, groups) -> int:
     return fast().semmoe_mx4_scales_size(rows, K, groups)
 
 
-def _mx4(codes, scales, rows, K, row_tiles, what):
-    """Refuse codes and scales that do not hold ``rows`` rows of K values in ``row_tiles`` 128-row tiles."""
-    if codes.dtype is not torch.uint8 or codes.numel() < rows * (K // 2):
-        _want(codes, torch.uint8, rows * (K // 2), what)
-    if scales.dtype is not torch.uint8 or scales.numel() < row_tiles * ((K + 127) // 128) * 512:
-        _want(scales, torch.uint8, row_tiles * ((K + 127) // 128) * 512, what + " scales")
-
-
 def semmoe_mx4_quantize(x, groups, group_rows, K, codes, scales, stream=None):
     """x [groups * group_rows, K] (fp32 or bf16) to 4-bit codes [rows, K/2] and scales (uint8)."""
-    _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
-    _check(fast().semmoe_mx4_quantize(x, dtype_code(x), groups, group_rows, K, codes, scales,
-                                     _stream(stream)))
+    fast().mx4_quantize(x, groups, group_rows, K, codes, scales, stream)
 
 
 def semmoe_mx4_dequantize(codes, scales, groups, group_rows, K, out, stream=None):
     """The values that codes and scales stand for, in out's type (fp32 or bf16; exact in both)."""
-    _mx4(codes, scales, groups * group_rows, K, groups * (-(-group_rows // 128)), "codes")
-    _check(fast().semmoe_mx4_dequantize(codes, scales, groups, group_rows, K, out, dtype_code(out),
-                                       _stream(stream)))
+    fast().mx4_dequantize(codes, scales, groups, group_rows, K, out, stream)
 
 
 def semmoe_mx4_quantize_rows(x, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes, scales, stream=None):
     """Token rows x [T, K] quantised into expert order (see include/semmoe.h)."""
-    _mx4(codes, scales, P, K, P // 128 + E, "codes")
-    _check(fast().semmoe_mx4_quantize_rows(x, dtype_code(x), T, K, pair_to_sorted, k_max, P,
-                                          expert_offsets, E, codes, scales, _stream(stream)))
+    fast().mx4_quantize_rows(x, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes, scales, stream)
 
 
 def semmoe_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream=None):
     """4-bit rows [P, K] times their expert's 4-bit matrix [N, K] into out [P, N] (fp32 or bf16)."""
-    _mx4(a, a_scales, P, K, P // 128 + E, "a")
-    _mx4(b, b_scales, E * N, K, E * (-(-N // 128)), "b")
-    _check(fast().semmoe_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b,
-                                         b_scales, P, E, N, K, out, dtype_code(out), _stream(stream)))
+    fast().mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream)
 
 
 def semmoe_mx4_grouped_ffn_workspace_size(P, E, I) -> int:
@@ -417,13 +387,8 @@ def semmoe_mx4_grouped_ffn_workspace_size(P, E, I) -> int:
 def semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I,
                            y_perm, ws, stream=None):
     """SwiGLU experts on 4-bit rows and weights, y_perm [P, H] bf16."""
-    _mx4(x, x_scales, P, H, P // 128 + E, "x")
-    _mx4(w13, w13_scales, 2 * E * I, H, 2 * E * (-(-I // 128)), "w13")
-    _mx4(w2, w2_scales, E * H, I, E * (-(-H // 128)), "w2")
-    _want(y_perm, torch.bfloat16, P * H, "y_perm")
-    _check(fast().semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13,
-                                        w13_scales, w2, w2_scales, P, E, H, I, y_perm, ws,
-                                        ws.numel() * ws.element_size(), _stream(stream)))
+    fast().mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I,
+                           y_perm, ws, stream)
 
 
 def semmoe_selftest_bounded_wait(stream=None):

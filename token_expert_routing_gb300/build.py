@@ -23,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsemmoe.so")
 FAST = os.path.join(PKG, "_fast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))  # the Python entry points
+BINDING_OBJ = os.path.join(BUILD, "binding.o")
+CXX = os.environ.get("CXX", "g++")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -49,6 +51,19 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     headers = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     nvcc = _nvcc()
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    binding = None  # the Python entry points, compiled beside the CUDA sources
+    src = os.path.join(CSRC, "binding.cpp")
+    if _stale(BINDING_OBJ, [src, os.path.join(INCLUDE, "semmoe.h")]):
+        inc = os.path.join(torch_dir, "include")
+        cmd = [CXX, "-c", src, "-o", BINDING_OBJ, "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + inc,
+               "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + sysconfig.get_paths()["include"],
+               "-I" + os.path.join(os.path.dirname(os.path.dirname(nvcc)) or "/usr/local/cuda", "include"),
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        binding = subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True)
     flags = NVCC_FLAGS + list(extra_flags or [])
 
     def compile_one(src: str) -> str:
@@ -73,15 +88,18 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    binding = os.path.join(CSRC, "binding.cpp")
-    if _stale(FAST, [binding, os.path.join(INCLUDE, "semmoe.h")]):
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", binding, "-o", FAST, "-I" + INCLUDE,
-               "-I" + sysconfig.get_paths()["include"], "-L" + PKG, "-l:libsemmoe.so", "-Wl,-rpath,$ORIGIN"]
+    if binding is not None:
+        err = binding.communicate()[1]
+        if binding.returncode != 0:
+            raise RuntimeError(f"the binding did not build:\n{err}")
+    if _stale(FAST, [BINDING_OBJ]):
+        cmd = [CXX, "-shared", BINDING_OBJ, "-o", FAST, "-L" + PKG, "-l:libsemmoe.so", "-Wl,-rpath,$ORIGIN",
+               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"the binding did not build:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"the binding did not link:\n{r.stdout}\n{r.stderr}")
     return LIB
 
 
