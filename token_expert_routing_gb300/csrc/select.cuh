@@ -109,20 +109,22 @@ __device__ __forceinline__ void warp_choose(const float (&v)[NPER], const float 
   }
   if (grouped) {
     const int per_group = E / G;
-    int L = 1;  // lanes per group
-    if (G <= 32) L = 32 >> (32 - __clz(G - 1));
+    // an expert's group without an integer division: (e + 1/2) / per_group is at least 1/512 from a whole number
+    const float per_group_inv = 1.0f / (float)per_group;
+    auto group_of = [&](int e) { return __float2int_rz(((float)e + 0.5f) * per_group_inv); };
+    const int lsh = G <= 32 ? __clz(G - 1) - 27 : 0, L = 1 << lsh;  // lanes per group, a power of two
     __syncwarp();
-    for (int g0 = 0; g0 < G; g0 += 32 / L) {
-      const int g = g0 + lane / L;
+    for (int g0 = 0; g0 < G; g0 += 32 >> lsh) {
+      const int g = g0 + (lane >> lsh);
       float a = -INFINITY, b = -INFINITY;
       if (g < G)
-        for (int i = lane % L; i < per_group; i += L) merge_top2(a, b, ch[g * per_group + i], -INFINITY);
+        for (int i = lane & (L - 1); i < per_group; i += L) merge_top2(a, b, ch[g * per_group + i], -INFINITY);
       for (int o = L / 2; o > 0; o >>= 1) {
         const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
         merge_top2(a, b, a2, b2);
       }
       // a sum past the lowest float (biases of the type's lowest value) still beats a group that is off
-      if (g < G && lane % L == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? fmaxf(a + b, -FLT_MAX) : a;
+      if (g < G && (lane & (L - 1)) == 0) gs[g] = sel.group_top == 2 && b > -INFINITY ? fmaxf(a + b, -FLT_MAX) : a;
     }
     __syncwarp();
     if (G <= 32) {  // lane g ranks group g
@@ -136,14 +138,14 @@ __device__ __forceinline__ void warp_choose(const float (&v)[NPER], const float 
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
         const int e = lane + 32 * i;
-        if (e < E && !((keep >> (e / per_group)) & 1u)) c[i] = -INFINITY;
+        if (e < E && !((keep >> group_of(e)) & 1u)) c[i] = -INFINITY;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
         const int e = lane + 32 * i;
         if (e < E) {
-          const int g = e / per_group;
+          const int g = group_of(e);
           const float mine = gs[g];
           int rank = 0;
           for (int o = 0; o < G; ++o) rank += gs[o] > mine || (gs[o] == mine && o < g);
