@@ -538,6 +538,7 @@ route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
   __syncthreads();  // (the other CTAs see the receive barrier once past the cluster barrier before the copies)
   fence_after();
   const uint32_t tmem = sh.tmem_base;
+  if constexpr (SEL) pdl_wait();  // launched as a dependent: nothing in global memory is touched before
 
   if (warp == 0) {
     if (lane == 0) {  // TMA producer: this CTA's k-blocks
@@ -1011,7 +1012,7 @@ static cudaError_t launch_cl(const void* x, const void* w, int w_dtype, int T, i
   cudaError_t e = ensure_smem_limit(kern, (int)smem_bytes(1), smem_set[ki]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)CS;
   attr[0].val.clusterDim.y = 1;
@@ -1020,8 +1021,10 @@ static cudaError_t launch_cl(const void* x, const void* w, int w_dtype, int T, i
   cfg.blockDim = dim3(kClThreads);
   cfg.dynamicSmemBytes = smem_bytes(1);
   cfg.stream = s;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = sel != nullptr ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, mx, mw, T, H, E, EC, KS, CS, stages, kb_slice, logits_out, kpt, k_uniform,
                          k_max, topk_idx, topk_w, counts, count_stride, sel != nullptr ? *sel : Select{});
   if (e != cudaSuccess) return e;
