@@ -189,6 +189,29 @@ def test_select_with_its_router_product(T, H, E, xd, wd):
     assert torch.equal(idx, idx2) and torch.equal(w, w2)
 
 
+@pytest.mark.parametrize("T,H,E,wd", [(1300, 512, 256, torch.float32), (1025, 264, 200, torch.float32),
+                                      (2100, 1024, 100, torch.bfloat16)])
+def test_select_count_table_of_calls_in_a_row(T, H, E, wd):
+    rng = np.random.default_rng(T)
+    xs = [torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in range(4)]
+    wr = torch.from_numpy((rng.standard_normal((E, H)) / np.sqrt(H)).astype(np.float32)).to(wd).cuda()
+    k_max = 5
+    pc = torch.full((E, abi().semmoe_pair_counts_stride(T)), -3, **i32)  # one table and one workspace for all
+    ws = torch.empty(abi().semmoe_route_select_workspace_size(T, H, E, abi().SEMMOE_BF16, abi().dtype_code(wr)),
+                     dtype=torch.uint8, device="cuda")
+    out = []
+    for x in xs:
+        idx, w = torch.empty(T, k_max, **i32), torch.empty(T, k_max, device="cuda")
+        abi().semmoe_route_select(x, wr, None, None, abi().SEMMOE_SCORE_SOFTMAX, None, 1, 1, 1, True, 1.0, None, k_max,
+                                  T, H, E, k_max, idx, w, ws=ws, pair_counts=pc)
+        out.append((idx, pc.clone()))
+    assert abi().semmoe_check_errors() == 0
+    for x, (idx, counts) in zip(xs, out):
+        table = np.zeros(counts.shape, dtype=np.int64)
+        np.add.at(table, (np_(idx), np.repeat(np.arange(T)[:, None] // 128, k_max, axis=1)), 1)
+        np.testing.assert_array_equal(np_(counts), table)
+
+
 def test_select_on_another_stream_and_in_place_logits():
     """The calls run on the stream they are given; logits routed as given may be written onto themselves."""
     rng = np.random.default_rng(21)

@@ -32,8 +32,11 @@ size_t route_tc_split_bytes(int H, int E, int w_dtype);
 size_t route_split_size(int H, int E);
 cudaError_t launch_route_split(const float* w, int H, int E, void* split, cudaStream_t s);
 int route_tc_k_slices(int T, int H, int E, int w_dtype);
+// rotate (the choice by score): launched as a dependent, tiles starting at different
+// k-blocks; counts: the count table, zeroed on the way.
 cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, float* partials,
-                                   int ks, void* split, cudaStream_t s, bool rotate = false);
+                                   int ks, void* split, cudaStream_t s, bool rotate = false,
+                                   int32_t* counts = nullptr, int count_stride = 0);
 // The router GEMM and the top-k in one tensor-core kernel (route_tc.cu), for
 // routers whose experts fit one MMA (route_topk_tc_ok); writes the count table
 // (counts, row stride count_stride) in full when counts is not null.

@@ -567,12 +567,14 @@ size_t route_ws_bytes(int T, int H, int E, int x_dtype, int w_dtype) {
 // Tensor-core logits into the workspace: fp32 partial sums over *ks K slices,
 // laid out [ks][T][E].
 static cudaError_t route_partials_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, void* ws,
-                                     const float** partials, int* ks, cudaStream_t s, bool rotate = false) {
+                                     const float** partials, int* ks, cudaStream_t s, bool rotate = false,
+                                     int32_t* counts = nullptr) {
   unsigned char* w8 = static_cast<unsigned char*>(ws);
   float* p = reinterpret_cast<float*>(w8);
   void* split = w8 + route_partials_bytes(T, H, E, w_dtype);
   int k = route_tc_k_slices(T, H, E, w_dtype);
-  cudaError_t e = launch_route_logits_tc(x, w, w_dtype, T, H, E, p, k, split, s, rotate);
+  cudaError_t e = launch_route_logits_tc(x, w, w_dtype, T, H, E, p, k, split, s, rotate, counts,
+                                         counts != nullptr ? pair_counts_stride(T) : 0);
   if (e != cudaSuccess) return e;
   const int kb_all = (H + 63) / 64, per = (kb_all + k - 1) / k;
   *ks = (kb_all + per - 1) / per;  // the slices the launcher actually used
@@ -661,13 +663,14 @@ size_t route_hier_ws_bytes(int T, int H, int Ep, int x_dtype, int w_dtype) {
 // copy onto itself is dropped), else they go to the workspace as *ks partial sums.
 static cudaError_t route_logits(const void* x, int x_dtype, const void* w, int w_dtype, int T, int H, int E, void* ws,
                                 const float** logits_in, float** logits_out, int* ks, cudaStream_t s,
-                                bool rotate = false) {
+                                bool rotate = false, int32_t* counts = nullptr) {
   *ks = 1;
   if (*logits_in != nullptr) {
     if (*logits_out == *logits_in) *logits_out = nullptr;
     return cudaSuccess;
   }
-  if (route_on_tensor_cores(x_dtype, H)) return route_partials_tc(x, w, w_dtype, T, H, E, ws, logits_in, ks, s, rotate);
+  if (route_on_tensor_cores(x_dtype, H))
+    return route_partials_tc(x, w, w_dtype, T, H, E, ws, logits_in, ks, s, rotate, counts);
   unsigned char* w8 = static_cast<unsigned char*>(ws);
   float* lg = reinterpret_cast<float*>(w8);
   unsigned char* rest = w8 + align_up((size_t)T * E * sizeof(float), 256);
@@ -726,18 +729,23 @@ cudaError_t launch_route_select(const void* x, int x_dtype, const void* w, int w
                                 void* ws, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   cudaError_t e;
-  if (logits_in == nullptr && route_on_tensor_cores(x_dtype, H)) {  // product and choice in one kernel
+  const bool tc = logits_in == nullptr && route_on_tensor_cores(x_dtype, H);
+  if (tc) {  // product and choice in one kernel
     const int ks = route_select_cl_slices(T, H, E, w_dtype);
     if (ks >= 1)
       return launch_route_select_cl(x, w, w_dtype, T, H, E, k_max, ks, logits_out, sel, kpt, k_uniform, topk_idx,
                                     topk_w, pair_counts, pair_counts != nullptr ? pair_counts_stride(T) : 0,
                                     ws, s);
   }
-  int ks = 1;
-  e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s, true);
-  if (e != cudaSuccess) return e;
   PairCounts pc;
-  e = pair_counts_begin(pair_counts, T, E, &pc, s);
+  if (tc) {  // the product zeroes the count table
+    pc.p = pair_counts;
+    pc.stride = pair_counts_stride(T);
+  } else if ((e = pair_counts_begin(pair_counts, T, E, &pc, s)) != cudaSuccess) {
+    return e;
+  }
+  int ks = 1;
+  e = route_logits(x, x_dtype, w, w_dtype, T, H, E, ws, &logits_in, &logits_out, &ks, s, true, pair_counts);
   if (e != cudaSuccess) return e;
   const size_t sm = (size_t)kTopkWarps * select_scratch(E, sel.n_group, k_max) * sizeof(float);
   // one warp per token until the GPU is full, then a few tokens each (the kernel is bound by

@@ -79,7 +79,8 @@ __global__ void split_router_kernel(const float* __restrict__ w, int E, int H, i
 template <int S, int CPS>  // CPS: resident CTAs per SM the ring is sized for
 __global__ void __launch_bounds__(THREADS, CPS)
 route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, int T, int H,
-                int E, int EC, int stages, int kb_per_slice, int rotate, float* __restrict__ partials) {
+                int E, int EC, int stages, int kb_per_slice, int rotate, float* __restrict__ partials,
+                int32_t* __restrict__ counts, int count_stride) {
   pdl_trigger();  // the kernel after it may start its setup
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -116,6 +117,7 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem_base;
+  if (rotate) pdl_wait();  // launched as a dependent: nothing in global memory is touched before
 
   if (warp == 0) {  // TMA producer
     int it = 0;
@@ -161,6 +163,15 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     if (lane == 0) mbar_drain(&sh.done, 0, &g_err);
   } else {  // epilogue: thread = one token row of the accumulator
     const int q = warp & 3;
+    // zero the tile's column of the count table, which the selection adds to (a memset before the
+    // selection and a plain launch of this kernel: 38.7 us a call at 16384 tokens of 128 experts, 34.3 so)
+    static_assert(BM == SEMMOE_PAIR_COUNT_CHUNK, "a tile is a chunk of the count table");
+    if (counts != nullptr && pass == 0 && slice == 0) {
+      const int last = (int)blockIdx.x + 1 == (int)gridDim.x;
+      const int n = last ? count_stride - (int)blockIdx.x : 1;  // the last tile's: and the padding after it
+      for (int i = (int)threadIdx.x - 64; i < E * n; i += THREADS - 64)
+        counts[(size_t)(i / n) * count_stride + blockIdx.x + i % n] = 0;
+    }
     int ok = 1;
     if (lane == 0) ok = mbar_wait(&sh.tfull, 0, abort_flag, &g_err);
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -822,12 +833,16 @@ cudaError_t launch_route_split(const float* w, int H, int E, void* split, cudaSt
 
 template <int S, int CPS>
 static cudaError_t launch_k(dim3 grid, const CUtensorMap& mx, const CUtensorMap& mw, int T, int H, int E, int EC,
-                            int stages, int kb_per_slice, int rotate, float* partials, cudaStream_t s) {
+                            int stages, int kb_per_slice, int rotate, float* partials, int32_t* counts,
+                            int count_stride, cudaStream_t s) {
   static std::atomic<unsigned long long> smem_set{0};
   cudaError_t e = ensure_smem_limit(route_tc_kernel<S, CPS>, (int)smem_bytes(CPS), smem_set);
   if (e != cudaSuccess) return e;
-  route_tc_kernel<S, CPS><<<grid, THREADS, smem_bytes(CPS), s>>>(mx, mw, T, H, E, EC, stages, kb_per_slice,
-                                                                 rotate, partials);
+  if (rotate)
+    return launch_kernel(route_tc_kernel<S, CPS>, grid, dim3(THREADS), smem_bytes(CPS), s, 1, true, mx, mw, T, H, E, EC,
+                         stages, kb_per_slice, rotate, partials, counts, count_stride);
+  route_tc_kernel<S, CPS><<<grid, THREADS, smem_bytes(CPS), s>>>(mx, mw, T, H, E, EC, stages, kb_per_slice, rotate,
+                                                                 partials, counts, count_stride);
   return cudaSuccess;
 }
 
@@ -836,7 +851,8 @@ static cudaError_t launch_k(dim3 grid, const CUtensorMap& mx, const CUtensorMap&
 // route_tc_k_slices(); the logits are their sum in slice order); split:
 // workspace of route_tc_split_bytes() (fp32 weight only).
 cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, int T, int H, int E, float* partials,
-                                   int ks, void* split, cudaStream_t s, bool rotate) {
+                                   int ks, void* split, cudaStream_t s, bool rotate, int32_t* counts,
+                                   int count_stride) {
   const int S = w_dtype == SEMMOE_BF16 ? 1 : 3;
   const int EC = experts_per_pass(E, S), n_pass = (E + EC - 1) / EC;
   const int kb_all = (H + BK - 1) / BK;
@@ -871,10 +887,11 @@ cudaError_t launch_route_logits_tc(const void* x, const void* w, int w_dtype, in
   int stages = (int)(stage_budget(cps) / stage_bytes);
   if (stages > MAX_STAGES) stages = MAX_STAGES;
   cudaError_t e;
-  if (S == 3 && cps == 1) e = launch_k<3, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
-  else if (S == 3) e = launch_k<3, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
-  else if (cps == 1) e = launch_k<1, 1>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
-  else e = launch_k<1, 2>(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, s);
+  auto run = [&](auto launch) {
+    return launch(grid, mx, mw, T, H, E, EC, stages, kb_per_slice, rotate, partials, counts, count_stride, s);
+  };
+  if (S == 3) e = cps == 1 ? run(launch_k<3, 1>) : run(launch_k<3, 2>);
+  else e = cps == 1 ? run(launch_k<1, 1>) : run(launch_k<1, 2>);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
