@@ -17,7 +17,7 @@
 // Bound by instructions where the GPU is full of tokens (16384 tokens, 128 experts, 8
 // picks: 69% of the issue slots, 690 instructions a token, 16 us beside 20 us of the
 // product) and by the latency of its steps where it is not (one token, 256 experts in 8
-// groups: about 5 us of the call's 14).
+// groups: about 5 us of the call's 13 on the device).
 #pragma once
 
 #include <float.h>
