@@ -576,7 +576,8 @@ int semmoe_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32
  * a, a_scales   [device] [P,K] quantised, groups of expert_offsets
  * b, b_scales   [device] [E,N,K] quantised, E groups of N rows
  * out           [device] [P,N] fp32 or bf16
- * Limits: K % 32 == 0, N % 8 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn.
+ * Limits: K % 32 == 0, N % 8 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn; a group skipped
+ * for its expert keeps its place among a_scales' row tiles, one skipped for its offsets has none.
  */
 int semmoe_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* expert_offsets,
                             const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,

@@ -72,7 +72,8 @@ struct Shared {
   int total_mtiles;
   int off[MAX_GROUPS + 1];
   int pe[MAX_GROUPS];
-  int tp[MAX_GROUPS + 1];  // row tiles before each group
+  int tp[MAX_GROUPS + 1];  // row tiles of work before each group
+  int skipped[MAX_GROUPS]; // row tiles before each group that are no work (an expert out of range): they have scales
 };
 
 constexpr int OUT_STAGE_BYTES = 8 * 2048;  // 2 KB per epilogue warp
@@ -115,9 +116,9 @@ __device__ __forceinline__ float swiglu(uint32_t gw, uint32_t uw) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-// A row tile: its first row, valid rows and expert.
+// A row tile: its first row, valid rows, expert, and its place among the scales' row tiles.
 struct RowTile {
-  int row0, rows, expert;
+  int row0, rows, expert, scales;
 };
 // Tiles come in increasing order, so a role keeps the group `g` it is at: the next tile
 // is a few groups on where groups are long, and anywhere after it where they are empty.
@@ -134,7 +135,7 @@ __device__ __forceinline__ RowTile decode_mtile(const Shared& sh, int G, int& g,
     }
   }
   const int row0 = sh.off[g] + (mt - sh.tp[g]) * BM, left = sh.off[g + 1] - row0;
-  return RowTile{row0, left < BM ? left : BM, sh.pe[g]};
+  return RowTile{row0, left < BM ? left : BM, sh.pe[g], mt + sh.skipped[g]};
 }
 
 // mbar_wait (same bounds), polling a few times before it looks at the clock, whose
@@ -216,42 +217,47 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
   if (warp == 1) tmem_alloc(&sh.tmem_base, TMEM_COLS);
   if (!pr.early) pdl_wait();
   pdl_trigger();
-  if (warp == 0) {  // the tables, and the exclusive prefix of row tiles per group: 8 groups per lane
-    int off[9], cnt[8], sum = 0;
+  // The tables, and the exclusive prefixes per group of row tiles and of those to skip: 8 groups per lane.  The
+  // offsets alone say where a group's scales are, so a group whose expert is out of range keeps its row tiles
+  // there while it has none in the list of work.
+  if (warp == 0) {
+    int off[9], cnt[8], skip[8], sum = 0, sum_skip = 0;
 #pragma unroll
     for (int i = 0; i < 9; ++i) off[i] = lane * 8 + i <= G ? pr.offsets[lane * 8 + i] : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
-      int c = 0;
+      int c = 0, c_skip = 0;
       if (g < G) {
         const int lo = off[i], hi = off[i + 1], e = pr.experts[g];
         sh.off[g] = lo;
         sh.pe[g] = e;
         if (g == G - 1) sh.off[G] = hi;
         if (lo < 0 || hi < lo || hi > pr.P) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
-        else if (e < 0 || e >= pr.E) atomicOr(&g_err, SEMMOE_DEVERR_EXPERT);
-        else c = row_tiles(hi - lo);
+        else if (e < 0 || e >= pr.E) {
+          atomicOr(&g_err, SEMMOE_DEVERR_EXPERT);
+          c_skip = row_tiles(hi - lo);
+        } else c = row_tiles(hi - lo);
       }
-      cnt[i] = c;
-      sum += c;
+      cnt[i] = c, skip[i] = c_skip;
+      sum += c, sum_skip += c_skip;
     }
-    int incl = sum;
+    int incl = sum, incl_skip = sum_skip;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
+      const int v = __shfl_up_sync(0xffffffffu, incl, d), v_skip = __shfl_up_sync(0xffffffffu, incl_skip, d);
+      if (lane >= d) incl += v, incl_skip += v_skip;
     }
-    int run = incl - sum;
+    int run = incl - sum, run_skip = incl_skip - sum_skip;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
-      if (g < G) sh.tp[g] = run;
-      run += cnt[i];
+      if (g < G) sh.tp[g] = run, sh.skipped[g] = run_skip;
+      run += cnt[i], run_skip += skip[i];
     }
     if (lane == 31) {
       // more tiles than any split of P rows has: offsets that step back, and scales that end before them
-      const bool bad = incl > pr.P / BM + G;
+      const bool bad = (long long)incl + incl_skip > pr.P / BM + G;
       if (bad) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
       sh.tp[G] = incl;
       sh.total_mtiles = bad ? 0 : incl;
@@ -291,7 +297,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
       unsigned char* a = ring + (size_t)s * STAGE_BYTES;
       tma_load_2d(a, &map_a, &sh.full[s], p.kb * (BK / 2), p.rt.row0);
       // two column tiles (of the next row tile, or past the end, where K has only one more: not used)
-      tma_load_2d(a + A_BYTES + B_BYTES, &map_as, &sh.full[s], 0, p.tile / n_tiles * kc + 2 * p.kb);
+      tma_load_2d(a + A_BYTES + B_BYTES, &map_as, &sh.full[s], 0, p.rt.scales * kc + 2 * p.kb);
     };
     auto load_b = [&](const Place& p, int s) {
       const int nt = p.tile % n_tiles, e = p.rt.expert, x = p.kb * (BK / 2);
@@ -417,8 +423,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     };
     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
     for (int tile = unit0; tile < total; tile += units, half += 2) {
-      const int mt = tile / n_tiles, nt = tile % n_tiles;
-      const RowTile rt = decode_mtile(sh, G, g, mt);
+      const int nt = tile % n_tiles;
+      const RowTile rt = decode_mtile(sh, G, g, tile / n_tiles);
       const int row0 = rt.row0, rows = rt.rows;
       if (GLU) {  // group w takes blocks w and w + 2 of 32 columns
         if (!wait_acc(half) || !wait_acc(half + 1)) break;
@@ -430,7 +436,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         tmem_ld_wait();
         leave_acc(half);
         uint8_t* hrow = static_cast<uint8_t*>(pr.out) + (size_t)(row0 + (r < rows ? r : 0)) * (pr.N / 2) + nt * 64;
-        uint8_t* hs = pr.out_scales + ((size_t)mt * n_tiles + nt) * kTileBytes + row_byte(r);
+        uint8_t* hs = pr.out_scales + ((size_t)rt.scales * n_tiles + nt) * kTileBytes + row_byte(r);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int j = w + 2 * i;
