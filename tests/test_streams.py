@@ -1,0 +1,119 @@
+"""Memory that a call takes for itself belongs to the stream that the call runs on."""
+import contextlib
+
+import numpy as np
+import pytest
+import torch
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class Recorder:
+    """Torch's stream context and allocation, recorded: which stream was current at each torch.empty."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.allocated = None, []
+        real = torch.empty
+
+        @contextlib.contextmanager
+        def use(stream):
+            before, self.current = self.current, stream
+            yield
+            self.current = before
+
+        def empty(*a, **kw):
+            kw.pop("device", None)
+            self.allocated.append(None if self.current is None else self.current.cuda_stream)
+            return real(*a, **kw)
+
+        monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
+        monkeypatch.setattr(torch.cuda, "stream", use)
+        monkeypatch.setattr(torch, "empty", empty)
+
+
+class FakeLibrary:
+    """The compiled entries: sizes are 1 MB, calls return success and keep the stream they were given."""
+
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 1 << 20
+
+        def call(*a):
+            self.streams.append(a[-1])
+            return 0
+        return call
+
+
+ROUTE, HIER, SELECT = "semmoe_route", "semmoe_route_hier", "semmoe_route_select"
+
+
+@pytest.mark.parametrize("name,kind", [(n, k) for n in (ROUTE, HIER, SELECT) for k in ("none", "stream")]
+                         + [(SELECT, "address"), (SELECT, "object")])
+def test_a_call_takes_its_workspace_on_its_own_stream(monkeypatch, name, kind):
+    from token_expert_routing_gb300 import _abi
+    lib = FakeLibrary()
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(4, 8)
+    idx, gw, sub = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1), torch.zeros(8)
+    rec = Recorder(monkeypatch)
+    monkeypatch.setattr(_abi, "fast", lambda: lib)
+    monkeypatch.setattr(_abi, "_stream", lambda s: 0 if s is None else s.cuda_stream)
+    stream = {"none": None, "stream": FakeStream(77), "address": 77, "object": type("S", (), {"cuda_stream": 77})()}[kind]
+    if name == ROUTE:
+        _abi.semmoe_route(x, w, None, None, None, 1, 2, 8, 4, 1, idx, gw, stream=stream)
+    elif name == HIER:
+        _abi.semmoe_route_hier(x, w, None, None, sub, 2, None, 1, 2, 8, 4, 1, idx, gw, stream=stream)
+    else:
+        _abi.semmoe_route_select(x, w, None, None, 0, None, 1, 1, 1, True, 1.0, None, 1, 2, 8, 4, 1, idx, gw, stream=stream)
+    assert rec.allocated == [None if kind == "none" else 77]
+    assert len(lib.streams) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", [ROUTE, HIER, SELECT])
+def test_workspace_on_a_side_stream_is_not_handed_on_early(name):
+    """A product with partial logits in its workspace, behind work on its own stream, and allocations of the
+    same size written on the current stream right after the call."""
+    from token_expert_routing_gb300 import _abi
+    rng = np.random.default_rng(3)
+    T, H, E, k = 3000, 512, 256, 6
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).cuda()
+    wr = torch.from_numpy((rng.standard_normal((E, H)) / np.sqrt(H)).astype(np.float32)).cuda()
+    Ep = 64
+    sub = torch.zeros(E, device="cuda")
+
+    def call(stream):
+        idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+        if name == ROUTE:
+            _abi.semmoe_route(x, wr, None, None, None, k, T, H, E, k, idx, w, stream=stream)
+        elif name == HIER:
+            _abi.semmoe_route_hier(x, wr[:Ep], None, None, sub, E // Ep, None, k, T, H, Ep, k, idx, w, stream=stream)
+        else:
+            _abi.semmoe_route_select(x, wr, None, None, _abi.SEMMOE_SCORE_SOFTMAX, None, 1, 1, 1, True, 1.0, None, k, T, H,
+                                     E, k, idx, w, stream=stream)
+        return idx, w
+
+    want = [t.clone() for t in call(None)]
+    n = max(_abi.semmoe_route_workspace_size(T, H, E, _abi.SEMMOE_BF16, _abi.SEMMOE_F32),
+            _abi.semmoe_route_select_workspace_size(T, H, E, _abi.SEMMOE_BF16, _abi.SEMMOE_F32))
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for form in ("stream", "address") if name == SELECT else ("stream",):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                busy @ busy  # the call waits behind these
+        got = call(side if form == "stream" else side.cuda_stream)
+        spoilers = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del spoilers
+    assert _abi.semmoe_check_errors() == 0

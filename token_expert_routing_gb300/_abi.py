@@ -150,6 +150,17 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on ``stream`` (a Stream, an address or None: the current one).  It is taken
+    from that stream's memory: torch may hand it on when it is dropped, which is then in order with the call's kernels."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream if isinstance(stream, int) else stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def dtype_code(t: torch.Tensor) -> int:
     try:
         return _DTYPE[t.dtype]
@@ -201,7 +212,7 @@ def semmoe_route(x, w_router, logits_in, logits_out, k_per_token, k_uniform, T, 
     wd = w_dtype if w_dtype is not None else (dtype_code(w_router) if w_router is not None else SEMMOE_F32)
     if ws is None:
         n = semmoe_route_workspace_size(T, max(H, 1), E, xd, wd)
-        ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
+        ws = _workspace(n, topk_idx.device, stream)
     _check(fast().semmoe_route(x, xd, w_router, wd, logits_in, logits_out,
                               k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w,
                               pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
@@ -228,7 +239,7 @@ def semmoe_route_hier(x, w_parent, logits_in, logits_out, sub_logw, N, k_per_tok
     wd = w_dtype if w_dtype is not None else (dtype_code(w_parent) if w_parent is not None else SEMMOE_F32)
     if ws is None:
         n = semmoe_route_hier_workspace_size(T, max(H, 1), Ep, xd, wd)
-        ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
+        ws = _workspace(n, topk_idx.device, stream)
     _check(fast().semmoe_route_hier(x, xd, w_parent, wd, logits_in, logits_out, sub_logw, N,
                                    k_per_token, k_uniform, T, H, Ep, k_max, topk_idx, topk_w,
                                    pair_counts, ws, ws.numel() * ws.element_size(), _stream(stream)))
@@ -249,7 +260,7 @@ def semmoe_route_select(x, w_router, logits_in, logits_out, score: int, bias, n_
         wd = w_dtype if w_dtype is not None else dtype_code(w_router)
         n = fast().semmoe_route_select_workspace_size(T, max(H, 1), E, dtype_code(x), wd)
         if n > 256:
-            ws = torch.empty(n, dtype=torch.uint8, device=topk_idx.device)
+            ws = _workspace(n, topk_idx.device, stream)
     fast().route_select(x, w_router, logits_in, logits_out, score, bias, n_group, topk_group, group_top, renorm, scale,
                         k_per_token, k_uniform, T, H, E, k_max, topk_idx, topk_w, pair_counts, ws, w_dtype, stream)
 
