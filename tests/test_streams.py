@@ -10,6 +10,12 @@ class FakeStream:
     def __init__(self, handle):
         self.cuda_stream = handle
 
+    def __eq__(self, other):
+        return self.cuda_stream == other.cuda_stream
+
+    def __hash__(self):
+        return hash(self.cuda_stream)
+
 
 class Recorder:
     """Torch's stream context and allocation, recorded: which stream was current at each torch.empty."""
@@ -32,6 +38,7 @@ class Recorder:
         monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(handle))
         monkeypatch.setattr(torch.cuda, "stream", use)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current or FakeStream(0))
         monkeypatch.setattr(torch, "empty", empty)
 
 
@@ -73,6 +80,27 @@ def test_a_call_takes_its_workspace_on_its_own_stream(monkeypatch, name, kind):
         _abi.semmoe_route_select(x, w, None, None, 0, None, 1, 1, 1, True, 1.0, None, 1, 2, 8, 4, 1, idx, gw, stream=stream)
     assert rec.allocated == [None if kind == "none" else 77]
     assert len(lib.streams) == 1
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("handle", [None, 0, 77])
+def test_a_forward_takes_its_memory_on_its_own_stream(monkeypatch, mx4, handle):
+    """Tables that a forward drops when it returns (the count table, workspaces), and its outputs."""
+    from token_expert_routing_gb300 import MoELayer, _abi
+    lib = FakeLibrary()
+    rec = Recorder(monkeypatch)
+    monkeypatch.setattr(_abi, "fast", lambda: lib)
+    monkeypatch.setattr(_abi, "_stream", lambda s: rec.current.cuda_stream if s is None and rec.current else 0 if s is None else s.cuda_stream)
+    bf16 = dict(dtype=torch.bfloat16)
+    layer = MoELayer(torch.zeros(4, 32, **bf16), torch.zeros(4, 64, 32, **bf16), torch.zeros(4, 32, 32, **bf16),
+                     torch.zeros(4, dtype=torch.int32), torch.zeros(10, 1), 1, 2, overlap=False, overlap_shared=False,
+                     device="cpu", mx4=mx4, fused_gather=None if mx4 else False)
+    rec.allocated.clear()
+    lib.streams.clear()
+    layer.forward(torch.zeros(3, 32, **bf16), torch.zeros(3, dtype=torch.int32), k=2,
+                  stream=None if handle is None else FakeStream(handle))
+    assert len(rec.allocated) > 10 and {h or 0 for h in rec.allocated} == {handle or 0}
+    assert len(lib.streams) >= 5
 
 
 @pytest.mark.gpu

@@ -222,8 +222,13 @@ class MoELayer:
         run on the second stream.  ``mark_external``: the marks' events are
         recorded as event nodes when the forward is captured in a CUDA graph
         (so each replay times its steps).  Every step has finished on ``stream``
-        when the work enqueued by this call has.
+        when the work enqueued by this call has.  All memory of the call, the
+        outputs' too, is taken from ``stream``'s.
         """
+        if stream is not None and stream != torch.cuda.current_stream():
+            with torch.cuda.stream(stream):
+                return self.forward(x, token_ids, k_per_token, k, P, logits_in, keep_logits, stream, marks,
+                                    req_offsets, side_marks, mark_external)
         s = torch.cuda.current_stream() if stream is None else stream
         side = self._side_stream() if (self.overlap or self.overlap_shared) else None
 
