@@ -1,5 +1,7 @@
 """Memory that a call takes for itself belongs to the stream that the call runs on."""
 import contextlib
+import gc
+import weakref
 
 import numpy as np
 import pytest
@@ -43,19 +45,27 @@ class Recorder:
 
 
 class FakeLibrary:
-    """The compiled entries: sizes are 1 MB, calls return success and keep the stream they were given."""
+    """The compiled entries: sizes are 1 MB unless set, calls return success and keep the stream they were given."""
 
     def __init__(self):
-        self.streams = []
+        self.streams, self.size = [], 1 << 20
 
     def __getattr__(self, name):
         if name.endswith("_size"):
-            return lambda *a: 1 << 20
+            return lambda *a: self.size
 
         def call(*a):
             self.streams.append(a[-1])
             return 0
         return call
+
+
+def small_layer(**kw):
+    from token_expert_routing_gb300 import MoELayer
+    bf16 = dict(dtype=torch.bfloat16)
+    return MoELayer(torch.zeros(4, 32, **bf16), torch.zeros(4, 64, 32, **bf16), torch.zeros(4, 32, 32, **bf16),
+                    torch.zeros(4, dtype=torch.int32), torch.zeros(10, 1), 1, 2, overlap=False, overlap_shared=False,
+                    device="cpu", **kw)
 
 
 ROUTE, HIER, SELECT = "semmoe_route", "semmoe_route_hier", "semmoe_route_select"
@@ -86,21 +96,49 @@ def test_a_call_takes_its_workspace_on_its_own_stream(monkeypatch, name, kind):
 @pytest.mark.parametrize("handle", [None, 0, 77])
 def test_a_forward_takes_its_memory_on_its_own_stream(monkeypatch, mx4, handle):
     """Tables that a forward drops when it returns (the count table, workspaces), and its outputs."""
-    from token_expert_routing_gb300 import MoELayer, _abi
+    from token_expert_routing_gb300 import _abi
     lib = FakeLibrary()
     rec = Recorder(monkeypatch)
     monkeypatch.setattr(_abi, "fast", lambda: lib)
     monkeypatch.setattr(_abi, "_stream", lambda s: rec.current.cuda_stream if s is None and rec.current else 0 if s is None else s.cuda_stream)
     bf16 = dict(dtype=torch.bfloat16)
-    layer = MoELayer(torch.zeros(4, 32, **bf16), torch.zeros(4, 64, 32, **bf16), torch.zeros(4, 32, 32, **bf16),
-                     torch.zeros(4, dtype=torch.int32), torch.zeros(10, 1), 1, 2, overlap=False, overlap_shared=False,
-                     device="cpu", mx4=mx4, fused_gather=None if mx4 else False)
+    layer = small_layer(mx4=mx4, fused_gather=None if mx4 else False)
     rec.allocated.clear()
     lib.streams.clear()
     layer.forward(torch.zeros(3, 32, **bf16), torch.zeros(3, dtype=torch.int32), k=2,
                   stream=None if handle is None else FakeStream(handle))
     assert len(rec.allocated) > 10 and {h or 0 for h in rec.allocated} == {handle or 0}
     assert len(lib.streams) >= 5
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+def test_a_captured_layer_keeps_the_workspaces_of_its_graph(monkeypatch, mx4):
+    """A forward of a larger batch replaces the layer's workspaces; a graph captured before still writes its own."""
+    from token_expert_routing_gb300 import CapturedLayer, _abi
+
+    class Graph:
+        pass
+
+    lib = FakeLibrary()
+    Recorder(monkeypatch)
+    monkeypatch.setattr(_abi, "fast", lambda: lib)
+    monkeypatch.setattr(_abi, "_stream", lambda s: 0)
+    monkeypatch.setattr(FakeStream, "wait_stream", lambda self, other: None, raising=False)
+    monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: FakeStream(5))
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
+    monkeypatch.setattr(torch.cuda, "graph", lambda g: torch.cuda.stream(FakeStream(9)))
+    layer = small_layer(mx4=mx4, fused_gather=None if mx4 else False)
+    cap = CapturedLayer(layer, 3, k=2)
+    used = {k: weakref.ref(b) for k, b in layer._ws.items()}
+    assert {"route", "permute", "ffn"} <= set(used) and ("mx4_rows" in used) == mx4
+    lib.size = 1 << 21
+    layer.forward(torch.zeros(300, 32, dtype=torch.bfloat16), torch.zeros(300, dtype=torch.int32), k=2)
+    gc.collect()
+    assert all(layer._ws[k] is not ref() for k, ref in used.items())
+    assert all(ref() is not None for ref in used.values())
+    del cap
+    gc.collect()
+    assert all(ref() is None for ref in used.values())
 
 
 @pytest.mark.gpu
@@ -144,4 +182,32 @@ def test_workspace_on_a_side_stream_is_not_handed_on_early(name):
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         del spoilers
+    assert _abi.semmoe_check_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx4", [False, True])
+def test_a_captured_layer_after_a_larger_forward_and_a_second_graph(mx4):
+    """Replays of a graph captured for a small batch, with the memory that larger forwards freed filled by others."""
+    import workloads as wl
+    from token_expert_routing_gb300 import CapturedLayer, MoELayer, _abi
+    d = wl.make_inputs(wl.scaled("qwen3_30b_a3b_T16384", T=900, H=256, I=96, V=3000))
+    s = d["spec"]
+    layer = MoELayer(d["w_router"], d["w13"], d["w2"], d["expert_rank"], d["lut"], s.R, s.k_max, mx4=mx4)
+    x, ids = d["x"].cuda(), d["token_ids"].cuda()
+    small = CapturedLayer(layer, 50, k=s.k)
+    larger = CapturedLayer(layer, 300, k=s.k)
+    want = [layer.forward(x[:n].clone(), ids[:n].clone(), k=s.k).out.clone() for n in (50, 300)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    whole = layer.forward(x, ids, k=s.k, stream=side).out  # replaces every workspace
+    side.synchronize()
+    spoilers = [torch.full((1 << n,), 255, dtype=torch.uint8, device="cuda") for n in range(8, 25) for _ in range(4)]
+    for cap, n, ref in ((small, 50, want[0]), (larger, 300, want[1])):
+        cap.x.copy_(x[:n])
+        cap.token_ids.copy_(ids[:n])
+        assert torch.equal(cap.replay().out, ref)
+    torch.cuda.synchronize()
+    assert all(bool((t == 255).all()) for t in spoilers)
+    assert torch.equal(layer.forward(x, ids, k=s.k).out, whole)
     assert _abi.semmoe_check_errors() == 0

@@ -163,6 +163,7 @@ class MoELayer:
         self.dtype, self.dcode = self.w13.dtype, abi.dtype_code(self.w13)
         self.device = dev
         self._ws = {}
+        self._before = self._last = None  # the streams of the last forward but one, and of the last
         if select is not None and select.bias is not None:
             select = dataclasses.replace(select, bias=c(select.bias).to(torch.float32))
         self.select = select
@@ -197,6 +198,8 @@ class MoELayer:
     def _workspace(self, key, nbytes):
         buf = self._ws.get(key)
         if buf is None or buf.numel() < nbytes:
+            if buf is not None and buf.is_cuda and self._before is not None:
+                buf.record_stream(self._before)  # where the forward before may still be using it
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[key] = buf
         return buf
@@ -230,6 +233,7 @@ class MoELayer:
                 return self.forward(x, token_ids, k_per_token, k, P, logits_in, keep_logits, stream, marks,
                                     req_offsets, side_marks, mark_external)
         s = torch.cuda.current_stream() if stream is None else stream
+        self._before, self._last = self._last, s
         side = self._side_stream() if (self.overlap or self.overlap_shared) else None
 
         def mark(name):
@@ -517,6 +521,8 @@ class CapturedLayer:
         with torch.cuda.graph(self.graph):
             self.result = layer.forward(self.x, self.token_ids, self.k_per_token, k, self.P,
                                         stream=torch.cuda.current_stream(dev), req_offsets=self.req_offsets)
+        # the graph uses the layer's workspaces: a later, larger forward replaces them there
+        self._workspaces = list(layer._ws.values())
 
     def replay(self) -> LayerOutput:
         self.graph.replay()
