@@ -678,6 +678,19 @@ int semmoe_selftest_bounded_wait(void* stream);
 int semmoe_selftest_fused_ready_wait(const void* x_perm, const void* w13, const void* w2, int P, int H, int I,
                                      void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * semmoe_selftest_mx4_wait -- exercises the failure path of the 4-bit product
+ * (not part of the layer; the pages have no counterpart).  It runs
+ * semmoe_mx4_grouped_gemm (0 < P <= 4096, fp32 out) with the issuing warp of
+ * every CTA first waiting for a barrier that only it could complete.  The wait gives up after
+ * its 2 s bound, sets SEMMOE_DEVERR_TIMEOUT and stops its CTA (in-flight copies drained,
+ * tensor memory freed), so the next semmoe_check_errors() on the stream returns
+ * SEMMOE_ERR_DEVICE_TIMEOUT and the CUDA context stays usable; out keeps what it held.
+ */
+int semmoe_selftest_mx4_wait(const uint8_t* a, const uint8_t* a_scales, const int32_t* expert_offsets,
+                             const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,
+                             int N, int K, float* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

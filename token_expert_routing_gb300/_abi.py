@@ -81,6 +81,7 @@ SIGNATURES = {
     "semmoe_mx4_grouped_ffn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_selftest_bounded_wait": (_i, [_vp]),
     "semmoe_selftest_fused_ready_wait": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "semmoe_selftest_mx4_wait": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
     "semmoe_dp_schedule": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "semmoe_transition_lookup": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _i, _vp, _vp]),
 }
@@ -414,3 +415,11 @@ def semmoe_selftest_fused_ready_wait(x_perm, w13, w2, P, H, I, y_perm, ws, strea
     include/semmoe.h."""
     _check(fast().semmoe_selftest_fused_ready_wait(x_perm, w13, w2, P, H, I, y_perm, ws,
                                                   ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def semmoe_selftest_mx4_wait(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream=None):
+    """Run the 4-bit product with its issuing warps' first waits made
+    unreachable (each gives up after 2 s and sets the timeout bit); see
+    include/semmoe.h."""
+    _check(fast().semmoe_selftest_mx4_wait(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out,
+                                           _stream(stream)))

@@ -647,6 +647,19 @@ int semmoe_selftest_bounded_wait(void* stream) {
   return cuda_status(launch_selftest_bounded_wait(static_cast<cudaStream_t>(stream)), "semmoe_selftest_bounded_wait");
 }
 
+int semmoe_selftest_mx4_wait(const uint8_t* a, const uint8_t* a_scales, const int32_t* expert_offsets,
+                             const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,
+                             int N, int K, float* out, void* stream) {
+  const char* fn = "semmoe_selftest_mx4_wait";
+  int rc = check_mx4_product(fn, P, E, N, K, a, a_scales, expert_offsets, phys_to_expert, b, b_scales, out);
+  if (rc != SEMMOE_OK) return rc;
+  REQUIRE(P > 0 && P <= 4096, "%s: need 0 < P <= 4096 (P=%d)", fn, P);
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_mx4_grouped_gemm(a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out,
+                                             SEMMOE_F32, static_cast<cudaStream_t>(stream), false, true),
+                     fn);
+}
+
 int semmoe_selftest_fused_ready_wait(const void* x_perm, const void* w13, const void* w2, int P, int H, int I,
                                      void* y_perm, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_ffn_args("semmoe_selftest_fused_ready_wait", x_perm, w13, w2, SEMMOE_BF16, P, H, I, y_perm, ws,

@@ -331,6 +331,7 @@ PyMethodDef methods[] = {
     ENTRY(semmoe_transition_lookup),
     ENTRY(semmoe_selftest_bounded_wait),
     ENTRY(semmoe_selftest_fused_ready_wait),
+    ENTRY(semmoe_selftest_mx4_wait),
     METHOD("mx4_quantize", &mx4_quantize),
     METHOD("mx4_dequantize", &mx4_dequantize),
     METHOD("mx4_quantize_rows", &mx4_quantize_rows),

@@ -159,7 +159,8 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
                                   void* out, int dtype, cudaStream_t s);
 cudaError_t launch_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* offsets,
                                     const int32_t* experts, const uint8_t* b, const uint8_t* b_scales, int P, int E,
-                                    int N, int K, void* out, int out_dtype, cudaStream_t s, bool early = false);
+                                    int N, int K, void* out, int out_dtype, cudaStream_t s, bool early = false,
+                                    bool stall = false);
 size_t mx4_ffn_ws_bytes(int P, int E, int I);
 cudaError_t launch_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int32_t* offsets,
                                    const int32_t* experts, const uint8_t* w13, const uint8_t* w13_scales,

@@ -146,6 +146,13 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, abort_flag, &g_err);
 }
+// The same by a whole converged warp, with one answer for all lanes (mbar_wait_warp).
+__device__ __forceinline__ bool wait_for_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return mbar_wait_warp(bar, parity, abort_flag, &g_err);
+}
 
 // Output of a 64-byte piece of an epilogue warp's 32 tile rows (w: the thread's
 // row, 16 words): transposed through the warp's 2 KB of shared memory (16-byte
@@ -177,6 +184,7 @@ struct Product {
   // early: launched as the dependent of a kernel of this file that triggers after its own wait (so that everything
   // before that kernel is complete): tables and B are read before this kernel's wait, only A is its output
   int early;
+  int stall;             // failure-path self-test only: the issuer first waits for what never comes
   void* out;             // plain: [P, N]; SwiGLU: the packed h [P, N / 2]
   uint8_t* out_scales;   // SwiGLU: h's scales
 };
@@ -333,7 +341,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     }
     for (; p.tile < total; ++it, next(p)) {
       const int s = it % STAGES;
-      if (!wait_for(&sh.empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) break;
+      if (!wait_for_warp(&sh.empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) break;
       if (elect_one()) {
         load_b(p, s);
         load_a(p, s);
@@ -343,7 +351,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     if (lane == 0) *reinterpret_cast<volatile int*>(&sh.armed) = (int)it;
   } else if (warp == 1) {
     uint32_t it = 0, half = 0;  // stage position; half tiles begun
-    bool ok = true;
+    bool ok = !pr.stall || wait_for_warp(&sh.done, 0, abort_flag);
     // descriptors of stage 0; their address field counts 16 bytes
     const uint64_t desc_a = sw128_desc(smem_u32(ring)), desc_b = sw128_desc(smem_u32(ring) + A_BYTES),
                    desc_s = scale_desc(smem_u32(ring) + A_BYTES + B_BYTES);
@@ -361,12 +369,12 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     for (int tile = unit0; ok && tile < total; tile += units, half += 2) {
       const uint32_t a0 = half % ACCS, a1 = (half + 1) % ACCS;
       // the epilogue has left the accumulator (three halves ago)
-      if (half >= ACCS && !wait_for(&sh.tempty[a0], (half / ACCS - 1) & 1, abort_flag)) break;
+      if (half >= ACCS && !wait_for_warp(&sh.tempty[a0], (half / ACCS - 1) & 1, abort_flag)) break;
       int done1 = 0;                // stages whose second half is issued
       bool free1 = half + 1 < ACCS; // the second half's accumulator is free
       for (int kb = 0; kb < kb_n; ++kb) {
         const uint32_t pos = it + kb, s = pos % STAGES;
-        if (!wait_for(&sh.full[s], (pos / STAGES) & 1, abort_flag)) {
+        if (!wait_for_warp(&sh.full[s], (pos / STAGES) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -382,8 +390,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         __syncwarp();
         if (!free1) {  // first halves go on while the epilogue still reads it, as far as the ring reaches
           const uint32_t ph = ((half + 1) / ACCS - 1) & 1;
-          if (kb + 1 < kb_n && kb + 1 < STAGES - 1) free1 = __any_sync(0xffffffffu, mbar_try_wait(&sh.tempty[a1], ph));
-          else free1 = ok = wait_for(&sh.tempty[a1], ph, abort_flag);
+          if (kb + 1 < kb_n && kb + 1 < STAGES - 1) free1 = __all_sync(0xffffffffu, mbar_try_wait(&sh.tempty[a1], ph));
+          else free1 = ok = wait_for_warp(&sh.tempty[a1], ph, abort_flag);
           if (!free1) {
             if (!ok) break;
             continue;
@@ -605,8 +613,8 @@ int mx4_gemm_take_errors(cudaStream_t s, int* bits) { return take_error_word(g_e
 
 cudaError_t launch_mx4_grouped_gemm(const uint8_t* a, const uint8_t* a_scales, const int32_t* offsets,
                                     const int32_t* experts, const uint8_t* b, const uint8_t* b_scales, int P, int E,
-                                    int N, int K, void* out, int out_dtype, cudaStream_t s, bool early) {
-  const Product pr{offsets, experts, E, P, E, N, K, (N + BN - 1) / BN, early, out, nullptr};
+                                    int N, int K, void* out, int out_dtype, cudaStream_t s, bool early, bool stall) {
+  const Product pr{offsets, experts, E, P, E, N, K, (N + BN - 1) / BN, early, stall, out, nullptr};
   return out_dtype == SEMMOE_BF16 ? launch_one<false, __nv_bfloat16>(a, a_scales, b, b_scales, pr, s)
                                   : launch_one<false, float>(a, a_scales, b, b_scales, pr, s);
 }
@@ -622,7 +630,7 @@ cudaError_t launch_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, co
                                    void* ws, cudaStream_t s) {
   uint8_t* h = static_cast<uint8_t*>(ws);
   uint8_t* hs = h + align_up((size_t)P * (I / 2), 256);
-  const Product p1{offsets, experts, E, P, E, I, H, (I + 127) / 128, 0, h, hs};
+  const Product p1{offsets, experts, E, P, E, I, H, (I + 127) / 128, 0, 0, h, hs};
   cudaError_t e = launch_one<true, __nv_bfloat16>(x, x_scales, w13, w13_scales, p1, s);
   if (e != cudaSuccess) return e;
   return launch_mx4_grouped_gemm(h, hs, offsets, experts, w2, w2_scales, P, E, H, I, y, SEMMOE_BF16, s, true);

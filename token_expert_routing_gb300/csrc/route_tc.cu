@@ -125,7 +125,7 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
       const int kb = kb_first + i < kb_n ? kb_first + i : kb_first + i - kb_n;
       const int s = i % stages;
       const uint32_t ph = (i / stages) & 1;
-      if (!mbar_wait(&sh.empty[s], ph ^ 1, abort_flag, &g_err)) break;
+      if (!mbar_wait_warp(&sh.empty[s], ph ^ 1, abort_flag, &g_err)) break;
       if (elect_one()) {
         unsigned char* st = ring + (size_t)s * stage_bytes;
         mbar_expect_tx(&sh.full[s], stage_bytes);
@@ -144,7 +144,7 @@ route_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     for (int kb = 0; kb < kb_n; ++kb) {
       const int s = kb % stages;
       const uint32_t ph = (kb / stages) & 1;
-      if (!mbar_wait(&sh.full[s], ph, abort_flag, &g_err)) { ok = false; break; }
+      if (!mbar_wait_warp(&sh.full[s], ph, abort_flag, &g_err)) { ok = false; break; }
       fence_after();
       const uint32_t sa = smem_u32(ring) + (uint32_t)s * stage_bytes, sb = sa + A_BYTES;
       if (elect_one()) {
@@ -639,7 +639,7 @@ route_topk_cl_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
       const int bits = load_bias<NPER>(sel, E, bias);
       if (bits) atomicOr(&g_err, bits);
     }
-    const bool got = mbar_wait(&recv_bar, 0, abort_flag, &g_err);  // every lane: acquire the copies
+    const bool got = mbar_wait_warp(&recv_bar, 0, abort_flag, &g_err);  // every lane: acquire the copies
     for (int row = rank * rpc + (warp - 2); got && row < (rank + 1) * rpc; row += kClThreads / 32 - 2) {
       const int t = t0 + row;
       int kt = 0;  // loaded first: its latency overlaps the sums

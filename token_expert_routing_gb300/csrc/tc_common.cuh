@@ -65,6 +65,14 @@ __device__ inline bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* a
   }
 }
 
+// mbar_wait by a whole converged warp, with one answer for all of its lanes: each
+// lane times its own wait, so where one runs out (or sees the abort flag) another
+// may have seen the phase complete, and lanes that then went different ways would
+// miss each other at the next elect.sync or __syncwarp.
+__device__ inline bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err)) != 0;
+}
+
 // Teardown wait: ignores the abort flag, still bounded.
 __device__ inline void mbar_drain(uint64_t* bar, uint32_t parity, int* err) {
   const uint64_t t0 = globaltimer_ns();
