@@ -6,7 +6,9 @@
 // its types -- a pointer takes None, an address or a contiguous CUDA tensor -- and
 // returns its value.  The routing choice and the 4-bit operators also have entries
 // named without the prefix, which take the tensors' types and sizes from the tensors, the
-// stream as a Stream, an address or None (the current one), and raise on an error.
+// stream as a Stream, an address or None (the current one), and raise on an error.  They
+// refuse a tensor of another type than the call reads it as, or of fewer elements than it touches;
+// an address is taken as it is, except where the type is the tensor's to say.
 // Calls run without the interpreter lock.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -131,6 +133,13 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // ---------------------------------------------------------------------------
 // entries that look at their tensors
 // ---------------------------------------------------------------------------
+// Elements of a buffer (nothing for sizes below 0, which the library refuses; no overflow).
+long long times(long long a, long long b, long long c = 1) {
+  long long r;
+  if (a < 0 || b < 0 || c < 0) return 0;
+  return __builtin_mul_overflow(a, b, &r) || __builtin_mul_overflow(r, c, &r) ? LLONG_MAX : r;
+}
+
 // Arguments taken in order; the first that does not convert sets the Python error
 // and `ok`, and the rest are skipped.
 struct In {
@@ -144,9 +153,15 @@ struct In {
   }
   void* ptr(int i) { return get<void*>(i); }
   int num(int i) { return get<int>(i); }
+  bool none(int i) const { return a[i] == Py_None; }
   // The SEMMOE_* code of a tensor's type (SEMMOE_F32 for None).
   int dtype(int i) {
-    if (!ok || a[i] == Py_None || !THPVariable_Check(a[i])) return SEMMOE_F32;
+    if (!ok || none(i)) return SEMMOE_F32;
+    if (!THPVariable_Check(a[i])) {
+      ok = false;
+      PyErr_Format(PyExc_ValueError, "expected a tensor, whose type is looked at, got %s", Py_TYPE(a[i])->tp_name);
+      return SEMMOE_F32;
+    }
     const at::ScalarType t = THPVariable_Unpack(a[i]).scalar_type();
     if (t == at::kBFloat16) return SEMMOE_BF16;
     if (t != at::kFloat) {
@@ -157,17 +172,33 @@ struct In {
   }
   // Refuse a tensor of another type, or of fewer elements than the library will touch.
   void holds(int i, at::ScalarType type, long long numel, const char* what) {
-    if (!ok || a[i] == Py_None || !THPVariable_Check(a[i])) return;
+    if (!ok || none(i) || !THPVariable_Check(a[i])) return;
     const at::Tensor& t = THPVariable_Unpack(a[i]);
     if (t.scalar_type() == type && t.numel() >= numel) return;
     ok = false;
     PyErr_Format(PyExc_ValueError, "%s: expected at least %lld elements of %s, got %lld of %s", what, numel,
                  c10::toString(type), (long long)t.numel(), c10::toString(t.scalar_type()));
   }
+  void holds_bytes(int i, size_t n, const char* what) {
+    if (!ok || none(i) || !THPVariable_Check(a[i]) || bytes(i) >= n) return;
+    ok = false;
+    PyErr_Format(PyExc_ValueError, "%s: expected at least %zu bytes, got %zu", what, n, bytes(i));
+  }
+  // The same for a tensor of one of the library's types; its code.
+  int values(int i, long long numel, const char* what) {
+    const int code = dtype(i);
+    holds(i, code == SEMMOE_BF16 ? at::kBFloat16 : at::kFloat, numel, what);
+    return code;
+  }
   // Codes and scales of `rows` rows of K values in `tiles` 128-row tiles.
   void mx4(int codes, int scales, long long rows, int K, long long tiles, const char* what) {
-    holds(codes, at::kByte, rows * (K / 2), what);
-    holds(scales, at::kByte, tiles * ((K + 127LL) / 128) * 512, (std::string(what) + " scales").c_str());
+    holds(codes, at::kByte, times(rows, K / 2), what);
+    holds(scales, at::kByte, times(tiles, (K + 127LL) / 128, 512), (std::string(what) + " scales").c_str());
+  }
+  // The tables of E groups of rows.
+  void groups(int offsets, int experts, int E) {
+    holds(offsets, at::kInt, E + 1LL, "expert_offsets");
+    holds(experts, at::kInt, E, "phys_to_expert");
   }
   size_t bytes(int i) {
     if (!ok || a[i] == Py_None || !THPVariable_Check(a[i])) return 0;
@@ -216,8 +247,8 @@ float* f32(void* p) { return static_cast<float*>(p); }
 // x, groups, group_rows, K, codes, scales, stream
 FUNCTION(mx4_quantize, 7) {
   const int G = in.num(1), n = in.num(2), K = in.num(3);
-  in.mx4(4, 5, (long long)G * n, K, G * tiles_of(n), "codes");
-  const int d = in.dtype(0);
+  in.mx4(4, 5, times(G, n), K, times(G, tiles_of(n)), "codes");
+  const int d = in.values(0, times(G, n, K), "x");
   void *x = in.ptr(0), *c = in.ptr(4), *s = in.ptr(5), *st = in.stream(6);
   return run(in, [&] { return semmoe_mx4_quantize(x, d, G, n, K, u8(c), u8(s), st); });
 }
@@ -225,8 +256,8 @@ FUNCTION(mx4_quantize, 7) {
 // codes, scales, groups, group_rows, K, out, stream
 FUNCTION(mx4_dequantize, 7) {
   const int G = in.num(2), n = in.num(3), K = in.num(4);
-  in.mx4(0, 1, (long long)G * n, K, G * tiles_of(n), "codes");
-  const int d = in.dtype(5);
+  in.mx4(0, 1, times(G, n), K, times(G, tiles_of(n)), "codes");
+  const int d = in.values(5, times(G, n, K), "out");
   void *c = in.ptr(0), *s = in.ptr(1), *o = in.ptr(5), *st = in.stream(6);
   return run(in, [&] { return semmoe_mx4_dequantize(u8(c), u8(s), G, n, K, o, d, st); });
 }
@@ -234,8 +265,10 @@ FUNCTION(mx4_dequantize, 7) {
 // x, T, K, pair_to_sorted, k_max, P, expert_offsets, E, codes, scales, stream
 FUNCTION(mx4_quantize_rows, 11) {
   const int T = in.num(1), K = in.num(2), k = in.num(4), P = in.num(5), E = in.num(7);
-  in.mx4(8, 9, P, K, P / 128 + E, "codes");
-  const int d = in.dtype(0);
+  in.mx4(8, 9, P, K, P / 128 + (long long)E, "codes");
+  in.holds(3, at::kInt, times(T, k), "pair_to_sorted");
+  in.holds(6, at::kInt, E + 1LL, "expert_offsets");
+  const int d = in.values(0, times(T, K), "x");
   void *x = in.ptr(0), *m = in.ptr(3), *o = in.ptr(6), *c = in.ptr(8), *s = in.ptr(9), *st = in.stream(10);
   return run(in, [&] { return semmoe_mx4_quantize_rows(x, d, T, K, i32(m), k, P, i32(o), E, u8(c), u8(s), st); });
 }
@@ -243,9 +276,10 @@ FUNCTION(mx4_quantize_rows, 11) {
 // a, a_scales, expert_offsets, phys_to_expert, b, b_scales, P, E, N, K, out, stream
 FUNCTION(mx4_grouped_gemm, 12) {
   const int P = in.num(6), E = in.num(7), N = in.num(8), K = in.num(9);
-  in.mx4(0, 1, P, K, P / 128 + E, "a");
-  in.mx4(4, 5, (long long)E * N, K, E * tiles_of(N), "b");
-  const int d = in.dtype(10);
+  in.mx4(0, 1, P, K, P / 128 + (long long)E, "a");
+  in.mx4(4, 5, times(E, N), K, times(E, tiles_of(N)), "b");
+  in.groups(2, 3, E);
+  const int d = in.values(10, times(P, N), "out");
   void *a = in.ptr(0), *as = in.ptr(1), *o = in.ptr(2), *e = in.ptr(3), *b = in.ptr(4), *bs = in.ptr(5),
        *y = in.ptr(10), *st = in.stream(11);
   return run(in, [&] {
@@ -256,10 +290,11 @@ FUNCTION(mx4_grouped_gemm, 12) {
 // x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I, y_perm, ws, stream
 FUNCTION(mx4_grouped_ffn, 15) {
   const int P = in.num(8), E = in.num(9), H = in.num(10), I = in.num(11);
-  in.mx4(0, 1, P, H, P / 128 + E, "x");
-  in.mx4(4, 5, 2LL * E * I, H, 2LL * E * tiles_of(I), "w13");
-  in.mx4(6, 7, (long long)E * H, I, E * tiles_of(H), "w2");
-  in.holds(12, at::kBFloat16, (long long)P * H, "y_perm");
+  in.mx4(0, 1, P, H, P / 128 + (long long)E, "x");
+  in.mx4(4, 5, times(2, E, I), H, times(2, E, tiles_of(I)), "w13");
+  in.mx4(6, 7, times(E, H), I, times(E, tiles_of(H)), "w2");
+  in.groups(2, 3, E);
+  in.holds(12, at::kBFloat16, times(P, H), "y_perm");
   void *x = in.ptr(0), *xs = in.ptr(1), *o = in.ptr(2), *e = in.ptr(3), *a = in.ptr(4), *as = in.ptr(5),
        *b = in.ptr(6), *bs = in.ptr(7), *y = in.ptr(12), *ws = in.ptr(13), *st = in.stream(14);
   const size_t n = in.bytes(13);
@@ -275,7 +310,18 @@ FUNCTION(route_select, 23) {
             T = in.num(13), H = in.num(14), E = in.num(15), k = in.num(16);
   const float scale = in.get<float>(10);
   in.holds(5, at::kFloat, E, "bias");
-  const int xd = in.dtype(0), wd = in.a[21] == Py_None ? in.dtype(1) : in.num(21);
+  in.holds(2, at::kFloat, times(T, E), "logits_in");
+  in.holds(3, at::kFloat, times(T, E), "logits_out");
+  in.holds(11, at::kInt, T, "k_per_token");
+  in.holds(17, at::kInt, times(T, k), "topk_idx");
+  in.holds(18, at::kFloat, times(T, k), "topk_w");
+  in.holds(19, at::kInt, (long long)(semmoe_pair_counts_size(T, E) / 4), "pair_counts");
+  const bool product = in.none(2);  // else x and w_router are not read
+  const int xd = in.values(0, product ? times(T, H) : 0, "x");
+  int wd = SEMMOE_F32;
+  if (in.none(21)) wd = in.values(1, product ? times(E, H) : 0, "w_router");
+  else if ((wd = in.num(21)) == SEMMOE_F32_SPLIT) in.holds_bytes(1, product ? semmoe_route_split_size(H, E) : 0, "w_router");
+  else in.holds(1, wd == SEMMOE_BF16 ? at::kBFloat16 : at::kFloat, product ? times(E, H) : 0, "w_router");
   void *x = in.ptr(0), *w = in.ptr(1), *li = in.ptr(2), *lo = in.ptr(3), *b = in.ptr(5), *kpt = in.ptr(11),
        *idx = in.ptr(17), *tw = in.ptr(18), *pc = in.ptr(19), *ws = in.ptr(20), *st = in.stream(22);
   const size_t n = in.bytes(20);
