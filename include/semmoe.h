@@ -238,7 +238,7 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
  * scale       finite
  * other arguments as semmoe_route; ws of semmoe_route_select_workspace_size() bytes
  *             (may be NULL when that size is 256)
- * Limits: 1 <= E <= 256, 1 <= k_max <= topk_group * E / n_group.
+ * Limits: 1 <= E <= 256, 1 <= k_max <= topk_group * E / n_group, T * E < 2^31, T <= 2^31 - 2^16.
  */
 enum { SEMMOE_SCORE_SIGMOID = 0, SEMMOE_SCORE_SOFTMAX = 1 };
 size_t semmoe_route_select_workspace_size(int T, int H, int E, int x_dtype, int w_dtype);
@@ -536,7 +536,7 @@ int semmoe_combine(const void* y_perm, const int32_t* pair_to_sorted, const floa
  *         Column blocks past K hold 0.
  * semmoe_mx4_scales_size(rows, K, groups) is enough for any split of `rows`
  * rows into `groups` groups: (rows / 128 + groups) ceil(K/128) 512 bytes.
- * Limits: K % 32 == 0; all pointers 16-byte aligned.
+ * Limits: K % 32 == 0; all pointers 16-byte aligned; at most 2^31 - 2^16 rows (pairs, tokens) a call.
  */
 size_t semmoe_mx4_scales_size(int rows, int K, int groups);
 

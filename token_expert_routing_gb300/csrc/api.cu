@@ -193,6 +193,9 @@ int semmoe_route_hier(const void* x, int x_dtype, const void* w_parent, int w_dt
                      "semmoe_route_hier");
 }
 
+// Rows of one call: a kernel's next row after the last, and the rows rounded up to a tile, still fit 32 bits.
+static constexpr long long kMaxRows = (1LL << 31) - (1 << 16);
+
 size_t semmoe_route_select_workspace_size(int T, int H, int E, int x_dtype, int w_dtype) {
   if (T < 0 || H < 1 || E < 1 || E > 256 || !valid_dtype(x_dtype) || !valid_router_dtype(w_dtype, x_dtype, H)) return 0;
   const size_t b = route_select_ws_bytes(T, H, E, x_dtype, w_dtype);
@@ -208,7 +211,7 @@ int semmoe_route_select(const void* x, int x_dtype, const void* w_router, int w_
   REQUIRE(T >= 0, "%s: T = %d < 0", fn, T);
   REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
   REQUIRE(k_max >= 1 && k_max <= E, "%s: k_max = %d outside [1, E = %d]", fn, k_max, E);
-  REQUIRE((long long)T * E < (1LL << 31), "%s: T * E too large", fn);
+  REQUIRE((long long)T * E < (1LL << 31) && T <= kMaxRows, "%s: T * E too large", fn);
   REQUIRE(score == SEMMOE_SCORE_SIGMOID || score == SEMMOE_SCORE_SOFTMAX, "%s: bad score %d", fn, score);
   REQUIRE(n_group >= 1 && E % n_group == 0, "%s: n_group = %d does not divide E = %d", fn, n_group, E);
   REQUIRE(topk_group >= 1 && topk_group <= n_group, "%s: topk_group = %d outside [1, n_group = %d]", fn, topk_group,
@@ -538,7 +541,7 @@ static int check_mx4_matrix(const char* fn, int groups, int group_rows, int K, c
   REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
   REQUIRE(groups >= 1 && group_rows >= 0, "%s: bad sizes groups=%d group_rows=%d", fn, groups, group_rows);
   REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
-  REQUIRE((long long)groups * group_rows < (1LL << 31), "%s: groups * group_rows too large", fn);
+  REQUIRE((long long)groups * group_rows <= kMaxRows, "%s: groups * group_rows too large", fn);
   if (group_rows == 0) return SEMMOE_OK;
   REQUIRE(full && codes && scales, "%s: null pointer", fn);
   REQUIRE(aligned(full, 16) && aligned(codes, 16) && aligned(scales, 16), "%s: pointers must be 16-byte aligned", fn);
@@ -573,7 +576,7 @@ int semmoe_mx4_quantize_rows(const void* x, int dtype, int T, int K, const int32
   REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
   REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
   REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
-  REQUIRE(T >= 0 && k_max >= 1 && (long long)T * k_max < (1LL << 31), "%s: bad sizes T=%d k_max=%d", fn, T, k_max);
+  REQUIRE(T >= 0 && k_max >= 1 && (long long)T * k_max <= kMaxRows, "%s: bad sizes T=%d k_max=%d", fn, T, k_max);
   REQUIRE(P >= 0 && P <= (long long)T * k_max, "%s: P = %d outside [0, T * k_max]", fn, P);
   if (P == 0) return SEMMOE_OK;
   REQUIRE(x && pair_to_sorted && expert_offsets && codes && scales, "%s: null pointer", fn);
@@ -589,7 +592,7 @@ static int check_mx4_product(const char* fn, int P, int E, int N, int K, const v
                              const void* offsets, const void* experts, const void* b, const void* b_scales,
                              const void* out) {
   REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
-  REQUIRE(P >= 0, "%s: P = %d < 0", fn, P);
+  REQUIRE(P >= 0 && P <= kMaxRows, "%s: P = %d outside [0, 2^31 - 2^16]", fn, P);
   REQUIRE(K >= 32 && K % 32 == 0, "%s: K = %d is not a positive multiple of 32", fn, K);
   REQUIRE(N >= 8 && N % 8 == 0, "%s: N = %d is not a positive multiple of 8", fn, N);
   // tile counts and the tensor maps' coordinates are 32-bit
