@@ -20,16 +20,20 @@
 // A stage's scales have TMEM columns of their own, so they are overwritten only after
 // the commit of the MMAs that read them.
 //
-// What bounds it (GB300).  Long groups: the operands' way into shared memory.  A stage is
-// 51 KB for 67 MFLOP, four of them in flight; the MMAs of a stage take 0.2 us at the
-// tensor cores' rate, a stage takes 0.45-0.5 us with its loads and no output.  32768 rows x
-// 2048 x 1536: 53 us, 3.9 PFLOP/s; 45 us with no output stored, 42 with nothing loaded either.
+// What bounds it (GB300).  Long groups: each stage's own time.  A stage is 51 KB for
+// 16.8 MFLOP, four of them in flight; its MMAs take 0.2 us at the tensor cores' rate, the
+// stage 0.45-0.5 us with no output.  32768 rows x 2048 x 1536: 53 us, 3.9 PFLOP/s; 45 us
+// with no output stored, 42 with nothing loaded either, so the loads are 3 us of it, the stores 8, and
+// more than half of what is left is neither, nor the MMAs' own rate: the scale copies in front of
+// a stage's MMAs, those MMAs' reads of shared memory (64 KB a stage) and the commit and wait between
+// stages have not been told apart.
 // 131072 rows x 768 x 2048 (537 MB of bf16 out): 130 us, 5.4 TB/s.  Pairs of CTAs
-// (cta_group::2, M256, 35 KB a stage and CTA, five in flight) were built and measured
-// slower, 61 us on the first and 178 us on the second: a stage's round trip between two
-// SMs costs more than its smaller copies save.  Three stages of this form: 68 and 146 us.
-// Few rows per group: the weights' bytes, 64 experts of 2048 x 1408 and 384 rows in 22 us
-// (98 MB, 4.4 TB/s, of which some 7 us are the launch, the first loads and the last tiles).
+// (cta_group::2, M256, 35 KB a stage and CTA, five in flight) took 61 us on the first and
+// 178 us on the second when stages were still released in twos and descriptors built for each
+// MMA; they were not measured again after this form had both mended.  Three stages of this
+// form: 68 and 146 us.
+// Few rows per group: the weights' bytes, 64 experts of 2048 x 1408 and 384 rows in 23 us
+// (98 MB, 4.3 TB/s, of which some 7 us are the launch, the first loads and the last tiles).
 //
 // Every wait is bounded; a wait that runs out sets the timeout bit of the device
 // error word and an abort flag, after which every role stops, loads and MMAs in
