@@ -22,7 +22,9 @@
  *                           (semmoe_mx4_quantize, _quantize_rows, _dequantize, _grouped_gemm)
  *   semmoe_shared_ffn       dense SwiGLU of the shared experts (optional)
  *   semmoe_combine          un-permute and gate-weighted sum
+ *   semmoe_combine_norm     the same with the norm after the layer, gate, residual and next norm
  * and, around the layer:
+ *   semmoe_norm             the norm before it
  *   semmoe_dp_schedule      requests placed on data-parallel ranks by affinity
  *   semmoe_transition_lookup next layer's rank predicted from this layer's experts
  *
@@ -517,6 +519,52 @@ int semmoe_shared_ffn(const void* x, const void* ws13, const void* ws2, int dtyp
 int semmoe_combine(const void* y_perm, const int32_t* pair_to_sorted, const float* topk_w,
                    const void* y_shared, int dtype, int T, int H, int k_max, int P,
                    void* out, void* stream);
+
+/*
+ * semmoe_norm -- the norm before the layer (or any block): every row of x by its
+ * root mean square, or about its mean:
+ *   m = 0 (SEMMOE_NORM_RMS) or the mean of the row (SEMMOE_NORM_LAYER)
+ *   out[t,h] = (x[t,h] - m) / sqrt(mean_h (x[t,h] - m)^2 + eps) * (weight_offset + weight[h]) + bias[h]
+ * in fp32, rounded once.  The pages have no counterpart: models put a norm in front of the layer.
+ *
+ * x       [device] [T,H] dtype;  out [device] [T,H] dtype, which may be x itself
+ * weight  [device] [H] w_dtype (SEMMOE_F32 or SEMMOE_BF16) or NULL (1; weight_offset is then not used)
+ * bias    [device] [H] w_dtype or NULL
+ * eps     finite, above 0
+ * Limits: H * element size a multiple of 16 and at most 32768; pointers 16-byte aligned.
+ */
+enum { SEMMOE_NORM_NONE = 0, SEMMOE_NORM_RMS = 1, SEMMOE_NORM_LAYER = 2 };
+int semmoe_norm(const void* x, int dtype, int T, int H, int kind, const void* weight, const void* bias, int w_dtype,
+                float weight_offset, float eps, void* out, void* stream);
+
+/*
+ * semmoe_combine_norm -- semmoe_combine and what stands between the layer and the
+ * next block, in one pass over the rows:
+ *   y[t] = y_shared[t] + sum_{j<k_t} topk_w[t,j] * y_perm[pair_to_sorted[t*k_max+j]]    (as semmoe_combine)
+ *   out[t] = residual_scale * residual[t] + block_scale * gate * post_norm(y[t])
+ *   next_out[t] = next_norm(out[t])
+ * all in fp32, each output rounded once (next_norm sees out before it is rounded).
+ *
+ * y_perm .. P  as semmoe_combine.  pair_to_sorted NULL: y_perm holds the T rows in
+ *              token order (a dense block, such as the attention before the layer);
+ *              topk_w, k_max and P are then not used
+ * post_kind    norm after the block: SEMMOE_NORM_NONE, _RMS or _LAYER, with post_weight and post_bias
+ * next_kind    norm before the next block, with next_weight and next_bias; SEMMOE_NORM_NONE: next_out is not written
+ * w_dtype, weight_offset, eps  of both norms, as semmoe_norm
+ * gate         [device] [gate_rows,H] gate_dtype (SEMMOE_F32 or SEMMOE_BF16) or NULL (1);
+ *              gate_rows 1 (a value per channel) or T (per token and channel)
+ * residual     [device] [T,H] dtype, or NULL for none
+ * out          [device] [T,H] dtype, which may be the residual's own buffer
+ * next_out     [device] [T,H] dtype, apart from every other buffer; NULL if next_kind is SEMMOE_NORM_NONE
+ * Limits: H * element size a multiple of 16 and at most 32768; pointers 16-byte aligned; scales finite.
+ * A sorted row >= P sets SEMMOE_DEVERR_PAIRS and its slot is skipped.
+ */
+int semmoe_combine_norm(const void* y_perm, const int32_t* pair_to_sorted, const float* topk_w, const void* y_shared,
+                        int dtype, int T, int H, int k_max, int P, int post_kind, const void* post_weight,
+                        const void* post_bias, int next_kind, const void* next_weight, const void* next_bias,
+                        int w_dtype, float weight_offset, float eps, const void* gate, int gate_dtype, int gate_rows,
+                        float block_scale, const void* residual, float residual_scale, void* out, void* next_out,
+                        void* stream);
 
 /*
  * 4-bit microscaled values ("mx4"): 32 consecutive values of a row share one

@@ -26,6 +26,8 @@ SEMMOE_FORM_DEFAULT, SEMMOE_FORM_SINGLE, SEMMOE_FORM_PAIR1, SEMMOE_FORM_PAIR, SE
     SEMMOE_FORM_CUDA_CORE, SEMMOE_FORM_FUSED = range(7)
 # scores of semmoe_route_select
 SEMMOE_SCORE_SIGMOID, SEMMOE_SCORE_SOFTMAX = 0, 1
+# norms of semmoe_norm and semmoe_combine_norm
+SEMMOE_NORM_NONE, SEMMOE_NORM_RMS, SEMMOE_NORM_LAYER = range(3)
 # device error word bits (semmoe_check_errors)
 SEMMOE_DEVERR_EXPERT, SEMMOE_DEVERR_TOKEN_ID, SEMMOE_DEVERR_LUT, SEMMOE_DEVERR_K, SEMMOE_DEVERR_PAIRS, \
     SEMMOE_DEVERR_TIMEOUT, SEMMOE_DEVERR_NONFINITE, SEMMOE_DEVERR_OFFSETS, SEMMOE_DEVERR_RANK = \
@@ -72,6 +74,9 @@ SIGNATURES = {
     "semmoe_shared_ffn_workspace_size": (_sz, [_i, _i, _i]),
     "semmoe_shared_ffn": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_combine": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
+    "semmoe_norm": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _i, _f, _f, _vp, _vp]),
+    "semmoe_combine_norm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _f, _f, _vp, _i,
+                                 _i, _f, _vp, _f, _vp, _vp, _vp]),
     "semmoe_mx4_scales_size": (_sz, [_i, _i, _i]),
     "semmoe_mx4_quantize": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "semmoe_mx4_dequantize": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp]),
@@ -354,6 +359,22 @@ def semmoe_shared_ffn(x, ws13, ws2, T, H, I_s, y_shared, ws, stream=None):
 def semmoe_combine(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, out, stream=None):
     _check(fast().semmoe_combine(y_perm, pair_to_sorted, topk_w, y_shared,
                                 dtype_code(out), T, H, k_max, P, out, _stream(stream)))
+
+
+def semmoe_norm(x, T, H, kind: int, weight, bias, weight_offset, eps, out, stream=None):
+    """out = the rows of x [T, H], normalised (SEMMOE_NORM_RMS or SEMMOE_NORM_LAYER), times weight_offset + weight, plus
+    bias; weight and bias [H] (fp32 or bf16, both of one type) or None.  ``out`` may be x."""
+    fast().norm(x, T, H, kind, weight, bias, weight_offset, eps, out, stream)
+
+
+def semmoe_combine_norm(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, post_kind: int, post_weight, post_bias,
+                        next_kind: int, next_weight, next_bias, weight_offset, eps, gate, gate_rows, block_scale, residual,
+                        residual_scale, out, next_out=None, stream=None):
+    """The combine (pair_to_sorted None: dense rows y_perm [T, H]), the norm after it, gate [gate_rows, H], residual,
+    and next_out = the next block's norm of out (see include/semmoe.h).  ``out`` may be the residual."""
+    fast().combine_norm(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, post_kind, post_weight, post_bias,
+                        next_kind, next_weight, next_bias, weight_offset, eps, gate, gate_rows, block_scale, residual,
+                        residual_scale, out, next_out, stream)
 
 
 def semmoe_dp_schedule(pred_rank, req_offsets, T, n_req, R, hist, req_rank, req_order, rank_req_offsets,

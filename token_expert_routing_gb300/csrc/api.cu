@@ -83,7 +83,7 @@ int semmoe_check_errors(void* stream, int* bits) {
   int b = 0;
   if (route_take_errors(s, &b) || permute_take_errors(s, &b) || ffn_take_errors(s, &b) ||
       combine_take_errors(s, &b) || schedule_take_errors(s, &b) || selftest_take_errors(s, &b) ||
-      mx4_take_errors(s, &b) || mx4_gemm_take_errors(s, &b))
+      mx4_take_errors(s, &b) || mx4_gemm_take_errors(s, &b) || norm_take_errors(s, &b))
     return cuda_status(cudaGetLastError(), "semmoe_check_errors: reading the device error word");
   if (bits != nullptr) *bits = b;
   if (b & SEMMOE_DEVERR_TIMEOUT) return fail(SEMMOE_ERR_DEVICE_TIMEOUT, "a bounded in-kernel wait ran out (bits 0x%x)", b);
@@ -494,6 +494,80 @@ int semmoe_combine(const void* y_perm, const int32_t* pair_to_sorted, const floa
   return cuda_status(launch_combine(y_perm, pair_to_sorted, topk_w, y_shared, dtype, T, H, k_max, P, out,
                                     static_cast<cudaStream_t>(stream)),
                      "semmoe_combine");
+}
+
+static bool is_finite(float v) { return v - v == 0.0f; }
+
+static int check_norm(const char* fn, const char* which, int kind, const void* weight, const void* bias, int w_dtype,
+                      float offset, float eps) {
+  REQUIRE(kind == SEMMOE_NORM_RMS || kind == SEMMOE_NORM_LAYER, "%s: bad %s %d", fn, which, kind);
+  REQUIRE((weight == nullptr && bias == nullptr) || valid_dtype(w_dtype), "%s: bad w_dtype %d", fn, w_dtype);
+  REQUIRE(is_finite(offset), "%s: weight_offset is not finite", fn);
+  REQUIRE(is_finite(eps) && eps > 0.0f, "%s: eps must be finite and above 0", fn);
+  REQUIRE(aligned(weight, 16) && aligned(bias, 16), "%s: weights and biases must be 16-byte aligned", fn);
+  return SEMMOE_OK;
+}
+
+static int check_rows(const char* fn, int dtype, int T, int H) {
+  REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
+  REQUIRE(T >= 0 && T <= kMaxRows, "%s: T = %d outside [0, 2^31 - 2^16]", fn, T);
+  REQUIRE(H >= 1 && (H * elem_size(dtype)) % 16 == 0 && H * elem_size(dtype) <= (size_t)kNormMaxRowBytes,
+          "%s: H = %d: rows are a multiple of 16 bytes, at most %d", fn, H, kNormMaxRowBytes);
+  return SEMMOE_OK;
+}
+
+int semmoe_norm(const void* x, int dtype, int T, int H, int kind, const void* weight, const void* bias, int w_dtype,
+                float weight_offset, float eps, void* out, void* stream) {
+  const char* fn = "semmoe_norm";
+  int rc = check_rows(fn, dtype, T, H);
+  if (rc == SEMMOE_OK) rc = check_norm(fn, "kind", kind, weight, bias, w_dtype, weight_offset, eps);
+  if (rc != SEMMOE_OK || T == 0) return rc;
+  REQUIRE(x && out, "%s: null pointer", fn);
+  REQUIRE(aligned(x, 16) && aligned(out, 16), "%s: pointers must be 16-byte aligned", fn);
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_norm(x, dtype, T, H, NormArgs{kind, weight, bias, w_dtype == SEMMOE_BF16, weight_offset, eps},
+                                 out, static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+int semmoe_combine_norm(const void* y_perm, const int32_t* pair_to_sorted, const float* topk_w, const void* y_shared,
+                        int dtype, int T, int H, int k_max, int P, int post_kind, const void* post_weight,
+                        const void* post_bias, int next_kind, const void* next_weight, const void* next_bias,
+                        int w_dtype, float weight_offset, float eps, const void* gate, int gate_dtype, int gate_rows,
+                        float block_scale, const void* residual, float residual_scale, void* out, void* next_out,
+                        void* stream) {
+  const char* fn = "semmoe_combine_norm";
+  int rc = check_rows(fn, dtype, T, H);
+  if (rc == SEMMOE_OK && post_kind != SEMMOE_NORM_NONE)
+    rc = check_norm(fn, "post_kind", post_kind, post_weight, post_bias, w_dtype, weight_offset, eps);
+  if (rc == SEMMOE_OK && next_kind != SEMMOE_NORM_NONE)
+    rc = check_norm(fn, "next_kind", next_kind, next_weight, next_bias, w_dtype, weight_offset, eps);
+  if (rc != SEMMOE_OK) return rc;
+  const bool dense = pair_to_sorted == nullptr;
+  if (!dense) {
+    REQUIRE(k_max >= 1 && P >= 0, "%s: bad sizes k_max=%d P=%d", fn, k_max, P);
+    REQUIRE((long long)T * k_max < (1LL << 31), "%s: T * k_max too large", fn);
+  }
+  REQUIRE(gate == nullptr || valid_dtype(gate_dtype), "%s: bad gate_dtype %d", fn, gate_dtype);
+  REQUIRE(gate == nullptr || gate_rows == 1 || gate_rows == T, "%s: gate_rows = %d is neither 1 nor T = %d", fn, gate_rows, T);
+  REQUIRE(is_finite(block_scale) && is_finite(residual_scale), "%s: scales must be finite", fn);
+  if (T == 0) return SEMMOE_OK;
+  REQUIRE(out && (dense || topk_w), "%s: null pointer", fn);
+  REQUIRE(y_perm || (!dense && P == 0), "%s: null y_perm", fn);
+  REQUIRE((next_kind != SEMMOE_NORM_NONE) == (next_out != nullptr), "%s: next_kind and next_out go together", fn);
+  REQUIRE(next_out == nullptr || (next_out != out && next_out != residual && next_out != y_perm && next_out != y_shared),
+          "%s: next_out is a buffer of its own", fn);
+  REQUIRE(aligned(y_perm, 16) && aligned(y_shared, 16) && aligned(gate, 16) && aligned(residual, 16) && aligned(out, 16) &&
+              aligned(next_out, 16),
+          "%s: pointers must be 16-byte aligned", fn);
+  REQUIRE(aligned(pair_to_sorted, 4) && aligned(topk_w, 4), "%s: misaligned table", fn);
+  CHECK_DEVICE(fn);
+  const bool wb = w_dtype == SEMMOE_BF16;
+  const CombineNorm a{y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P,
+                      NormArgs{post_kind, post_weight, post_bias, wb, weight_offset, eps},
+                      NormArgs{next_kind, next_weight, next_bias, wb, weight_offset, eps},
+                      gate, gate_dtype == SEMMOE_BF16, gate_rows, block_scale, residual, residual_scale, out, next_out};
+  return cuda_status(launch_combine_norm(a, dtype, static_cast<cudaStream_t>(stream)), fn);
 }
 
 int semmoe_dp_schedule(const int32_t* pred_rank, const int32_t* req_offsets, int T, int n_req, int R, int32_t* hist,

@@ -4,7 +4,7 @@
 //
 // One function per call of semmoe.h takes the C function's arguments, converted by
 // its types -- a pointer takes None, an address or a contiguous CUDA tensor -- and
-// returns its value.  The routing choice and the 4-bit operators also have entries
+// returns its value.  The routing choice, the 4-bit operators and the norms also have entries
 // named without the prefix, which take the tensors' types and sizes from the tensors, the
 // stream as a Stream, an address or None (the current one), and raise on an error.  They
 // refuse a tensor of another type than the call reads it as, or of fewer elements than it touches;
@@ -331,6 +331,55 @@ FUNCTION(route_select, 23) {
   });
 }
 
+// The code of the type that a norm's weight and bias share (SEMMOE_F32 where both are None).
+int norm_weights(In& in, int weight, int bias, int H, const char* what) {
+  const std::string w = what;
+  const int code = in.values(in.none(weight) ? bias : weight, H, (w + (in.none(weight) ? "bias" : "weight")).c_str());
+  in.holds(bias, code == SEMMOE_BF16 ? at::kBFloat16 : at::kFloat, H, (w + "bias").c_str());
+  return code;
+}
+
+// x, T, H, kind, weight, bias, weight_offset, eps, out, stream
+FUNCTION(norm, 10) {
+  const int T = in.num(1), H = in.num(2), kind = in.num(3);
+  const int d = in.values(0, times(T, H), "x"), wd = norm_weights(in, 4, 5, H, "");
+  const float off = in.get<float>(6), eps = in.get<float>(7);
+  in.holds(8, d == SEMMOE_BF16 ? at::kBFloat16 : at::kFloat, times(T, H), "out");
+  void *x = in.ptr(0), *w = in.ptr(4), *b = in.ptr(5), *o = in.ptr(8), *st = in.stream(9);
+  return run(in, [&] { return semmoe_norm(x, d, T, H, kind, w, b, wd, off, eps, o, st); });
+}
+
+// y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, post_kind, post_weight, post_bias, next_kind, next_weight,
+// next_bias, weight_offset, eps, gate, gate_rows, block_scale, residual, residual_scale, out, next_out, stream
+FUNCTION(combine_norm, 24) {
+  const int T = in.num(4), H = in.num(5), k = in.num(6), P = in.num(7), post = in.num(8), next = in.num(11),
+            g_rows = in.num(17);
+  const float off = in.get<float>(14), eps = in.get<float>(15), bs = in.get<float>(18), rs = in.get<float>(20);
+  const bool dense = in.none(1);
+  const int d = in.values(21, times(T, H), "out");
+  const at::ScalarType type = d == SEMMOE_BF16 ? at::kBFloat16 : at::kFloat;
+  in.holds(0, type, times(dense ? T : P, H), "y_perm");
+  in.holds(1, at::kInt, times(T, k), "pair_to_sorted");
+  if (!dense) in.holds(2, at::kFloat, times(T, k), "topk_w");
+  in.holds(3, type, times(T, H), "y_shared");
+  in.holds(19, type, times(T, H), "residual");
+  in.holds(22, type, times(T, H), "next_out");
+  const int gd = in.values(16, times(g_rows, H), "gate");
+  const int pd = norm_weights(in, 9, 10, H, "post_"), nd = norm_weights(in, 12, 13, H, "next_");
+  const bool has_post = !in.none(9) || !in.none(10), has_next = !in.none(12) || !in.none(13);
+  if (in.ok && has_post && has_next && pd != nd) {
+    PyErr_SetString(PyExc_ValueError, "the weights of both norms are of one type");
+    return nullptr;
+  }
+  void *y = in.ptr(0), *m = in.ptr(1), *tw = in.ptr(2), *ys = in.ptr(3), *pw = in.ptr(9), *pb = in.ptr(10),
+       *nw = in.ptr(12), *nb = in.ptr(13), *g = in.ptr(16), *r = in.ptr(19), *o = in.ptr(21), *no = in.ptr(22),
+       *st = in.stream(23);
+  return run(in, [&] {
+    return semmoe_combine_norm(y, i32(m), f32(tw), ys, d, T, H, k, P, post, pw, pb, next, nw, nb, has_post ? pd : nd, off,
+                               eps, g, gd, g_rows, bs, r, rs, o, no, st);
+  });
+}
+
 // The callable that raises for a status.
 PyObject* set_raise(PyObject*, PyObject* f) {
   Py_INCREF(f);
@@ -373,6 +422,8 @@ PyMethodDef methods[] = {
     ENTRY(semmoe_mx4_grouped_gemm),
     ENTRY(semmoe_mx4_grouped_ffn_workspace_size),
     ENTRY(semmoe_mx4_grouped_ffn),
+    ENTRY(semmoe_norm),
+    ENTRY(semmoe_combine_norm),
     ENTRY(semmoe_dp_schedule),
     ENTRY(semmoe_transition_lookup),
     ENTRY(semmoe_selftest_bounded_wait),
@@ -384,6 +435,8 @@ PyMethodDef methods[] = {
     METHOD("mx4_grouped_gemm", &mx4_grouped_gemm),
     METHOD("mx4_grouped_ffn", &mx4_grouped_ffn),
     METHOD("route_select", &route_select),
+    METHOD("norm", &norm),
+    METHOD("combine_norm", &combine_norm),
     {"set_raise", &set_raise, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -21,6 +21,7 @@ int schedule_take_errors(cudaStream_t s, int* bits);
 int selftest_take_errors(cudaStream_t s, int* bits);
 int mx4_take_errors(cudaStream_t s, int* bits);
 int mx4_gemm_take_errors(cudaStream_t s, int* bits);
+int norm_take_errors(cudaStream_t s, int* bits);
 cudaError_t launch_selftest_bounded_wait(cudaStream_t s);
 cudaError_t launch_selftest_fused_ready_wait(const void* x, const void* w13, const void* w2, int P, int H, int I,
                                              void* y, void* ws, cudaStream_t s);
@@ -139,6 +140,32 @@ cudaError_t launch_combine_finish(const float* acc, const void* y_shared, int T,
 cudaError_t launch_combine(const void* y_perm, const int32_t* pair_to_sorted, const float* topk_w,
                            const void* y_shared, int dtype, int T, int H, int k_max, int P,
                            void* out, cudaStream_t s);
+
+// Norms around the layer (norm.cu).
+struct NormArgs {
+  int kind;                      // SEMMOE_NORM_*
+  const void *weight, *bias;     // [H] or NULL
+  bool w_bf16;
+  float offset, eps;
+};
+constexpr int kNormMaxRowBytes = 32768;
+cudaError_t launch_norm(const void* x, int dtype, int T, int H, const NormArgs& n, void* out, cudaStream_t s);
+struct CombineNorm {
+  const void* y_perm;
+  const int32_t* pair_to_sorted;  // NULL: y_perm holds the T rows themselves
+  const float* topk_w;
+  const void* y_shared;
+  int T, H, k_max, P;
+  NormArgs post, next;
+  const void* gate;               // [gate_rows, H], gate_rows 1 or T, or NULL
+  bool gate_bf16;
+  int gate_rows;
+  float block_scale;
+  const void* residual;           // or NULL
+  float residual_scale;
+  void *out, *next_out;
+};
+cudaError_t launch_combine_norm(const CombineNorm& a, int dtype, cudaStream_t s);
 
 cudaError_t launch_dp_schedule(const int32_t* pred, const int32_t* off, int T, int n_req, int R, int32_t* hist,
                                int32_t* req_rank, int32_t* req_order, int32_t* rank_req_offsets,
