@@ -20,6 +20,8 @@
  *   semmoe_grouped_ffn_gather  the same, reading x through the permutation
  *   semmoe_mx4_grouped_ffn  the same on 4-bit microscaled rows and weights
  *                           (semmoe_mx4_quantize, _quantize_rows, _dequantize, _grouped_gemm)
+ *   semmoe_w4_grouped_ffn   the same on 4-bit weights with group scales and bf16 rows
+ *                           (semmoe_w4_quantize, _dequantize, _grouped_gemm)
  *   semmoe_shared_ffn       dense SwiGLU of the shared experts (optional)
  *   semmoe_combine          un-permute and gate-weighted sum
  *   semmoe_combine_norm     the same with the norm after the layer, gate, residual and next norm
@@ -647,6 +649,63 @@ int semmoe_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int3
                            const int32_t* phys_to_expert, const uint8_t* w13, const uint8_t* w13_scales,
                            const uint8_t* w2, const uint8_t* w2_scales, int P, int E, int H, int I, void* y_perm,
                            void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 4-bit weights with group scales ("w4"), for bf16 activations: integer codes
+ * 0..15, and for each group of `group` columns of a row a scale and a zero point:
+ *   w[r,k] = (code[r,k] - zero[r,k/group]) * scale[r,k/group]
+ * The pages have no counterpart: it is the form of most 4-bit checkpoints.
+ *
+ * codes   row-major [rows, K/2] bytes, two codes each, the lower column in the low four bits
+ * scales  row-major [rows, K/group] scale_dtype (SEMMOE_F32 or SEMMOE_BF16)
+ * zeros   row-major [rows, K/group] bytes 0..15 (the low four bits are read), or NULL: 8 everywhere
+ * Limits: group 32, 64 or a multiple of 128; K % group == 0; pointers to codes, rows and outputs 16-byte
+ * aligned, to scales aligned to their type; at most 2^31 - 2^16 rows a call.
+ *
+ * semmoe_w4_quantize -- codes, scales and zero points of x [rows,K] (fp32 or bf16).  With zeros, a group's
+ * range lo = min(0, min x) .. hi = max(0, max x) is covered: scale = (hi - lo) / 15, zero = round(-lo / scale);
+ * without, scale = max |x| / 7.  The scale is rounded to its type first; then code = round(x / scale) + zero
+ * (8 without zeros), within 0..15; ties go to the even number.  A group of zeros has scale 0, one
+ * that holds NaN or an infinity has scale NaN.
+ * semmoe_w4_dequantize -- the values they stand for, rounded to out_dtype.
+ */
+int semmoe_w4_quantize(const void* x, int dtype, int rows, int K, int group, uint8_t* codes, void* scales,
+                       int scale_dtype, uint8_t* zeros, void* stream);
+int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int rows, int K,
+                         int group, void* out, int out_dtype, void* stream);
+
+/*
+ * semmoe_w4_grouped_gemm -- bf16 rows times their expert's 4-bit matrix: rows
+ * [expert_offsets[b], expert_offsets[b+1]) with expert e = phys_to_expert[b]:
+ *   out[q, n] = sum_k x[q, k] w[e, n, k]      (fp32 accumulation, stored in bf16)
+ * From a single row (a matrix-vector product: E = 1, P = 1) to any number.
+ *
+ * x       [device] [P,K] bf16
+ * codes, scales, zeros  [device] E matrices of N rows
+ * out     [device] [P,N] bf16
+ * Limits: N % 8 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn (a group that is skipped leaves its rows of
+ * out as they were).
+ */
+int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert,
+                           const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int P, int E,
+                           int N, int K, int group, void* out, void* stream);
+
+/*
+ * semmoe_w4_grouped_ffn -- semmoe_grouped_ffn (bf16) on 4-bit weights:
+ *   h = silu(x W1_e^T) * (x W3_e^T), stored in bf16;  y = h W2_e^T
+ *
+ * x       [device] [P,H] bf16
+ * w13, w13_scales, w13_zeros  [device] [E,2I,H] (gate rows, then up rows);  w2 ...  [device] [E,H,I]
+ *         (both with zeros or both without, one scale_dtype, one group)
+ * y_perm  [device] [P,H] bf16 out
+ * ws      [device] workspace of semmoe_w4_grouped_ffn_workspace_size() bytes (256-byte aligned)
+ * Limits: H and I multiples of group, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn.
+ */
+size_t semmoe_w4_grouped_ffn_workspace_size(int P, int I);
+int semmoe_w4_grouped_ffn(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert,
+                          const uint8_t* w13, const void* w13_scales, const uint8_t* w13_zeros, const uint8_t* w2,
+                          const void* w2_scales, const uint8_t* w2_zeros, int scale_dtype, int P, int E, int H, int I,
+                          int group, void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * semmoe_dp_schedule -- online inter-request scheduling of Attention-DP: a

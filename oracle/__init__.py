@@ -36,3 +36,4 @@ from .prism import hier_route, split_expert_weights, sub_scores  # noqa: F401
 from .mx4 import mx4_encode, mx4_grouped_ffn, mx4_grouped_product, mx4_round, mx4_values  # noqa: F401
 from .select import choice_scores, route_select, scores  # noqa: F401
 from .norm import block_rows, combine_norm, norm  # noqa: F401
+from .w4 import w4_encode, w4_grouped_ffn, w4_grouped_product, w4_values  # noqa: F401

@@ -84,6 +84,11 @@ SIGNATURES = {
     "semmoe_mx4_grouped_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]),
     "semmoe_mx4_grouped_ffn_workspace_size": (_sz, [_i, _i, _i]),
     "semmoe_mx4_grouped_ffn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "semmoe_w4_quantize": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]),
+    "semmoe_w4_dequantize": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _vp, _i, _vp]),
+    "semmoe_w4_grouped_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
+    "semmoe_w4_grouped_ffn_workspace_size": (_sz, [_i, _i]),
+    "semmoe_w4_grouped_ffn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_selftest_bounded_wait": (_i, [_vp]),
     "semmoe_selftest_fused_ready_wait": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "semmoe_selftest_mx4_wait": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
@@ -422,6 +427,36 @@ def semmoe_mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13
     """SwiGLU experts on 4-bit rows and weights, y_perm [P, H] bf16."""
     fast().mx4_grouped_ffn(x, x_scales, expert_offsets, phys_to_expert, w13, w13_scales, w2, w2_scales, P, E, H, I,
                            y_perm, ws, stream)
+
+
+def semmoe_w4_quantize(x, rows, K, group, codes, scales, zeros=None, stream=None):
+    """x [rows, K] (fp32 or bf16) to 4-bit codes [rows, K/2], scales [rows, K/group] (fp32 or bf16) and, unless None,
+    zero points [rows, K/group] (uint8)."""
+    fast().w4_quantize(x, rows, K, group, codes, scales, zeros, stream)
+
+
+def semmoe_w4_dequantize(codes, scales, zeros, rows, K, group, out, stream=None):
+    """The values that codes, scales and zero points (None: 8) stand for, in out's type (fp32 or bf16)."""
+    fast().w4_dequantize(codes, scales, zeros, rows, K, group, out, stream)
+
+
+def semmoe_w4_grouped_gemm(x, expert_offsets, phys_to_expert, codes, scales, zeros, P, E, N, K, group, out, stream=None):
+    """bf16 rows x [P, K], sorted by expert, times their expert's 4-bit matrix [N, K] into out [P, N] (bf16)."""
+    fast().w4_grouped_gemm(x, expert_offsets, phys_to_expert, codes, scales, zeros, P, E, N, K, group, out, stream)
+
+
+def semmoe_w4_grouped_ffn_workspace_size(P, I) -> int:
+    return fast().semmoe_w4_grouped_ffn_workspace_size(P, I)
+
+
+def semmoe_w4_grouped_ffn(x, expert_offsets, phys_to_expert, w13, w13_scales, w13_zeros, w2, w2_scales, w2_zeros, P, E, H,
+                          I, group, y_perm, ws=None, stream=None):
+    """SwiGLU experts on 4-bit weights, x and y_perm [P, H] bf16.  ``ws`` defaults to a fresh workspace of the size
+    the library asks for."""
+    if ws is None:
+        ws = _workspace(fast().semmoe_w4_grouped_ffn_workspace_size(P, I), y_perm.device, stream)
+    fast().w4_grouped_ffn(x, expert_offsets, phys_to_expert, w13, w13_scales, w13_zeros, w2, w2_scales, w2_zeros, P, E, H,
+                          I, group, y_perm, ws, stream)
 
 
 def semmoe_selftest_bounded_wait(stream=None):

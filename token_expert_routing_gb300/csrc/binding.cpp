@@ -380,6 +380,65 @@ FUNCTION(combine_norm, 24) {
   });
 }
 
+// Codes, scales (their code is returned) and zero points of `rows` rows of K columns.
+int w4(In& in, int codes, int scales, int zeros, long long rows, int K, int group, const char* what) {
+  const std::string w = what;
+  const long long n = group > 0 ? times(rows, K / group) : 0;
+  in.holds(codes, at::kByte, times(rows, K / 2), (w + "codes").c_str());
+  in.holds(zeros, at::kByte, n, (w + "zeros").c_str());
+  return in.values(scales, n, (w + "scales").c_str());
+}
+
+// x, rows, K, group, codes, scales, zeros, stream
+FUNCTION(w4_quantize, 8) {
+  const int n = in.num(1), K = in.num(2), g = in.num(3);
+  const int d = in.values(0, times(n, K), "x"), sd = w4(in, 4, 5, 6, n, K, g, "");
+  void *x = in.ptr(0), *c = in.ptr(4), *s = in.ptr(5), *z = in.ptr(6), *st = in.stream(7);
+  return run(in, [&] { return semmoe_w4_quantize(x, d, n, K, g, u8(c), s, sd, u8(z), st); });
+}
+
+// codes, scales, zeros, rows, K, group, out, stream
+FUNCTION(w4_dequantize, 8) {
+  const int n = in.num(3), K = in.num(4), g = in.num(5);
+  const int d = in.values(6, times(n, K), "out"), sd = w4(in, 0, 1, 2, n, K, g, "");
+  void *c = in.ptr(0), *s = in.ptr(1), *z = in.ptr(2), *o = in.ptr(6), *st = in.stream(7);
+  return run(in, [&] { return semmoe_w4_dequantize(u8(c), s, sd, u8(z), n, K, g, o, d, st); });
+}
+
+// x, expert_offsets, phys_to_expert, codes, scales, zeros, P, E, N, K, group, out, stream
+FUNCTION(w4_grouped_gemm, 13) {
+  const int P = in.num(6), E = in.num(7), N = in.num(8), K = in.num(9), g = in.num(10);
+  in.holds(0, at::kBFloat16, times(P, K), "x");
+  in.groups(1, 2, E);
+  const int sd = w4(in, 3, 4, 5, times(E, N), K, g, "");
+  in.holds(11, at::kBFloat16, times(P, N), "out");
+  void *x = in.ptr(0), *o = in.ptr(1), *e = in.ptr(2), *c = in.ptr(3), *s = in.ptr(4), *z = in.ptr(5), *y = in.ptr(11),
+       *st = in.stream(12);
+  return run(in, [&] {
+    return semmoe_w4_grouped_gemm(x, i32(o), i32(e), u8(c), s, sd, u8(z), P, E, N, K, g, y, st);
+  });
+}
+
+// x, expert_offsets, phys_to_expert, w13, w13_scales, w13_zeros, w2, w2_scales, w2_zeros, P, E, H, I, group, y_perm, ws,
+// stream
+FUNCTION(w4_grouped_ffn, 17) {
+  const int P = in.num(9), E = in.num(10), H = in.num(11), I = in.num(12), g = in.num(13);
+  in.holds(0, at::kBFloat16, times(P, H), "x");
+  in.groups(1, 2, E);
+  const int sd = w4(in, 3, 4, 5, times(2, E, I), H, g, "w13 "), sd2 = w4(in, 6, 7, 8, times(E, H), I, g, "w2 ");
+  in.holds(14, at::kBFloat16, times(P, H), "y_perm");
+  if (in.ok && sd != sd2) {
+    PyErr_SetString(PyExc_ValueError, "the scales of w13 and w2 are of one type");
+    return nullptr;
+  }
+  void *x = in.ptr(0), *o = in.ptr(1), *e = in.ptr(2), *a = in.ptr(3), *as = in.ptr(4), *az = in.ptr(5), *b = in.ptr(6),
+       *bs = in.ptr(7), *bz = in.ptr(8), *y = in.ptr(14), *ws = in.ptr(15), *st = in.stream(16);
+  const size_t n = in.bytes(15);
+  return run(in, [&] {
+    return semmoe_w4_grouped_ffn(x, i32(o), i32(e), u8(a), as, u8(az), u8(b), bs, u8(bz), sd, P, E, H, I, g, y, ws, n, st);
+  });
+}
+
 // The callable that raises for a status.
 PyObject* set_raise(PyObject*, PyObject* f) {
   Py_INCREF(f);
@@ -424,6 +483,11 @@ PyMethodDef methods[] = {
     ENTRY(semmoe_mx4_grouped_ffn),
     ENTRY(semmoe_norm),
     ENTRY(semmoe_combine_norm),
+    ENTRY(semmoe_w4_quantize),
+    ENTRY(semmoe_w4_dequantize),
+    ENTRY(semmoe_w4_grouped_gemm),
+    ENTRY(semmoe_w4_grouped_ffn_workspace_size),
+    ENTRY(semmoe_w4_grouped_ffn),
     ENTRY(semmoe_dp_schedule),
     ENTRY(semmoe_transition_lookup),
     ENTRY(semmoe_selftest_bounded_wait),
@@ -435,6 +499,10 @@ PyMethodDef methods[] = {
     METHOD("mx4_grouped_gemm", &mx4_grouped_gemm),
     METHOD("mx4_grouped_ffn", &mx4_grouped_ffn),
     METHOD("route_select", &route_select),
+    METHOD("w4_quantize", &w4_quantize),
+    METHOD("w4_dequantize", &w4_dequantize),
+    METHOD("w4_grouped_gemm", &w4_grouped_gemm),
+    METHOD("w4_grouped_ffn", &w4_grouped_ffn),
     METHOD("norm", &norm),
     METHOD("combine_norm", &combine_norm),
     {"set_raise", &set_raise, METH_O, nullptr},

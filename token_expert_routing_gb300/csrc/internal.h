@@ -22,6 +22,7 @@ int selftest_take_errors(cudaStream_t s, int* bits);
 int mx4_take_errors(cudaStream_t s, int* bits);
 int mx4_gemm_take_errors(cudaStream_t s, int* bits);
 int norm_take_errors(cudaStream_t s, int* bits);
+int w4_gemm_take_errors(cudaStream_t s, int* bits);
 cudaError_t launch_selftest_bounded_wait(cudaStream_t s);
 cudaError_t launch_selftest_fused_ready_wait(const void* x, const void* w13, const void* w2, int P, int H, int I,
                                              void* y, void* ws, cudaStream_t s);
@@ -193,5 +194,20 @@ cudaError_t launch_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, co
                                    const int32_t* experts, const uint8_t* w13, const uint8_t* w13_scales,
                                    const uint8_t* w2, const uint8_t* w2_scales, int P, int E, int H, int I, void* y,
                                    void* ws, cudaStream_t s);
+
+// 4-bit weights with group scales (w4.cuh): conversions (w4.cu) and grouped products (w4_gemm.cu).
+namespace w4 {
+struct Weights;
+}
+cudaError_t launch_w4_quantize(const void* x, int dtype, long long rows, int K, int group, uint8_t* codes, void* scales,
+                               int scale_dtype, uint8_t* zeros, cudaStream_t s);
+cudaError_t launch_w4_dequantize(const w4::Weights& w, long long rows, int K, int group, void* out, int dtype,
+                                 cudaStream_t s);
+cudaError_t launch_w4_grouped_gemm(const void* x, const int32_t* offsets, const int32_t* experts, const w4::Weights& w,
+                                   int P, int E, int N, int K, int group, void* out, cudaStream_t s);
+size_t w4_ffn_ws_bytes(int P, int I);
+cudaError_t launch_w4_grouped_ffn(const void* x, const int32_t* offsets, const int32_t* experts, const w4::Weights& w13,
+                                  const w4::Weights& w2, int P, int E, int H, int I, int group, void* y, void* ws,
+                                  cudaStream_t s);
 
 }  // namespace semmoe
