@@ -85,7 +85,7 @@ int semmoe_check_errors(void* stream, int* bits) {
   if (route_take_errors(s, &b) || permute_take_errors(s, &b) || ffn_take_errors(s, &b) ||
       combine_take_errors(s, &b) || schedule_take_errors(s, &b) || selftest_take_errors(s, &b) ||
       mx4_take_errors(s, &b) || mx4_gemm_take_errors(s, &b) || norm_take_errors(s, &b) ||
-      w4_gemm_take_errors(s, &b))
+      w4_gemm_take_errors(s, &b) || w4_tc_take_errors(s, &b))
     return cuda_status(cudaGetLastError(), "semmoe_check_errors: reading the device error word");
   if (bits != nullptr) *bits = b;
   if (b & SEMMOE_DEVERR_TIMEOUT) return fail(SEMMOE_ERR_DEVICE_TIMEOUT, "a bounded in-kernel wait ran out (bits 0x%x)", b);

@@ -18,7 +18,7 @@
 // rounded.
 #include "common.cuh"
 #include "internal.h"
-#include "w4.cuh"
+#include "w4_groups.cuh"
 
 namespace semmoe {
 namespace {
@@ -27,74 +27,12 @@ using namespace w4;
 
 __device__ int g_err;
 
-constexpr int MAX_GROUPS = 256;
 constexpr int THREADS = 128;
 constexpr int STAGES = 4;
 constexpr int CHUNK = 128;            // columns of a warp's stage
 constexpr int W_STAGE = 8192;         // bytes of codes a stage: 32 rows x 64 bytes x 4 warps
 constexpr int X_STAGE = 8192;         // bytes of rows a stage: 8 NT x 256 bytes x WK
 constexpr int STAGE_BYTES = W_STAGE + X_STAGE;
-
-// What a launch multiplies.  N: columns of the output (SwiGLU: I, with 2 I weight rows).
-struct Product {
-  const __nv_bfloat16* x;
-  const int32_t* offsets;
-  const int32_t* experts;
-  Weights w;
-  int P, E, N, K, group, n_tiles;
-  __nv_bfloat16* out;
-};
-
-struct Groups {
-  int total;                 // units / n_tiles: blocks of rows
-  int off[MAX_GROUPS + 1];
-  int pe[MAX_GROUPS];
-  int tp[MAX_GROUPS + 1];    // blocks of rows before each group
-};
-
-// One warp: the tables and the exclusive prefix of the groups' blocks of `block` rows, 8 groups per lane.
-__device__ inline void load_groups(Groups& sh, const Product& pr, int block, int lane) {
-  const int G = pr.E;
-  int off[9], cnt[8], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 9; ++i) off[i] = lane * 8 + i <= G ? pr.offsets[lane * 8 + i] : 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int g = lane * 8 + i;
-    int c = 0;
-    if (g < G) {
-      const int lo = off[i], hi = off[i + 1], e = pr.experts[g];
-      sh.off[g] = lo;
-      sh.pe[g] = e;
-      if (g == G - 1) sh.off[G] = hi;
-      if (lo < 0 || hi < lo || hi > pr.P) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
-      else if (e < 0 || e >= pr.E) atomicOr(&g_err, SEMMOE_DEVERR_EXPERT);
-      else c = (hi - lo + block - 1) / block;
-    }
-    cnt[i] = c;
-    sum += c;
-  }
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  int run = incl - sum;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int g = lane * 8 + i;
-    if (g < G) sh.tp[g] = run;
-    run += cnt[i];
-  }
-  if (lane == 31) {
-    // more blocks than any split of P rows has: offsets that step back
-    const bool bad = incl > pr.P / block + G;
-    if (bad) atomicOr(&g_err, SEMMOE_DEVERR_PAIRS);
-    sh.tp[G] = incl;
-    sh.total = bad ? 0 : incl;
-  }
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   const int n = live ? 16 : 0;  // nothing read, zeros written
@@ -124,26 +62,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// A unit: rows [row0, row0 + rows) with expert e, the tile nt of its weight rows.
-struct Unit {
-  int row0, rows, e, nt;
-};
-
-__device__ __forceinline__ Unit decode_unit(const Groups& sh, int G, int n_tiles, int block, long long u) {
-  int lo = 0, hi = G - 1;  // largest g with tp[g] * n_tiles <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)sh.tp[mid] * n_tiles <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const int v = (int)(u - (long long)sh.tp[lo] * n_tiles), blocks = sh.tp[lo + 1] - sh.tp[lo];
-  const int nt = v / blocks, b = v - nt * blocks;
-  const int row0 = sh.off[lo] + b * block, left = sh.off[lo + 1] - row0;
-  return Unit{row0, left < block ? left : block, sh.pe[lo], nt};
-}
-
 // GS: groups of scales in a chunk of 128 columns (4, 2, or 1 for groups of 128 and more).
 template <int NT, int WM, bool GLU, typename S, int GS>
 __global__ void __launch_bounds__(THREADS, 3)
@@ -160,7 +78,7 @@ w4_rows_kernel(Product pr) {
   const int wm = warp % WM, wk = warp / WM;
   pdl_trigger();
   pdl_wait();
-  if (warp == 0) load_groups(sh, pr, NB, lane);
+  if (warp == 0) load_groups(sh, pr, NB, lane, &g_err);
   __syncthreads();
   const int G = pr.E, K = pr.K, KG = K / pr.group, ki = (K + BK - 1) / BK;
   const int rows_w = GLU ? 2 * pr.N : pr.N;          // weight rows of an expert
@@ -400,8 +318,12 @@ cudaError_t launch_rows(const Product& pr, cudaStream_t s) {
   return launch_rows_t<4, 4, GLU, S, GS>(pr, s);
 }
 
+#ifndef W4_TC_FROM
+#define W4_TC_FROM 8
+#endif
 template <bool GLU>
 cudaError_t launch_product(const Product& pr, cudaStream_t s) {
+  if (pr.P / (pr.E < pr.P ? pr.E : pr.P) > W4_TC_FROM) return launch_w4_tc(pr, GLU, s);
   if (pr.w.scales_bf16) {
     if (pr.group == 32) return launch_rows<GLU, __nv_bfloat16, 4>(pr, s);
     if (pr.group == 64) return launch_rows<GLU, __nv_bfloat16, 2>(pr, s);
