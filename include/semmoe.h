@@ -659,8 +659,8 @@ int semmoe_mx4_grouped_ffn(const uint8_t* x, const uint8_t* x_scales, const int3
  * codes   row-major [rows, K/2] bytes, two codes each, the lower column in the low four bits
  * scales  row-major [rows, K/group] scale_dtype (SEMMOE_F32 or SEMMOE_BF16)
  * zeros   row-major [rows, K/group] bytes 0..15 (the low four bits are read), or NULL: 8 everywhere
- * Limits: group 32, 64 or a multiple of 128; K % group == 0; pointers to codes, rows and outputs 16-byte
- * aligned, to scales aligned to their type; at most 2^31 - 2^16 rows a call.
+ * Limits: group 32, 64 or a multiple of 128; K % group == 0; all pointers 16-byte aligned; at most 2^31 - 2^16
+ * rows a call.
  *
  * semmoe_w4_quantize -- codes, scales and zero points of x [rows,K] (fp32 or bf16).  With zeros, a group's
  * range lo = min(0, min x) .. hi = max(0, max x) is covered: scale = (hi - lo) / 15, zero = round(-lo / scale);

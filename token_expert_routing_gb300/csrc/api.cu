@@ -85,7 +85,8 @@ int semmoe_check_errors(void* stream, int* bits) {
   if (route_take_errors(s, &b) || permute_take_errors(s, &b) || ffn_take_errors(s, &b) ||
       combine_take_errors(s, &b) || schedule_take_errors(s, &b) || selftest_take_errors(s, &b) ||
       mx4_take_errors(s, &b) || mx4_gemm_take_errors(s, &b) || norm_take_errors(s, &b) ||
-      w4_gemm_take_errors(s, &b) || w4_tc_take_errors(s, &b))
+      w4_gemm_take_errors(s, &b) || w4_tc_plain_take_errors(s, &b) ||
+      w4_tc_glu_take_errors(s, &b))
     return cuda_status(cudaGetLastError(), "semmoe_check_errors: reading the device error word");
   if (bits != nullptr) *bits = b;
   if (b & SEMMOE_DEVERR_TIMEOUT) return fail(SEMMOE_ERR_DEVICE_TIMEOUT, "a bounded in-kernel wait ran out (bits 0x%x)", b);
@@ -730,20 +731,20 @@ static int check_w4_shape(const char* fn, int scale_dtype, int K, int group) {
 }
 
 static int check_w4_matrix(const char* fn, int rows, int K, int group, const void* full, int dtype, const void* codes,
-                           const void* scales, int scale_dtype) {
+                           const void* scales, int scale_dtype, const void* zeros) {
   REQUIRE(valid_dtype(dtype), "%s: bad dtype %d", fn, dtype);
   REQUIRE(rows >= 0 && rows <= kMaxRows, "%s: rows = %d outside [0, 2^31 - 2^16]", fn, rows);
   int rc = check_w4_shape(fn, scale_dtype, K, group);
   if (rc != SEMMOE_OK || rows == 0) return rc;
   REQUIRE(full && codes && scales, "%s: null pointer", fn);
-  REQUIRE(aligned(full, 16) && aligned(codes, 16) && aligned(scales, elem_size(scale_dtype)), "%s: misaligned pointer", fn);
+  REQUIRE(aligned(full, 16) && aligned(codes, 16) && aligned(scales, 16) && aligned(zeros, 16), "%s: misaligned pointer", fn);
   return SEMMOE_OK;
 }
 
 int semmoe_w4_quantize(const void* x, int dtype, int rows, int K, int group, uint8_t* codes, void* scales,
                        int scale_dtype, uint8_t* zeros, void* stream) {
   const char* fn = "semmoe_w4_quantize";
-  int rc = check_w4_matrix(fn, rows, K, group, x, dtype, codes, scales, scale_dtype);
+  int rc = check_w4_matrix(fn, rows, K, group, x, dtype, codes, scales, scale_dtype, zeros);
   if (rc != SEMMOE_OK || rows == 0) return rc;
   CHECK_DEVICE(fn);
   return cuda_status(launch_w4_quantize(x, dtype, rows, K, group, codes, scales, scale_dtype, zeros,
@@ -754,7 +755,7 @@ int semmoe_w4_quantize(const void* x, int dtype, int rows, int K, int group, uin
 int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int rows, int K,
                          int group, void* out, int out_dtype, void* stream) {
   const char* fn = "semmoe_w4_dequantize";
-  int rc = check_w4_matrix(fn, rows, K, group, out, out_dtype, codes, scales, scale_dtype);
+  int rc = check_w4_matrix(fn, rows, K, group, out, out_dtype, codes, scales, scale_dtype, zeros);
   if (rc != SEMMOE_OK || rows == 0) return rc;
   CHECK_DEVICE(fn);
   return cuda_status(launch_w4_dequantize(w4::Weights{codes, scales, zeros, scale_dtype == SEMMOE_BF16}, rows, K, group,
@@ -763,16 +764,19 @@ int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dty
 }
 
 static int check_w4_product(const char* fn, const void* x, const void* offsets, const void* experts, const void* codes,
-                            const void* scales, int scale_dtype, int P, int E, int N, int K, int group, const void* out) {
+                            const void* scales, int scale_dtype, const void* zeros, int P, int E, int N, int K, int group,
+                            const void* out) {
   REQUIRE(E >= 1 && E <= 256, "%s: E = %d outside [1, 256]", fn, E);
   REQUIRE(P >= 0 && P <= kMaxRows, "%s: P = %d outside [0, 2^31 - 2^16]", fn, P);
   int rc = check_w4_shape(fn, scale_dtype, K, group);
   if (rc != SEMMOE_OK) return rc;
   REQUIRE(N >= 8 && N % 8 == 0, "%s: N = %d is not a positive multiple of 8", fn, N);
   REQUIRE(N <= kMaxRows / 2 && K <= kMaxRows, "%s: N or K too large", fn);
+  // units of work (at least 8 rows x 16 columns) are counted in 32 bits
+  REQUIRE(((long long)P / 8 + E) * ((N + 15) / 16) <= kMaxRows, "%s: P * N too large", fn);
   if (P == 0) return SEMMOE_OK;
   REQUIRE(x && offsets && experts && codes && scales && out, "%s: null pointer", fn);
-  REQUIRE(aligned(x, 16) && aligned(codes, 16) && aligned(out, 16) && aligned(scales, elem_size(scale_dtype)) &&
+  REQUIRE(aligned(x, 16) && aligned(codes, 16) && aligned(out, 16) && aligned(scales, 16) && aligned(zeros, 16) &&
               aligned(offsets, 4) && aligned(experts, 4),
           "%s: misaligned pointer", fn);
   return SEMMOE_OK;
@@ -782,7 +786,7 @@ int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const i
                            const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int P, int E,
                            int N, int K, int group, void* out, void* stream) {
   const char* fn = "semmoe_w4_grouped_gemm";
-  int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, codes, scales, scale_dtype, P, E, N, K, group, out);
+  int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, codes, scales, scale_dtype, zeros, P, E, N, K, group, out);
   if (rc != SEMMOE_OK || P == 0) return rc;
   CHECK_DEVICE(fn);
   return cuda_status(launch_w4_grouped_gemm(x, expert_offsets, phys_to_expert,
@@ -801,14 +805,15 @@ int semmoe_w4_grouped_ffn(const void* x, const int32_t* expert_offsets, const in
                           const void* w2_scales, const uint8_t* w2_zeros, int scale_dtype, int P, int E, int H, int I,
                           int group, void* y_perm, void* ws, size_t ws_bytes, void* stream) {
   const char* fn = "semmoe_w4_grouped_ffn";
-  int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, w13, w13_scales, scale_dtype, P, E, H, H, group, y_perm);
+  int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, w13, w13_scales, scale_dtype, w13_zeros, P, E, H, H,
+                            group, y_perm);
   if (rc != SEMMOE_OK) return rc;
   rc = check_w4_shape(fn, scale_dtype, I, group);
   if (rc != SEMMOE_OK || P == 0) return rc;
-  REQUIRE(I <= kMaxRows / 2, "%s: I too large", fn);
+  REQUIRE(I <= kMaxRows / 2 && ((long long)P / 8 + E) * ((I + 15) / 16) <= kMaxRows, "%s: I or P * I too large", fn);
   REQUIRE(w2 && w2_scales, "%s: null pointer", fn);
   REQUIRE((w13_zeros == nullptr) == (w2_zeros == nullptr), "%s: zeros of w13 and w2 go together", fn);
-  REQUIRE(aligned(w2, 16) && aligned(w2_scales, elem_size(scale_dtype)), "%s: misaligned pointer", fn);
+  REQUIRE(aligned(w2, 16) && aligned(w2_scales, 16) && aligned(w2_zeros, 16), "%s: misaligned pointer", fn);
   REQUIRE(ws != nullptr && aligned(ws, 256) && ws_bytes >= w4_ffn_ws_bytes(P, I),
           "%s: workspace null, not 256-byte aligned or below %zu bytes", fn, w4_ffn_ws_bytes(P, I));
   CHECK_DEVICE(fn);

@@ -23,7 +23,8 @@ int mx4_take_errors(cudaStream_t s, int* bits);
 int mx4_gemm_take_errors(cudaStream_t s, int* bits);
 int norm_take_errors(cudaStream_t s, int* bits);
 int w4_gemm_take_errors(cudaStream_t s, int* bits);
-int w4_tc_take_errors(cudaStream_t s, int* bits);
+int w4_tc_plain_take_errors(cudaStream_t s, int* bits);
+int w4_tc_glu_take_errors(cudaStream_t s, int* bits);
 cudaError_t launch_selftest_bounded_wait(cudaStream_t s);
 cudaError_t launch_selftest_fused_ready_wait(const void* x, const void* w13, const void* w2, int P, int H, int I,
                                              void* y, void* ws, cudaStream_t s);

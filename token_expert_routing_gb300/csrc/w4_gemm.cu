@@ -82,7 +82,7 @@ w4_rows_kernel(Product pr) {
   __syncthreads();
   const int G = pr.E, K = pr.K, KG = K / pr.group, ki = (K + BK - 1) / BK;
   const int rows_w = GLU ? 2 * pr.N : pr.N;          // weight rows of an expert
-  const long long total = (long long)sh.total * pr.n_tiles;
+  const int total = sh.total * pr.n_tiles;
   // row r of the unit's weight rows (of warp block r / 32) among the expert's
   auto weight_row = [&](int nt, int r) {
     if (GLU) {
@@ -98,12 +98,12 @@ w4_rows_kernel(Product pr) {
   constexpr int XN = X_STAGE / 16 / THREADS;
   const int w_seg = tid % WP, x_seg = tid % XP;
   const uint32_t base = smem_addr(smem);
-  long long lu = blockIdx.x;                         // the unit being copied ...
+  int lu = blockIdx.x, lg = 0, ug = 0;               // the unit being copied, its group ...
   int lkb = 0;                                       // ... and its k-block
   const uint8_t* wsrc[4];
   const __nv_bfloat16* xsrc[XN];
   auto copy_rows = [&]() {
-    const Unit un = decode_unit(sh, G, pr.n_tiles, NB, lu);
+    const Unit un = decode_unit(sh, G, lg, pr.n_tiles, NB, lu);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       wsrc[i] = pr.w.codes + ((size_t)un.e * rows_w + weight_row(un.nt, tid / WP + i * (THREADS / WP))) * (K / 2) + w_seg * 16;
@@ -166,12 +166,12 @@ w4_rows_kernel(Product pr) {
     }
   };
 
-  long long u = blockIdx.x;
+  int u = blockIdx.x;
   if (u >= total) return;
   copy_rows();
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) copy_stage(s);
-  Unit un = decode_unit(sh, G, pr.n_tiles, NB, u);
+  Unit un = decode_unit(sh, G, ug, pr.n_tiles, NB, u);
   scale_rows(un);
   load_scales(0, sc, zp);
   float acc[MT][NT][4];
@@ -192,9 +192,9 @@ w4_rows_kernel(Product pr) {
     Unit nx = un;
     float nsc[MT][2][GS];
     uint32_t nzp[MT][2][GS];
-    const bool more = !last || u + gridDim.x < total;
+    const bool more = !last || u + (int)gridDim.x < total;
     if (last && more) {
-      nx = decode_unit(sh, G, pr.n_tiles, NB, u + gridDim.x);
+      nx = decode_unit(sh, G, ug, pr.n_tiles, NB, u + gridDim.x);
       scale_rows(nx);
     }
     load_scales(last ? 0 : kb + 1, nsc, nzp);  // (of this unit again where there is none: not used)
@@ -323,7 +323,7 @@ cudaError_t launch_rows(const Product& pr, cudaStream_t s) {
 #endif
 template <bool GLU>
 cudaError_t launch_product(const Product& pr, cudaStream_t s) {
-  if (pr.P / (pr.E < pr.P ? pr.E : pr.P) > W4_TC_FROM) return launch_w4_tc(pr, GLU, s);
+  if (pr.P / (pr.E < pr.P ? pr.E : pr.P) > W4_TC_FROM) return GLU ? launch_w4_tc_glu(pr, s) : launch_w4_tc_plain(pr, s);
   if (pr.w.scales_bf16) {
     if (pr.group == 32) return launch_rows<GLU, __nv_bfloat16, 4>(pr, s);
     if (pr.group == 64) return launch_rows<GLU, __nv_bfloat16, 2>(pr, s);

@@ -72,29 +72,41 @@ __device__ inline void load_groups(Groups& sh, const Product& pr, int block, int
 
 // Unit u of the (group, weight tile, block of rows) list, blocks innermost: rows
 // [row0, row0 + rows) with expert e, weight tile nt.  round > 0: a group's blocks
-// are of one size, rounded up to that many rows (at most `block`).
+// are of one size, rounded up to that many rows (at most `block`).  Units come in
+// increasing order, so a role keeps the group `g` it is at: the next unit is a few
+// groups on where groups are long, and anywhere after it where they are empty.
 struct Unit {
   int row0, rows, e, nt;
 };
-__device__ __forceinline__ Unit decode_unit(const Groups& sh, int G, int n_tiles, int block, long long u, int round = 0) {
-  int lo = 0, hi = G - 1;  // largest g with tp[g] * n_tiles <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)sh.tp[mid] * n_tiles <= u) lo = mid;
-    else hi = mid - 1;
+__device__ __forceinline__ Unit decode_unit(const Groups& sh, int G, int& g, int n_tiles, int block, int u, int round = 0) {
+  const int at = u / n_tiles;  // tp[g] * n_tiles <= u < tp[g + 1] * n_tiles, as tp[g] <= at < tp[g + 1]
+  int steps = 4;
+  while (sh.tp[g + 1] <= at && --steps) ++g;
+  if (steps == 0) {
+    int hi = G - 1;
+    while (g < hi) {
+      const int mid = (g + hi) >> 1;
+      if (sh.tp[mid + 1] > at) hi = mid;
+      else g = mid + 1;
+    }
   }
-  const int v = (int)(u - (long long)sh.tp[lo] * n_tiles), blocks = sh.tp[lo + 1] - sh.tp[lo];
-  const int nt = v / blocks, b = v - nt * blocks;
-  if (round > 0) block = ((sh.off[lo + 1] - sh.off[lo] + blocks - 1) / blocks + round - 1) / round * round;
-  const int row0 = sh.off[lo] + b * block, left = sh.off[lo + 1] - row0;
-  return Unit{row0, left < block ? left : block, sh.pe[lo], nt};
+  const int v = u - sh.tp[g] * n_tiles, blocks = sh.tp[g + 1] - sh.tp[g];
+  int nt = v, b = 0, rows = sh.off[g + 1] - sh.off[g];
+  if (blocks > 1) {
+    nt = v / blocks;
+    b = v - nt * blocks;
+    if (round > 0) block = ((rows + blocks - 1) / blocks + round - 1) / round * round;
+  }
+  const int left = rows - b * block;
+  return Unit{sh.off[g] + b * block, left < block ? left : block, sh.pe[g], nt};
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 }  // namespace w4
 
-// Many rows per expert (w4_tc.cu); glu: the SwiGLU form.
-cudaError_t launch_w4_tc(const w4::Product& pr, bool glu, cudaStream_t s);
+// Many rows per expert (w4_tc.cuh): the plain product, and the SwiGLU form.
+cudaError_t launch_w4_tc_plain(const w4::Product& pr, cudaStream_t s);
+cudaError_t launch_w4_tc_glu(const w4::Product& pr, cudaStream_t s);
 
 }  // namespace semmoe

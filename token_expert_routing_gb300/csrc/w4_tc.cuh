@@ -1,0 +1,595 @@
+// Grouped products of bf16 rows with 4-bit weights (w4.cuh) on the 5th-generation
+// tensor cores, for experts with more than a few rows.
+//
+// The weights are the left operand (M = 128 weight rows), held in tensor memory: a
+// thread turns the codes of its row into bf16 in registers and writes them to its
+// TMEM lane, so the expanded weights never pass through shared memory, whose
+// bandwidth bounds the bf16 products (ffn_tc.cu).  The token rows are the right
+// operand (N = up to 128 rows of a group, a multiple of 16), by TMA.
+//
+// A unit has two accumulators of up to 128 columns (tokens):
+//   plain:  128 weight rows x up to 256 token rows; both halves read one A block
+//   SwiGLU: 128 gate rows and the 128 up rows x up to 128 token rows; two A blocks
+// TMEM holds three accumulators and a ring of A blocks: a unit's first accumulator
+// is free while the epilogue still reads the unit before.
+//
+// One persistent CTA per SM takes units in turn.  Warp roles:
+//   expansion   EXP / 4 groups of four warps, a chunk of 128 columns at a time in turn
+//               (SwiGLU: half of the groups for gate rows, half for up rows)
+//   epilogue    EPI / 4 groups of four, the columns of an accumulator divided between them
+//   producers   one warp for codes ([128 rows x 128 columns] a slot), one for token rows
+//   issuer      allocates TMEM, issues the MMAs (M128 N16..128 K16)
+// Units of few token rows are bound by the expansion: 16 warps of it, k-blocks of 128 columns
+// (fewer barriers a weight); units of many by the MMAs: 8 and 8 warps, k-blocks of 64.
+//
+// Expansion of a word of eight codes: two masked halves (codes of even and odd columns), then
+// one byte permutation a pair of columns, whose result reads as two bf16 denormals
+// code * 2^-133, and
+//   without zero points, bf16 scales:  w = code * (s 2^93) - 8 s 2^-40      one fused operation, one rounding
+//   else: d = code * 2^127 - z 2^-6 (exact),  w = d * (s 2^-34), an fp32 scale as the sum of two bf16 numbers, the
+//   smaller product first
+// so a weight is held as w 2^-40 (the sums are multiplied by 2^40), rounded once to bf16: at most half a
+// step off, as in any bf16 copy of the weights.
+//
+// Every wait is bounded; a wait that runs out sets the timeout bit of the device error
+// word and an abort flag, after which every role stops, loads and MMAs in flight are
+// drained (again with a bound), and TMEM is freed before the CTA exits.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc_common.cuh"
+#include "w4_groups.cuh"
+
+namespace semmoe {
+namespace {
+
+using namespace tc;
+using namespace w4;
+
+__device__ int g_err;
+
+constexpr int BM = 128;               // weight rows of an A block
+constexpr int UK = 16;                // K per MMA
+constexpr int CHUNK = 128;            // columns of a slot of codes: 64 bytes a row
+constexpr int C_BYTES = BM * CHUNK / 2;
+constexpr int XR = 32;                // rows of a box of token rows
+constexpr int XC = 64;                // its columns: a 128-byte swizzle row
+constexpr int X_BOX = XR * XC * 2;
+constexpr int ACCS = 3;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int ROUND = 16;             // token rows of a unit: a multiple of this
+
+enum Mode { SYM, ZEROS, F32 };        // bf16 scales without and with zero points; fp32 scales
+
+// ROWS: token rows of a unit, at most.
+template <bool GLU, int ROWS>
+struct Shape {
+  static constexpr bool few = ROWS <= 64;
+  static constexpr int HN = ROWS < 128 ? ROWS : 128;   // columns of an accumulator
+  static constexpr int BK = few ? 128 : 64;            // columns of a k-block
+  static constexpr int EXP = few ? 16 : 8, EPI = few ? 4 : 8;
+  static constexpr int THREADS = (EXP + EPI + 3) * 32;
+  static constexpr int AB = GLU ? 2 : 1;               // A blocks of a k-block
+  static constexpr int A_COLS = AB * BK / 2;           // TMEM columns of a k-block's
+  static constexpr int AD = (TMEM_COLS - ACCS * HN) / A_COLS;
+  static constexpr int X_BYTES = ROWS * BK * 2;        // a stage of token rows
+  static constexpr int XD = ROWS == 32 ? 8 : ROWS == 256 ? 5 : 6;
+  static constexpr int C_SLOTS = (204 * 1024 - XD * X_BYTES) / C_BYTES < 16 ? (204 * 1024 - XD * X_BYTES) / C_BYTES : 16;
+  static constexpr size_t smem = 1024 + (size_t)C_SLOTS * C_BYTES + (size_t)XD * X_BYTES;
+  static_assert(AD >= 2 && XD >= AD, "rings");
+};
+
+template <int C_SLOTS, int XD, int AD>
+struct Shared {
+  uint64_t cfull[C_SLOTS], cempty[C_SLOTS], xfull[XD], afull[AD];
+  uint64_t done[XD];  // a k-block's MMAs: its token rows and A blocks may be overwritten
+  uint64_t tfull[ACCS], tempty[ACCS], last;
+  uint32_t tmem_base;
+  int abort_flag;
+  int c_armed, x_armed;  // slots and stages that the producers have armed
+  Groups groups;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]^T.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t both(float v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v, v);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// What a group's codes are expanded with.
+struct Factors {
+  uint32_t f[3];
+};
+template <int MODE>
+__device__ __forceinline__ Factors factors(float s, uint32_t z) {
+  constexpr float k93 = 9903520314283042199192993792.0f, k40 = 9.094947017729282379150390625e-13f,
+                  k34 = 5.82076609134674072265625e-11f;  // 2^93, 2^-40, 2^-34
+  if (MODE == SYM) return Factors{{both(s * k93), both(-8.0f * k40 * s), 0u}};
+  const uint32_t zero = both(-0.015625f * (float)(z & 15u));
+  if (MODE == ZEROS) return Factors{{zero, both(s * k34), 0u}};
+  const float hi = __bfloat162float(__float2bfloat16_rn(s)), rest = s - hi;
+  return Factors{{zero, both(hi * k34), both(rest == rest ? rest * k34 : 0.0f)}};  // (an infinite scale has no rest)
+}
+
+// The eight codes of a word as bf16 weights, in column order.
+template <int MODE>
+__device__ __forceinline__ void expand(uint32_t w, const Factors& f, uint32_t* r) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    uint32_t q;  // byte i of each, with its sign bit's copies, 0, above
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(even), "r"(odd), "r"(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12)));
+    if (MODE == SYM) {
+      r[i] = fma_bf16x2(q, f.f[0], f.f[1]);
+    } else {
+      const uint32_t d = fma_bf16x2(q, 0x7f007f00u, f.f[0]);
+      r[i] = MODE == ZEROS ? mul_bf16x2(d, f.f[1]) : fma_bf16x2(d, f.f[1], mul_bf16x2(d, f.f[2]));
+    }
+  }
+}
+
+// mbar_wait by a whole converged warp, polling a few times before it looks at the clock.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return mbar_wait_warp(bar, parity, abort_flag, &g_err);
+}
+
+// Two tokens' columns of a warp's 32 weight rows (v0, v1: this lane's row): even lanes
+// store the first token's pair of rows, odd lanes the second's.
+__device__ __forceinline__ void store_pair(float v0, float v1, __nv_bfloat16* first, size_t stride, int left, bool live, int lane) {
+  const __nv_bfloat162 own2 = __floats2bfloat162_rn(v0, v1);
+  const uint32_t own = *reinterpret_cast<const uint32_t*>(&own2);
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+  const int odd = lane & 1;
+  const uint32_t v = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+  if (live && odd < left) *reinterpret_cast<uint32_t*>(first + (odd ? stride : 0)) = v;
+}
+
+template <bool GLU, int ROWS, int MODE>
+__global__ void __launch_bounds__(Shape<GLU, ROWS>::THREADS, 1)
+w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_x, Product pr) {
+  using SH = Shape<GLU, ROWS>;
+  constexpr int AB = SH::AB, XD = SH::XD, AD = SH::AD, C_SLOTS = SH::C_SLOTS, BK = SH::BK, HN = SH::HN;
+  constexpr uint32_t A_COL = ACCS * HN;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ Shared<C_SLOTS, XD, AD> sh;
+  unsigned char* xs = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* codes = xs + XD * SH::X_BYTES;
+  volatile int* abort_flag = &sh.abort_flag;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  constexpr int EPI0 = SH::EXP, C_WARP = EPI0 + SH::EPI, X_WARP = C_WARP + 1, MMA_WARP = C_WARP + 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C_SLOTS; ++i) {
+      mbar_init(&sh.cfull[i], 1);
+      mbar_init(&sh.cempty[i], 4);  // the warps that read it
+    }
+    for (int i = 0; i < XD; ++i) {
+      mbar_init(&sh.xfull[i], 1);
+      mbar_init(&sh.done[i], 1);
+    }
+    for (int i = 0; i < AD; ++i) mbar_init(&sh.afull[i], 4 * AB);
+    for (int i = 0; i < ACCS; ++i) {
+      mbar_init(&sh.tfull[i], 1);
+      mbar_init(&sh.tempty[i], SH::EPI);
+    }
+    mbar_init(&sh.last, 1);
+    sh.abort_flag = 0;
+    sh.c_armed = sh.x_armed = 0;
+    mbar_init_fence();
+    prefetch_map(&map_c);
+    prefetch_map(&map_x);
+  }
+  if (warp == MMA_WARP) tmem_alloc(&sh.tmem_base, TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) load_groups(sh.groups, pr, ROWS, lane, &g_err);
+  fence_before();
+  __syncthreads();
+  fence_after();
+
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
+  const int G = pr.E, n_tiles = pr.n_tiles, K = pr.K, units = gridDim.x;
+  const int total = __shfl_sync(0xffffffffu, sh.groups.total, 0) * n_tiles;
+  const int kb_n = (K + BK - 1) / BK, ch_n = (K + CHUNK - 1) / CHUNK;
+  int group = 0;  // of this role's unit
+  auto unit_at = [&](int u) { return decode_unit(sh.groups, G, group, n_tiles, ROWS, u, ROUND); };
+
+  if (warp < SH::EXP) {
+    // ---------------- codes to bf16 weights in TMEM ----------------
+    constexpr int STEP = SH::EXP / 4 / AB;              // chunks between this group's
+    const int wg = warp / 4, ab = GLU ? wg & 1 : 0, r = (warp % 4) * 32 + lane;
+    const int KG = K / pr.group, rows_w = GLU ? 2 * pr.N : pr.N;
+    const int gs = pr.group >= CHUNK ? 1 : CHUNK / pr.group;    // scales of a chunk
+    const bool whole = K % CHUNK == 0;                          // a chunk's scales are aligned to their size
+    const int per = pr.group > CHUNK ? pr.group / CHUNK : 1;    // chunks of a scale
+    const uint32_t a_lane = tmem + ((uint32_t)((warp % 4) * 32) << 16) + A_COL + ab * (BK / 2);
+    size_t srow = 0;  // the row's first scale
+    auto at_row = [&](const Unit& un) {
+      int n = un.nt * BM + r;
+      if (n >= pr.N) n = pr.N - 1;  // a row past the matrix: its codes are 0, nothing of it is stored
+      srow = ((size_t)un.e * rows_w + n + (GLU && ab ? pr.N : 0)) * KG;
+    };
+    // a chunk's scales and zero points as they lie in memory, loaded one chunk of this group ahead
+    uint32_t raw[MODE == F32 ? 4 : 2], rawz = 0x08080808u;
+    auto load = [&](int ch) {
+      const size_t at = srow + (gs > 1 ? ch * gs : per > 1 ? ch / per : ch);
+      if (gs == 1 || whole) {
+        if (MODE == F32) {
+          const float* p = static_cast<const float*>(pr.w.scales) + at;
+          if (gs == 1) raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          if (gs == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            raw[0] = v.x, raw[1] = v.y;
+          }
+          if (gs == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            raw[0] = v.x, raw[1] = v.y, raw[MODE == F32 ? 2 : 0] = v.z, raw[MODE == F32 ? 3 : 1] = v.w;
+          }
+        } else {
+          const unsigned short* p = static_cast<const unsigned short*>(pr.w.scales) + at;
+          if (gs == 1) raw[0] = __ldg(p);
+          if (gs == 2) raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          if (gs == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            raw[0] = v.x, raw[1] = v.y;
+          }
+        }
+        if (MODE != SYM && pr.w.zeros != nullptr) {
+          const uint8_t* p = pr.w.zeros + at;
+          if (gs == 1) rawz = __ldg(p);
+          if (gs == 2) rawz = __ldg(reinterpret_cast<const unsigned short*>(p));
+          if (gs == 4) rawz = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
+        return;
+      }
+      uint32_t v[4], z = 0;  // scale by scale; past K the last one again (codes and token rows are 0 there)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const size_t j = srow + (ch * gs + i < KG ? ch * gs + i : KG - 1);
+        v[i] = MODE == F32 ? __ldg(static_cast<const uint32_t*>(pr.w.scales) + j)
+                           : __ldg(static_cast<const unsigned short*>(pr.w.scales) + j);
+        if (MODE != SYM) z |= (pr.w.zeros != nullptr ? (uint32_t)__ldg(pr.w.zeros + j) : 8u) << (8 * i);
+      }
+      rawz = z;
+      if (MODE == F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[MODE == F32 ? i : 0] = v[i];
+      } else {
+        raw[0] = v[0] | (v[1] << 16), raw[1] = v[2] | (v[3] << 16);
+      }
+    };
+    // scale i of the loaded chunk (i < gs)
+    auto scale_of = [&](int i) {
+      if (MODE == F32) return __uint_as_float(raw[MODE == F32 ? i : 0]);
+      return __uint_as_float(i & 1 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16);
+    };
+    int u = blockIdx.x, ch = GLU ? wg >> 1 : wg;
+    uint32_t before = 0;  // units before u
+    auto settle = [&]() {  // the place: of a unit's chunks
+      while (ch >= ch_n) ch -= ch_n, u += units, ++before;
+    };
+    settle();
+    int loaded = -1;  // the unit whose row srow is
+    if (u < total) {
+      at_row(unit_at(u));
+      loaded = u;
+      load(ch);
+    }
+    bool ok = true;
+    while (ok && u < total) {
+      const uint32_t cg = before * ch_n + ch, j = cg * AB + ab, slot = j % C_SLOTS;
+      Factors f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int g = gs == 4 ? i : gs == 2 ? i / 2 : 0;
+        if (i == 0 || gs == 4 || (gs == 2 && i == 2)) {
+          const float s = i == 0 ? scale_of(0) : gs == 4 ? scale_of(i) : scale_of(1);
+          f[i] = factors<MODE>(s, rawz >> (8 * g));
+        } else {
+          f[i] = f[i - 1];
+        }
+      }
+      const uint32_t it0 = before * kb_n + ch * (CHUNK / BK);
+      const int blocks = kb_n - ch * (CHUNK / BK);  // k-blocks from here on
+      ch += STEP;
+      settle();
+      if (u < total) {
+        if (u != loaded) {
+          at_row(unit_at(u));
+          loaded = u;
+        }
+        load(ch);
+      }
+      if (!(ok = wait_warp(&sh.cfull[slot], (j / C_SLOTS) & 1, abort_flag))) break;
+      const unsigned char* src = codes + slot * C_BYTES + r * 64;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // 64 columns
+        if (BK == 64 && h >= blocks) break;
+        uint4 c[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c[i] = *reinterpret_cast<const uint4*>(src + (((2 * h + i) ^ ((r >> 1) & 3)) << 4));
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          expand<MODE>(c[i].x, f[2 * h + i], w + 16 * i);
+          expand<MODE>(c[i].y, f[2 * h + i], w + 16 * i + 4);
+          expand<MODE>(c[i].z, f[2 * h + i], w + 16 * i + 8);
+          expand<MODE>(c[i].w, f[2 * h + i], w + 16 * i + 12);
+        }
+        const uint32_t it = it0 + (BK == 64 ? h : 0);
+        if ((BK == 64 || h == 0) && it >= AD) {  // the MMAs that read this place
+          if (!(ok = wait_warp(&sh.done[(it - AD) % XD], ((it - AD) / XD) & 1, abort_flag))) break;
+          fence_after();
+        }
+        tmem_st32(a_lane + (it % AD) * SH::A_COLS + (BK == 128 ? h * 32 : 0), w);
+        if (BK == 64 || h == 1) {
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.afull[it % AD]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.cempty[slot]);
+    }
+  } else if (warp < C_WARP) {
+    // ---------------- epilogue ----------------
+    constexpr int PART = HN / (SH::EPI / 4);              // columns of a group of four warps
+    constexpr int W = PART < 32 ? PART : 32;              // a load
+    constexpr float kUnscale = 1099511627776.0f;          // 2^40
+    const int q = warp & 3, w = (warp - EPI0) >> 2;
+    const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + PART * w;
+    uint32_t half = 0;
+    auto wait_acc = [&](uint32_t h) { return wait_warp(&sh.tfull[h % ACCS], (h / ACCS) & 1, abort_flag); };
+    auto leave_acc = [&](uint32_t h) {
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.tempty[h % ACCS]);
+    };
+    for (int u = blockIdx.x; u < total; u += units) {
+      const Unit un = unit_at(u);
+      const int n = un.nt * BM + q * 32 + lane;  // this lane's output column
+      const bool live = n < pr.N;
+      __nv_bfloat16* col = pr.out + (size_t)un.row0 * pr.N + (live ? n & ~1 : 0);
+      if (GLU) {
+        if (!wait_acc(half) || !wait_acc(half + 1)) break;
+        fence_after();
+        const int left = un.rows - PART * w;
+        const uint32_t tg = t_row + (half % ACCS) * HN, tu = t_row + ((half + 1) % ACCS) * HN;
+        uint32_t g[PART / W][32];
+        if (left > 0) {
+#pragma unroll
+          for (int c = 0; c < PART / W; ++c)
+            if (left > W * c) tmem_ld32(tg + W * c, g[c]);
+          tmem_ld_wait();
+        }
+        leave_acc(half);
+#pragma unroll
+        for (int c = 0; c < PART / 16; ++c) {
+          if (left > 16 * c) {
+            uint32_t up[16];
+            tmem_ld16(tu + 16 * c, up);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const uint32_t* gc = g[16 * c / W] + 16 * c % W;
+              const int t = 16 * c + i;
+              const float v0 = swiglu(__uint_as_float(gc[i]) * kUnscale, __uint_as_float(up[i]) * kUnscale);
+              const float v1 = swiglu(__uint_as_float(gc[i + 1]) * kUnscale, __uint_as_float(up[i + 1]) * kUnscale);
+              store_pair(v0, v1, col + (size_t)(PART * w + t) * pr.N, pr.N, left - t, live, lane);
+            }
+          }
+        }
+        leave_acc(half + 1);
+        half += 2;
+      } else {
+        const int nh = un.rows > HN ? 2 : 1;
+        bool ok = true;
+        for (int h = 0; h < nh; ++h, ++half) {
+          if (!(ok = wait_acc(half))) break;
+          fence_after();
+          const int t0 = h * HN + PART * w, left = un.rows - t0;
+          const uint32_t ty = t_row + (half % ACCS) * HN;
+          uint32_t y[PART / W][32];
+          if (left > 0) {
+#pragma unroll
+            for (int c = 0; c < PART / W; ++c)
+              if (left > W * c) tmem_ld32(ty + W * c, y[c]);
+            tmem_ld_wait();
+          }
+          leave_acc(half);
+#pragma unroll
+          for (int c = 0; c < PART / W; ++c) {
+            if (left > W * c) {
+#pragma unroll
+              for (int i = 0; i < W; i += 2) {
+                const int t = W * c + i;
+                store_pair(__uint_as_float(y[c][i]) * kUnscale, __uint_as_float(y[c][i + 1]) * kUnscale,
+                           col + (size_t)(t0 + t) * pr.N, pr.N, left - t, live, lane);
+              }
+            }
+          }
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == C_WARP) {
+    // ---------------- producer of codes ----------------
+    uint32_t j = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += units) {
+      const Unit un = unit_at(u);
+      for (int i = 0; i < ch_n * AB; ++i, ++j) {
+        const uint32_t slot = j % C_SLOTS;
+        if (!(ok = wait_warp(&sh.cempty[slot], ((j / C_SLOTS) & 1) ^ 1, abort_flag))) break;
+        if (elect_one()) {
+          mbar_expect_tx(&sh.cfull[slot], C_BYTES);
+          if (GLU)
+            tma_load_4d(codes + slot * C_BYTES, &map_c, &sh.cfull[slot], (i / 2) * (CHUNK / 2), un.nt * BM, i & 1, un.e);
+          else tma_load_3d(codes + slot * C_BYTES, &map_c, &sh.cfull[slot], i * (CHUNK / 2), un.nt * BM, un.e);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) *reinterpret_cast<volatile int*>(&sh.c_armed) = (int)j;
+  } else if (warp == X_WARP) {
+    // ---------------- producer of token rows ----------------
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < total; u += units) {
+      const Unit un = unit_at(u);
+      const int boxes = (un.rows + XR - 1) / XR;
+      for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        const uint32_t s = it % XD;
+        if (it >= XD && !(ok = wait_warp(&sh.done[s], ((it / XD) & 1) ^ 1, abort_flag))) break;
+        if (elect_one()) {
+          mbar_expect_tx(&sh.xfull[s], boxes * (BK / XC) * X_BOX);
+          for (int b = 0; b < boxes; ++b)
+#pragma unroll
+            for (int k = 0; k < BK / XC; ++k)
+              tma_load_2d(xs + s * SH::X_BYTES + k * (ROWS * XC * 2) + b * X_BOX, &map_x, &sh.xfull[s], kb * BK + k * XC,
+                          un.row0 + b * XR);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) *reinterpret_cast<volatile int*>(&sh.x_armed) = (int)it;
+  } else {
+    // ---------------- MMA issuer ----------------
+    uint32_t it = 0, half = 0;
+    bool ok = true;
+    const uint64_t desc_x = sw128_desc(smem_u32(xs));  // its address field counts 16 bytes
+    for (int u = blockIdx.x; ok && u < total; u += units) {
+      const Unit un = unit_at(u);
+      const int n = (un.rows + ROUND - 1) / ROUND * ROUND;
+      const int nh = GLU || n > HN ? 2 : 1;
+      for (int h = 0; ok && h < nh; ++h)  // the epilogue has left the accumulators (three halves ago)
+        if (half + h >= ACCS) ok = wait_warp(&sh.tempty[(half + h) % ACCS], ((half + h) / ACCS - 1) & 1, abort_flag);
+      if (!ok) break;
+      fence_after();
+      const uint32_t d0 = tmem + (half % ACCS) * HN, d1 = tmem + ((half + 1) % ACCS) * HN;
+      const uint32_t id0 = idesc_bf16_f32(BM, n < HN ? n : HN), id1 = idesc_bf16_f32(BM, GLU ? n : n - HN);
+      for (int kb = 0; kb < kb_n; ++kb, ++it) {
+        const uint32_t s = it % XD, a = it % AD;
+        if (!(ok = wait_warp(&sh.xfull[s], (it / XD) & 1, abort_flag))) break;
+        if (!(ok = wait_warp(&sh.afull[a], (it / AD) & 1, abort_flag))) break;
+        fence_after();
+        if (elect_one()) {
+          const uint64_t dx = desc_x + s * (SH::X_BYTES / 16);
+          const uint32_t ta = tmem + A_COL + a * SH::A_COLS;
+#pragma unroll
+          for (int k = 0; k < BK / UK; ++k) {
+            const uint32_t acc = (kb | k) != 0;
+            const uint64_t b = dx + (k / 4) * (ROWS * XC * 2 / 16) + (k % 4) * (UK * 2 / 16);
+            mma_ts(d0, ta + k * (UK / 2), b, id0, acc);
+            if (GLU) mma_ts(d1, ta + BK / 2 + k * (UK / 2), b, id1, acc);
+            else if (nh == 2) mma_ts(d1, ta + k * (UK / 2), b + HN * XC * 2 / 16, id1, acc);
+          }
+          commit(&sh.done[s]);
+          if (kb == kb_n - 1) {
+            commit(&sh.tfull[half % ACCS]);
+            if (nh == 2) commit(&sh.tfull[(half + 1) % ACCS]);
+          }
+        }
+        __syncwarp();
+      }
+      half += nh;
+    }
+    if (elect_one()) commit(&sh.last);
+    __syncwarp();
+    if (lane == 0) mbar_drain(&sh.last, 0, &g_err);
+  }
+
+  fence_before();
+  __syncthreads();
+  if (lane == 0 && *abort_flag) {  // no TMA write may still be landing when the CTA exits
+    if (warp == C_WARP)
+      for (int j = sh.c_armed > C_SLOTS ? sh.c_armed - C_SLOTS : 0; j < sh.c_armed; ++j)
+        mbar_drain(&sh.cfull[j % C_SLOTS], (j / C_SLOTS) & 1, &g_err);
+    if (warp == X_WARP)
+      for (int j = sh.x_armed > XD ? sh.x_armed - XD : 0; j < sh.x_armed; ++j)
+        mbar_drain(&sh.xfull[j % XD], (j / XD) & 1, &g_err);
+  }
+  if (warp == MMA_WARP) {
+    __syncwarp();
+    fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+bool map_codes(CUtensorMap* m, const Product& pr, bool glu) {
+  auto enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = (cuuint64_t)pr.K / 2, n = (cuuint64_t)pr.N, e = (cuuint64_t)pr.E;
+  const cuuint64_t dims4[4] = {row, n, 2, e}, strides4[3] = {row, row * n, row * n * 2};
+  const cuuint64_t dims3[3] = {row, n, e}, strides3[2] = {row, row * n};
+  const cuuint32_t box[4] = {CHUNK / 2, BM, 1, 1}, step[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, glu ? 4 : 3, const_cast<uint8_t*>(pr.w.codes), glu ? dims4 : dims3,
+             glu ? strides4 : strides3, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool GLU, int ROWS, int MODE>
+cudaError_t launch_t(Product pr, cudaStream_t s) {
+  using SH = Shape<GLU, ROWS>;
+  CUtensorMap mc, mx;
+  const cuuint64_t dims[2] = {(cuuint64_t)pr.K, (cuuint64_t)pr.P}, strides[1] = {(cuuint64_t)pr.K * 2};
+  const cuuint32_t box[2] = {XC, XR};
+  if (!map_codes(&mc, pr, GLU) || !make_map_bf16(&mx, pr.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  auto kern = w4_tc_kernel<GLU, ROWS, MODE>;
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = ensure_smem_limit(kern, (int)SH::smem, smem_set);
+  if (e != cudaSuccess) return e;
+  pr.n_tiles = (pr.N + BM - 1) / BM;
+  const long long units = ((long long)pr.P / ROWS + (pr.E < pr.P ? pr.E : pr.P)) * pr.n_tiles;
+  const int sms = sm_count();
+  e = launch_kernel(kern, dim3((unsigned)(units < sms ? units : sms)), dim3(SH::THREADS), SH::smem, s, 1, true, mc, mx, pr);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+template <bool GLU, int ROWS>
+cudaError_t launch_mode(const Product& pr, cudaStream_t s) {
+  if (!pr.w.scales_bf16) return launch_t<GLU, ROWS, F32>(pr, s);
+  return pr.w.zeros != nullptr ? launch_t<GLU, ROWS, ZEROS>(pr, s) : launch_t<GLU, ROWS, SYM>(pr, s);
+}
+
+}  // namespace
+}  // namespace semmoe
