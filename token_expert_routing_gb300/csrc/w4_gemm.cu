@@ -307,31 +307,20 @@ cudaError_t launch_rows_t(Product pr, cudaStream_t s) {
   return e;
 }
 
-template <bool GLU, typename S, int GS>
-cudaError_t launch_rows(const Product& pr, cudaStream_t s) {
-  const long long rows = pr.P / (pr.E < pr.P ? pr.E : pr.P);  // of a group, on average
-#ifdef W4_NT
-  return launch_rows_t<W4_NT, W4_NT, GLU, S, GS>(pr, s);
-#endif
-  if (rows <= 4) return launch_rows_t<1, 1, GLU, S, GS>(pr, s);
-  if (rows <= 12) return launch_rows_t<2, 2, GLU, S, GS>(pr, s);
-  return launch_rows_t<4, 4, GLU, S, GS>(pr, s);
-}
-
-#ifndef W4_TC_FROM
-#define W4_TC_FROM 8
-#endif
 template <bool GLU>
 cudaError_t launch_product(const Product& pr, cudaStream_t s) {
-  if (pr.P / (pr.E < pr.P ? pr.E : pr.P) > W4_TC_FROM) return GLU ? launch_w4_tc_glu(pr, s) : launch_w4_tc_plain(pr, s);
+  // a few rows whose 128-row weight tiles would not fill the SMs
+  const int used = pr.E < pr.P ? pr.E : pr.P;
+  if (pr.P > 8LL * used || (long long)used * ((pr.N + 127) / 128) >= sm_count())
+    return GLU ? launch_w4_tc_glu(pr, s) : launch_w4_tc_plain(pr, s);
   if (pr.w.scales_bf16) {
-    if (pr.group == 32) return launch_rows<GLU, __nv_bfloat16, 4>(pr, s);
-    if (pr.group == 64) return launch_rows<GLU, __nv_bfloat16, 2>(pr, s);
-    return launch_rows<GLU, __nv_bfloat16, 1>(pr, s);
+    if (pr.group == 32) return launch_rows_t<1, 1, GLU, __nv_bfloat16, 4>(pr, s);
+    if (pr.group == 64) return launch_rows_t<1, 1, GLU, __nv_bfloat16, 2>(pr, s);
+    return launch_rows_t<1, 1, GLU, __nv_bfloat16, 1>(pr, s);
   }
-  if (pr.group == 32) return launch_rows<GLU, float, 4>(pr, s);
-  if (pr.group == 64) return launch_rows<GLU, float, 2>(pr, s);
-  return launch_rows<GLU, float, 1>(pr, s);
+  if (pr.group == 32) return launch_rows_t<1, 1, GLU, float, 4>(pr, s);
+  if (pr.group == 64) return launch_rows_t<1, 1, GLU, float, 2>(pr, s);
+  return launch_rows_t<1, 1, GLU, float, 1>(pr, s);
 }
 
 }  // namespace

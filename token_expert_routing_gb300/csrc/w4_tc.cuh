@@ -59,6 +59,9 @@ constexpr int X_BOX = XR * XC * 2;
 constexpr int ACCS = 3;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int ROUND = 16;             // token rows of a unit: a multiple of this
+// Barriers of finished k-blocks.  A wait tells a phase from the one before only, so that a role must never be a whole
+// turn of the ring behind its own wait before: an expansion group's k-blocks are at most 7 apart.
+constexpr uint32_t DONES = 16;
 
 enum Mode { SYM, ZEROS, F32 };        // bf16 scales without and with zero points; fp32 scales
 
@@ -68,7 +71,7 @@ struct Shape {
   static constexpr bool few = ROWS <= 64;
   static constexpr int HN = ROWS < 128 ? ROWS : 128;   // columns of an accumulator
   static constexpr int BK = few ? 128 : 64;            // columns of a k-block
-  static constexpr int EXP = few ? 16 : 8, EPI = few ? 4 : 8;
+  static constexpr int EXP = 16, EPI = few ? 4 : 8;
   static constexpr int THREADS = (EXP + EPI + 3) * 32;
   static constexpr int AB = GLU ? 2 : 1;               // A blocks of a k-block
   static constexpr int A_COLS = AB * BK / 2;           // TMEM columns of a k-block's
@@ -77,13 +80,13 @@ struct Shape {
   static constexpr int XD = ROWS == 32 ? 8 : ROWS == 256 ? 5 : 6;
   static constexpr int C_SLOTS = (204 * 1024 - XD * X_BYTES) / C_BYTES < 16 ? (204 * 1024 - XD * X_BYTES) / C_BYTES : 16;
   static constexpr size_t smem = 1024 + (size_t)C_SLOTS * C_BYTES + (size_t)XD * X_BYTES;
-  static_assert(AD >= 2 && XD >= AD, "rings");
+  static_assert(AD >= 2 && AD <= (int)DONES && XD <= (int)DONES && (EXP / 4 / AB - 1) * (CHUNK / BK) + 1 <= (int)DONES, "rings");
 };
 
 template <int C_SLOTS, int XD, int AD>
 struct Shared {
   uint64_t cfull[C_SLOTS], cempty[C_SLOTS], xfull[XD], afull[AD];
-  uint64_t done[XD];  // a k-block's MMAs: its token rows and A blocks may be overwritten
+  uint64_t done[DONES];  // a k-block's MMAs: its token rows and A blocks may be overwritten
   uint64_t tfull[ACCS], tempty[ACCS], last;
   uint32_t tmem_base;
   int abort_flag;
@@ -178,7 +181,11 @@ __device__ __forceinline__ void store_pair(float v0, float v1, __nv_bfloat16* fi
   const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
   const int odd = lane & 1;
   const uint32_t v = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-  if (live && odd < left) *reinterpret_cast<uint32_t*>(first + (odd ? stride : 0)) = v;
+  // (predicated: as a branch it cost four times the epilogue's time)
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(
+                   (int)(live && odd < left)),
+               "l"(first + (odd ? stride : 0)), "r"(v)
+               : "memory");
 }
 
 template <bool GLU, int ROWS, int MODE>
@@ -200,10 +207,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
       mbar_init(&sh.cfull[i], 1);
       mbar_init(&sh.cempty[i], 4);  // the warps that read it
     }
-    for (int i = 0; i < XD; ++i) {
-      mbar_init(&sh.xfull[i], 1);
-      mbar_init(&sh.done[i], 1);
-    }
+    for (int i = 0; i < XD; ++i) mbar_init(&sh.xfull[i], 1);
+    for (uint32_t i = 0; i < DONES; ++i) mbar_init(&sh.done[i], 1);
     for (int i = 0; i < AD; ++i) mbar_init(&sh.afull[i], 4 * AB);
     for (int i = 0; i < ACCS; ++i) {
       mbar_init(&sh.tfull[i], 1);
@@ -295,10 +300,13 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
         raw[0] = v[0] | (v[1] << 16), raw[1] = v[2] | (v[3] << 16);
       }
     };
-    // scale i of the loaded chunk (i < gs)
-    auto scale_of = [&](int i) {
-      if (MODE == F32) return __uint_as_float(raw[MODE == F32 ? i : 0]);
-      return __uint_as_float(i & 1 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16);
+    // the factors of 32 columns, quarter i of a chunk whose scales are v and z
+    auto factors_of = [&](const uint32_t (&v)[MODE == F32 ? 4 : 2], uint32_t z, int i) {
+      const int j = gs == 4 ? i : gs == 2 ? i / 2 : 0;
+      uint32_t s;
+      if (MODE == F32) s = i < 2 ? (j == 0 ? v[0] : v[1]) : j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[MODE == F32 ? 2 : 0] : v[MODE == F32 ? 3 : 0];
+      else s = j & 1 ? (j & 2 ? v[1] : v[0]) & 0xffff0000u : (j & 2 ? v[1] : v[0]) << 16;
+      return factors<MODE>(__uint_as_float(s), z >> (8 * j));
     };
     int u = blockIdx.x, ch = GLU ? wg >> 1 : wg;
     uint32_t before = 0;  // units before u
@@ -315,17 +323,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     bool ok = true;
     while (ok && u < total) {
       const uint32_t cg = before * ch_n + ch, j = cg * AB + ab, slot = j % C_SLOTS;
-      Factors f[4];
+      uint32_t now[MODE == F32 ? 4 : 2], nowz = rawz;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int g = gs == 4 ? i : gs == 2 ? i / 2 : 0;
-        if (i == 0 || gs == 4 || (gs == 2 && i == 2)) {
-          const float s = i == 0 ? scale_of(0) : gs == 4 ? scale_of(i) : scale_of(1);
-          f[i] = factors<MODE>(s, rawz >> (8 * g));
-        } else {
-          f[i] = f[i - 1];
-        }
-      }
+      for (int i = 0; i < (MODE == F32 ? 4 : 2); ++i) now[i] = raw[i];
       const uint32_t it0 = before * kb_n + ch * (CHUNK / BK);
       const int blocks = kb_n - ch * (CHUNK / BK);  // k-blocks from here on
       ch += STEP;
@@ -348,14 +348,15 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          expand<MODE>(c[i].x, f[2 * h + i], w + 16 * i);
-          expand<MODE>(c[i].y, f[2 * h + i], w + 16 * i + 4);
-          expand<MODE>(c[i].z, f[2 * h + i], w + 16 * i + 8);
-          expand<MODE>(c[i].w, f[2 * h + i], w + 16 * i + 12);
+          const Factors f = factors_of(now, nowz, 2 * h + i);
+          expand<MODE>(c[i].x, f, w + 16 * i);
+          expand<MODE>(c[i].y, f, w + 16 * i + 4);
+          expand<MODE>(c[i].z, f, w + 16 * i + 8);
+          expand<MODE>(c[i].w, f, w + 16 * i + 12);
         }
         const uint32_t it = it0 + (BK == 64 ? h : 0);
         if ((BK == 64 || h == 0) && it >= AD) {  // the MMAs that read this place
-          if (!(ok = wait_warp(&sh.done[(it - AD) % XD], ((it - AD) / XD) & 1, abort_flag))) break;
+          if (!(ok = wait_warp(&sh.done[(it - AD) % DONES], ((it - AD) / DONES) & 1, abort_flag))) break;
           fence_after();
         }
         tmem_st32(a_lane + (it % AD) * SH::A_COLS + (BK == 128 ? h * 32 : 0), w);
@@ -372,7 +373,6 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
   } else if (warp < C_WARP) {
     // ---------------- epilogue ----------------
     constexpr int PART = HN / (SH::EPI / 4);              // columns of a group of four warps
-    constexpr int W = PART < 32 ? PART : 32;              // a load
     constexpr float kUnscale = 1099511627776.0f;          // 2^40
     const int q = warp & 3, w = (warp - EPI0) >> 2;
     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + PART * w;
@@ -393,31 +393,23 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
         fence_after();
         const int left = un.rows - PART * w;
         const uint32_t tg = t_row + (half % ACCS) * HN, tu = t_row + ((half + 1) % ACCS) * HN;
-        uint32_t g[PART / W][32];
-        if (left > 0) {
-#pragma unroll
-          for (int c = 0; c < PART / W; ++c)
-            if (left > W * c) tmem_ld32(tg + W * c, g[c]);
+        // pieces of 16 columns: the registers of 27 warps hold no more (the accumulators are held for the whole of it)
+#pragma unroll 1
+        for (int c = 0; c < PART; c += 16) {
+          if (left <= c) break;
+          uint32_t g[16], up[16];
+          tmem_ld16(tg + c, g);
+          tmem_ld16(tu + c, up);
           tmem_ld_wait();
-        }
-        leave_acc(half);
+          if (c + 16 >= PART || left <= c + 16) leave_acc(half), leave_acc(half + 1);
 #pragma unroll
-        for (int c = 0; c < PART / 16; ++c) {
-          if (left > 16 * c) {
-            uint32_t up[16];
-            tmem_ld16(tu + 16 * c, up);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const uint32_t* gc = g[16 * c / W] + 16 * c % W;
-              const int t = 16 * c + i;
-              const float v0 = swiglu(__uint_as_float(gc[i]) * kUnscale, __uint_as_float(up[i]) * kUnscale);
-              const float v1 = swiglu(__uint_as_float(gc[i + 1]) * kUnscale, __uint_as_float(up[i + 1]) * kUnscale);
-              store_pair(v0, v1, col + (size_t)(PART * w + t) * pr.N, pr.N, left - t, live, lane);
-            }
+          for (int i = 0; i < 16; i += 2) {
+            const float v0 = swiglu(__uint_as_float(g[i]) * kUnscale, __uint_as_float(up[i]) * kUnscale);
+            const float v1 = swiglu(__uint_as_float(g[i + 1]) * kUnscale, __uint_as_float(up[i + 1]) * kUnscale);
+            store_pair(v0, v1, col + (size_t)(PART * w + c + i) * pr.N, pr.N, left - c - i, live, lane);
           }
         }
-        leave_acc(half + 1);
+        if (left <= 0) leave_acc(half), leave_acc(half + 1);
         half += 2;
       } else {
         const int nh = un.rows > HN ? 2 : 1;
@@ -427,25 +419,19 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
           fence_after();
           const int t0 = h * HN + PART * w, left = un.rows - t0;
           const uint32_t ty = t_row + (half % ACCS) * HN;
-          uint32_t y[PART / W][32];
-          if (left > 0) {
-#pragma unroll
-            for (int c = 0; c < PART / W; ++c)
-              if (left > W * c) tmem_ld32(ty + W * c, y[c]);
+#pragma unroll 1
+          for (int c = 0; c < PART; c += 32) {
+            if (left <= c) break;
+            uint32_t y[32];
+            tmem_ld32(ty + c, y);
             tmem_ld_wait();
-          }
-          leave_acc(half);
+            if (c + 32 >= PART || left <= c + 32) leave_acc(half);
 #pragma unroll
-          for (int c = 0; c < PART / W; ++c) {
-            if (left > W * c) {
-#pragma unroll
-              for (int i = 0; i < W; i += 2) {
-                const int t = W * c + i;
-                store_pair(__uint_as_float(y[c][i]) * kUnscale, __uint_as_float(y[c][i + 1]) * kUnscale,
-                           col + (size_t)(t0 + t) * pr.N, pr.N, left - t, live, lane);
-              }
-            }
+            for (int i = 0; i < 32; i += 2)
+              store_pair(__uint_as_float(y[i]) * kUnscale, __uint_as_float(y[i + 1]) * kUnscale,
+                         col + (size_t)(t0 + c + i) * pr.N, pr.N, left - c - i, live, lane);
           }
+          if (left <= 0) leave_acc(half);
         }
         if (!ok) break;
       }
@@ -478,7 +464,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
       const int boxes = (un.rows + XR - 1) / XR;
       for (int kb = 0; kb < kb_n; ++kb, ++it) {
         const uint32_t s = it % XD;
-        if (it >= XD && !(ok = wait_warp(&sh.done[s], ((it / XD) & 1) ^ 1, abort_flag))) break;
+        if (it >= XD && !(ok = wait_warp(&sh.done[(it - XD) % DONES], ((it - XD) / DONES) & 1, abort_flag))) break;
         if (elect_one()) {
           mbar_expect_tx(&sh.xfull[s], boxes * (BK / XC) * X_BOX);
           for (int b = 0; b < boxes; ++b)
@@ -522,7 +508,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
             if (GLU) mma_ts(d1, ta + BK / 2 + k * (UK / 2), b, id1, acc);
             else if (nh == 2) mma_ts(d1, ta + k * (UK / 2), b + HN * XC * 2 / 16, id1, acc);
           }
-          commit(&sh.done[s]);
+          commit(&sh.done[it % DONES]);
           if (kb == kb_n - 1) {
             commit(&sh.tfull[half % ACCS]);
             if (nh == 2) commit(&sh.tfull[(half + 1) % ACCS]);
