@@ -59,9 +59,7 @@ constexpr int X_BOX = XR * XC * 2;
 constexpr int ACCS = 3;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int ROUND = 16;             // token rows of a unit: a multiple of this
-// Barriers of finished k-blocks.  A wait tells a phase from the one before only, so that a role must never be a whole
-// turn of the ring behind its own wait before: an expansion group's k-blocks are at most 7 apart.
-constexpr uint32_t DONES = 16;
+constexpr uint32_t DONES = 16;        // barriers of finished k-blocks
 
 enum Mode { SYM, ZEROS, F32 };        // bf16 scales without and with zero points; fp32 scales
 
@@ -78,9 +76,15 @@ struct Shape {
   static constexpr int AD = (TMEM_COLS - ACCS * HN) / A_COLS;
   static constexpr int X_BYTES = ROWS * BK * 2;        // a stage of token rows
   static constexpr int XD = ROWS == 32 ? 8 : ROWS == 256 ? 5 : 6;
-  static constexpr int C_SLOTS = (204 * 1024 - XD * X_BYTES) / C_BYTES < 16 ? (204 * 1024 - XD * X_BYTES) / C_BYTES : 16;
+  static constexpr int C_FIT = (208 * 1024 - XD * X_BYTES) / C_BYTES, C_SLOTS = C_FIT < 16 ? C_FIT : 16;
   static constexpr size_t smem = 1024 + (size_t)C_SLOTS * C_BYTES + (size_t)XD * X_BYTES;
-  static_assert(AD >= 2 && AD <= (int)DONES && XD <= (int)DONES && (EXP / 4 / AB - 1) * (CHUNK / BK) + 1 <= (int)DONES, "rings");
+  static constexpr int STEP = EXP / 4 / AB, BLOCKS = CHUNK / BK;  // chunks between an expansion group's, k-blocks of one
+  static_assert(AD >= 2 && AD <= (int)DONES && XD <= (int)DONES, "rings");
+  // A wait tells a barrier's phase from the one before it only: whoever waits for a phase must know that the one before it
+  // is over.  Roles that take every turn know; an expansion group, which skips the others' turns, knows that the k-blocks
+  // AD before its last one are done.
+  static_assert((STEP - 1) * BLOCKS + 1 <= (int)DONES, "the turns of done[] that a group skips");
+  static_assert(C_SLOTS >= AB * (STEP + (AD + BLOCKS - 1) / BLOCKS), "the turns of cfull[] that a group skips");
 };
 
 template <int C_SLOTS, int XD, int AD>
@@ -165,12 +169,32 @@ __device__ __forceinline__ void expand(uint32_t w, const Factors& f, uint32_t* r
   }
 }
 
+// silu(g) * u of sums held as g 2^-40 and u 2^-40.
+__device__ __forceinline__ float unscaled_swiglu(float g, float u) {
+  constexpr float k40 = 1099511627776.0f;
+  const float z = g * k40;
+  return __fdividef(z, 1.0f + __expf(-z)) * (u * k40);
+}
+
 // mbar_wait by a whole converged warp, polling a few times before it looks at the clock.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
 #pragma unroll 1
   for (int i = 0; i < 16; ++i)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return mbar_wait_warp(bar, parity, abort_flag, &g_err);
+}
+
+// Whether a phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Two tokens' columns of a warp's 32 weight rows (v0, v1: this lane's row): even lanes
@@ -238,95 +262,89 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
 
   if (warp < SH::EXP) {
     // ---------------- codes to bf16 weights in TMEM ----------------
-    constexpr int STEP = SH::EXP / 4 / AB;              // chunks between this group's
+    constexpr int STEP = SH::STEP;
+    constexpr int SB = MODE == F32 ? 4 : 2;             // bytes of a scale
+    constexpr int NR = MODE == F32 ? 4 : 2;             // registers of a chunk's scales
     const int wg = warp / 4, ab = GLU ? wg & 1 : 0, r = (warp % 4) * 32 + lane;
     const int KG = K / pr.group, rows_w = GLU ? 2 * pr.N : pr.N;
     const int gs = pr.group >= CHUNK ? 1 : CHUNK / pr.group;    // scales of a chunk
-    const bool whole = K % CHUNK == 0;                          // a chunk's scales are aligned to their size
+    const bool whole = gs == 1 || K % CHUNK == 0;               // a chunk's scales are aligned to their size
     const int per = pr.group > CHUNK ? pr.group / CHUNK : 1;    // chunks of a scale
     const uint32_t a_lane = tmem + ((uint32_t)((warp % 4) * 32) << 16) + A_COL + ab * (BK / 2);
-    size_t srow = 0;  // the row's first scale
+    const unsigned char* srow = nullptr;  // the row's scales and zero points
+    const uint8_t* zrow = nullptr;
     auto at_row = [&](const Unit& un) {
       int n = un.nt * BM + r;
       if (n >= pr.N) n = pr.N - 1;  // a row past the matrix: its codes are 0, nothing of it is stored
-      srow = ((size_t)un.e * rows_w + n + (GLU && ab ? pr.N : 0)) * KG;
+      const size_t at = ((size_t)un.e * rows_w + n + (GLU && ab ? pr.N : 0)) * KG;
+      srow = static_cast<const unsigned char*>(pr.w.scales) + at * SB;
+      if (MODE != SYM) zrow = pr.w.zeros != nullptr ? pr.w.zeros + at : nullptr;
     };
     // a chunk's scales and zero points as they lie in memory, loaded one chunk of this group ahead
-    uint32_t raw[MODE == F32 ? 4 : 2], rawz = 0x08080808u;
+    uint32_t raw[NR], rawz = 0x08080808u;
     auto load = [&](int ch) {
-      const size_t at = srow + (gs > 1 ? ch * gs : per > 1 ? ch / per : ch);
-      if (gs == 1 || whole) {
-        if (MODE == F32) {
-          const float* p = static_cast<const float*>(pr.w.scales) + at;
-          if (gs == 1) raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          if (gs == 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-            raw[0] = v.x, raw[1] = v.y;
-          }
-          if (gs == 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-            raw[0] = v.x, raw[1] = v.y, raw[MODE == F32 ? 2 : 0] = v.z, raw[MODE == F32 ? 3 : 1] = v.w;
-          }
-        } else {
-          const unsigned short* p = static_cast<const unsigned short*>(pr.w.scales) + at;
-          if (gs == 1) raw[0] = __ldg(p);
-          if (gs == 2) raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          if (gs == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-            raw[0] = v.x, raw[1] = v.y;
-          }
+      const int i0 = per > 1 ? ch / per : ch * gs;
+      if (whole) {
+        const unsigned char* p = srow + i0 * SB;
+        if (gs * SB == 2) raw[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        if (gs * SB == 4) raw[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        if (gs * SB == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+          raw[0] = v.x, raw[1] = v.y;
         }
-        if (MODE != SYM && pr.w.zeros != nullptr) {
-          const uint8_t* p = pr.w.zeros + at;
-          if (gs == 1) rawz = __ldg(p);
-          if (gs == 2) rawz = __ldg(reinterpret_cast<const unsigned short*>(p));
-          if (gs == 4) rawz = __ldg(reinterpret_cast<const uint32_t*>(p));
+        if (MODE == F32 && gs == 4) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+          raw[0] = v.x, raw[1] = v.y, raw[NR - 2] = v.z, raw[NR - 1] = v.w;
+        }
+        if (MODE != SYM && zrow != nullptr) {
+          if (gs == 1) rawz = __ldg(zrow + i0);
+          if (gs == 2) rawz = __ldg(reinterpret_cast<const unsigned short*>(zrow + i0));
+          if (gs == 4) rawz = __ldg(reinterpret_cast<const uint32_t*>(zrow + i0));
         }
         return;
       }
       uint32_t v[4], z = 0;  // scale by scale; past K the last one again (codes and token rows are 0 there)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const size_t j = srow + (ch * gs + i < KG ? ch * gs + i : KG - 1);
-        v[i] = MODE == F32 ? __ldg(static_cast<const uint32_t*>(pr.w.scales) + j)
-                           : __ldg(static_cast<const unsigned short*>(pr.w.scales) + j);
-        if (MODE != SYM) z |= (pr.w.zeros != nullptr ? (uint32_t)__ldg(pr.w.zeros + j) : 8u) << (8 * i);
+        const int j = i0 + i < KG ? i0 + i : KG - 1;
+        v[i] = MODE == F32 ? __ldg(reinterpret_cast<const uint32_t*>(srow) + j)
+                           : __ldg(reinterpret_cast<const unsigned short*>(srow) + j);
+        if (MODE != SYM) z |= (zrow != nullptr ? (uint32_t)__ldg(zrow + j) : 8u) << (8 * i);
       }
-      rawz = z;
+      if (MODE != SYM) rawz = z;
       if (MODE == F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[MODE == F32 ? i : 0] = v[i];
+        raw[0] = v[0], raw[1] = v[1], raw[NR - 2] = v[2], raw[NR - 1] = v[3];
       } else {
         raw[0] = v[0] | (v[1] << 16), raw[1] = v[2] | (v[3] << 16);
       }
     };
-    // the factors of 32 columns, quarter i of a chunk whose scales are v and z
-    auto factors_of = [&](const uint32_t (&v)[MODE == F32 ? 4 : 2], uint32_t z, int i) {
-      const int j = gs == 4 ? i : gs == 2 ? i / 2 : 0;
+    // the factors of scale j of a chunk
+    auto factors_of = [&](const uint32_t (&v)[NR], uint32_t z, int j) {
       uint32_t s;
-      if (MODE == F32) s = i < 2 ? (j == 0 ? v[0] : v[1]) : j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[MODE == F32 ? 2 : 0] : v[MODE == F32 ? 3 : 0];
-      else s = j & 1 ? (j & 2 ? v[1] : v[0]) & 0xffff0000u : (j & 2 ? v[1] : v[0]) << 16;
+      if (MODE == F32) s = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[NR - 2] : v[NR - 1];
+      else s = j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16;
       return factors<MODE>(__uint_as_float(s), z >> (8 * j));
     };
+    // this group's place: unit u, chunk ch of it; its slot of codes and first k-block, counted from the start
     int u = blockIdx.x, ch = GLU ? wg >> 1 : wg;
-    uint32_t before = 0;  // units before u
-    auto settle = [&]() {  // the place: of a unit's chunks
-      while (ch >= ch_n) ch -= ch_n, u += units, ++before;
+    uint32_t slot = ch * AB + ab, slot_phase = 0, first = 0;  // first: k-blocks of the units before
+    auto settle = [&]() {
+      while (ch >= ch_n) ch -= ch_n, u += units, first += kb_n;
     };
     settle();
-    int loaded = -1;  // the unit whose row srow is
+    int loaded = -1;  // the unit of srow
     if (u < total) {
       at_row(unit_at(u));
       loaded = u;
       load(ch);
     }
     bool ok = true;
-    while (ok && u < total) {
-      const uint32_t cg = before * ch_n + ch, j = cg * AB + ab, slot = j % C_SLOTS;
-      uint32_t now[MODE == F32 ? 4 : 2], nowz = rawz;
+    while (u < total) {
+      uint32_t now[NR];
+      const uint32_t nowz = rawz;
 #pragma unroll
-      for (int i = 0; i < (MODE == F32 ? 4 : 2); ++i) now[i] = raw[i];
-      const uint32_t it0 = before * kb_n + ch * (CHUNK / BK);
+      for (int i = 0; i < NR; ++i) now[i] = raw[i];
+      const uint32_t it0 = first + ch * (CHUNK / BK);
       const int blocks = kb_n - ch * (CHUNK / BK);  // k-blocks from here on
       ch += STEP;
       settle();
@@ -337,38 +355,48 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
         }
         load(ch);
       }
-      if (!(ok = wait_warp(&sh.cfull[slot], (j / C_SLOTS) & 1, abort_flag))) break;
+      if (!(ok = wait_warp(&sh.cfull[slot], slot_phase, abort_flag))) break;
       const unsigned char* src = codes + slot * C_BYTES + r * 64;
+      Factors fa, fb;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // 64 columns
         if (BK == 64 && h >= blocks) break;
         uint4 c[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) c[i] = *reinterpret_cast<const uint4*>(src + (((2 * h + i) ^ ((r >> 1) & 3)) << 4));
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Factors f = factors_of(now, nowz, 2 * h + i);
-          expand<MODE>(c[i].x, f, w + 16 * i);
-          expand<MODE>(c[i].y, f, w + 16 * i + 4);
-          expand<MODE>(c[i].z, f, w + 16 * i + 8);
-          expand<MODE>(c[i].w, f, w + 16 * i + 12);
+        if (gs == 4) {
+          fa = factors_of(now, nowz, 2 * h);
+          fb = factors_of(now, nowz, 2 * h + 1);
+        } else if (h == 0 || gs == 2) {
+          fb = fa = factors_of(now, nowz, h);
         }
-        const uint32_t it = it0 + (BK == 64 ? h : 0);
+        uint32_t w[32];
+        expand<MODE>(c[0].x, fa, w);
+        expand<MODE>(c[0].y, fa, w + 4);
+        expand<MODE>(c[0].z, fa, w + 8);
+        expand<MODE>(c[0].w, fa, w + 12);
+        expand<MODE>(c[1].x, fb, w + 16);
+        expand<MODE>(c[1].y, fb, w + 20);
+        expand<MODE>(c[1].z, fb, w + 24);
+        expand<MODE>(c[1].w, fb, w + 28);
+        const uint32_t it = it0 + (BK == 64 ? h : 0), place = it % AD;
         if ((BK == 64 || h == 0) && it >= AD) {  // the MMAs that read this place
           if (!(ok = wait_warp(&sh.done[(it - AD) % DONES], ((it - AD) / DONES) & 1, abort_flag))) break;
           fence_after();
         }
-        tmem_st32(a_lane + (it % AD) * SH::A_COLS + (BK == 128 ? h * 32 : 0), w);
+        tmem_st32(a_lane + place * SH::A_COLS + (BK == 128 ? h * 32 : 0), w);
         if (BK == 64 || h == 1) {
           tmem_st_wait();
           fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.afull[it % AD]);
+          if (lane == 0) mbar_arrive(&sh.afull[place]);
         }
       }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.cempty[slot]);
+      slot += STEP * AB;
+      if (slot >= C_SLOTS) slot -= C_SLOTS, slot_phase ^= 1;
     }
   } else if (warp < C_WARP) {
     // ---------------- epilogue ----------------
@@ -404,8 +432,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
           if (c + 16 >= PART || left <= c + 16) leave_acc(half), leave_acc(half + 1);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float v0 = swiglu(__uint_as_float(g[i]) * kUnscale, __uint_as_float(up[i]) * kUnscale);
-            const float v1 = swiglu(__uint_as_float(g[i + 1]) * kUnscale, __uint_as_float(up[i + 1]) * kUnscale);
+            const float v0 = unscaled_swiglu(__uint_as_float(g[i]), __uint_as_float(up[i]));
+            const float v1 = unscaled_swiglu(__uint_as_float(g[i + 1]), __uint_as_float(up[i + 1]));
             store_pair(v0, v1, col + (size_t)(PART * w + c + i) * pr.N, pr.N, left - c - i, live, lane);
           }
         }
@@ -479,8 +507,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     if (lane == 0) *reinterpret_cast<volatile int*>(&sh.x_armed) = (int)it;
   } else {
     // ---------------- MMA issuer ----------------
-    uint32_t it = 0, half = 0;
-    bool ok = true;
+    uint32_t it = 0, half = 0, s = 0, s_phase = 0, a = 0, a_phase = 0;  // k-block, half tile; places and phases
+    bool ok = true, ready = false;  // ready: this k-block's operands have been seen
     const uint64_t desc_x = sw128_desc(smem_u32(xs));  // its address field counts 16 bytes
     for (int u = blockIdx.x; ok && u < total; u += units) {
       const Unit un = unit_at(u);
@@ -492,29 +520,42 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
       fence_after();
       const uint32_t d0 = tmem + (half % ACCS) * HN, d1 = tmem + ((half + 1) % ACCS) * HN;
       const uint32_t id0 = idesc_bf16_f32(BM, n < HN ? n : HN), id1 = idesc_bf16_f32(BM, GLU ? n : n - HN);
-      for (int kb = 0; kb < kb_n; ++kb, ++it) {
-        const uint32_t s = it % XD, a = it % AD;
-        if (!(ok = wait_warp(&sh.xfull[s], (it / XD) & 1, abort_flag))) break;
-        if (!(ok = wait_warp(&sh.afull[a], (it / AD) & 1, abort_flag))) break;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!ready) {
+          if (!(ok = wait_warp(&sh.xfull[s], s_phase, abort_flag))) break;
+          if (!(ok = wait_warp(&sh.afull[a], a_phase, abort_flag))) break;
+        }
         fence_after();
-        if (elect_one()) {
-          const uint64_t dx = desc_x + s * (SH::X_BYTES / 16);
-          const uint32_t ta = tmem + A_COL + a * SH::A_COLS;
+        const uint64_t dx = desc_x + s * (SH::X_BYTES / 16);
+        const uint32_t ta = tmem + A_COL + a * SH::A_COLS;
+        auto issue = [&](int k0, int k1) {
 #pragma unroll
-          for (int k = 0; k < BK / UK; ++k) {
+          for (int k = k0; k < k1; ++k) {
             const uint32_t acc = (kb | k) != 0;
             const uint64_t b = dx + (k / 4) * (ROWS * XC * 2 / 16) + (k % 4) * (UK * 2 / 16);
             mma_ts(d0, ta + k * (UK / 2), b, id0, acc);
             if (GLU) mma_ts(d1, ta + BK / 2 + k * (UK / 2), b, id1, acc);
             else if (nh == 2) mma_ts(d1, ta + k * (UK / 2), b + HN * XC * 2 / 16, id1, acc);
           }
-          commit(&sh.done[it % DONES]);
+        };
+        // The issue of an MMA waits for the ones before it, and a look at a barrier takes as long as one or two of
+        // them, so the next k-block's barriers are looked at between this one's MMAs.
+        if (elect_one()) issue(0, BK / UK / 2);
+        __syncwarp();
+        const uint32_t done = it++ % DONES;
+        if (++s == XD) s = 0, s_phase ^= 1;
+        if (++a == AD) a = 0, a_phase ^= 1;
+        const bool next_x = mbar_test(&sh.xfull[s], s_phase), next_a = mbar_test(&sh.afull[a], a_phase);
+        if (elect_one()) {
+          issue(BK / UK / 2, BK / UK);
+          commit(&sh.done[done]);
           if (kb == kb_n - 1) {
             commit(&sh.tfull[half % ACCS]);
             if (nh == 2) commit(&sh.tfull[(half + 1) % ACCS]);
           }
         }
         __syncwarp();
+        ready = __all_sync(0xffffffffu, next_x && next_a);
       }
       half += nh;
     }
