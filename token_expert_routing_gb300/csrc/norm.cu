@@ -8,8 +8,9 @@
 // What bounds them: bytes.  A row stays in registers from its loads to its
 // stores, so every input is read once and y never reaches memory; the squares are taken
 // about the mean in a second sweep over the registers, not as a difference of sums.
-// A row belongs to one warp while it fits 32 lanes x 4 pieces of 16 bytes, else to one
-// CTA with 1, 2 or 4 pieces a thread.
+// A row belongs to one warp while it fits 32 lanes x 4 pieces of 16 bytes, else to one CTA.
+// Measured (GB300): the norm of 16384 x 2048 bf16, 23.4 us (5.7 TB/s); the combine of 8 rows a token with both norms, a gate
+// per channel and the residual, 16384 x 2048 bf16, 139 us (5.3 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -21,12 +22,18 @@ __device__ int g_err;
 __device__ __forceinline__ void flag(int bit) { atomicOr(&g_err, bit); }
 
 constexpr int kWarpRows = 4;     // rows of a CTA whose rows belong to warps
+constexpr int PIECES = 2;        // of 16 bytes a thread, of many rows (more only where a CTA's threads would not do)
+constexpr int RING = 4;          // rows on their way to a row's threads, and the one in use
 constexpr int kMaxWarps = 32;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Threads of a CTA (plan below): rows of up to 512 pieces take 256, longer ones up to 512.
+// Threads of a CTA (plan below), and CTAs that an SM's registers have to hold.
 template <bool WARP, int CH>
 constexpr int max_threads() { return WARP ? 32 * kWarpRows : CH == 4 ? 512 : 256; }
+template <bool WARP, int CH>
+constexpr int norm_ctas() { return WARP ? (CH == 4 ? 6 : 8) : CH == 1 ? 5 : CH == 2 ? 4 : 1; }
+template <bool WARP, int CH>
+constexpr int min_ctas() { return WARP ? (CH == 4 ? 6 : 8) : CH == 1 ? 4 : CH == 2 ? 3 : 1; }
 
 // VEC weights from `col` on, fp32 or bf16 (16-byte aligned base; col a multiple of VEC).
 template <int VEC>
@@ -77,9 +84,9 @@ struct RowReduce {
   }
 };
 
-// What turns a row's values into normalised ones: (v * scale - mean) * rstd.
+// What turns a row's values into normalised ones: v * a + b.
 struct RowStats {
-  float scale, mean, rstd;
+  float a, b;
 };
 
 // Columns past the row's end hold 0 and are left out of the squares about the mean.
@@ -90,7 +97,7 @@ template <bool WARP, int CH, int VEC>
 __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kind, int H, float eps, int col0, int step,
                                               RowReduce& red) {
   const float inv = 1.0f / (float)H;
-  RowStats st{1.0f, 0.0f, 0.0f};
+  float scale = 1.0f, mean = 0.0f;
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     if (kind == SEMMOE_NORM_LAYER) {
@@ -98,22 +105,30 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kin
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s += v[c][i] * st.scale;
-      st.mean = red.run<WARP, false>(s) * inv;
+        for (int i = 0; i < VEC; ++i) s += pass ? v[c][i] * scale : v[c][i];
+      mean = red.run<WARP, false>(s) * inv;
     }
     float ss = 0.f;
+    if (pass || kind == SEMMOE_NORM_LAYER) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (col0 + c * step < H) {
+      for (int c = 0; c < CH; ++c) {
+        if (col0 + c * step < H) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float d = fmaf(v[c][i], st.scale, -st.mean);
-          ss = fmaf(d, d, ss);
+          for (int i = 0; i < VEC; ++i) {
+            const float d = fmaf(v[c][i], scale, -mean);
+            ss = fmaf(d, d, ss);
+          }
         }
       }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ss = fmaf(v[c][i], v[c][i], ss);
     }
     ss = red.run<WARP, false>(ss);
-    st.rstd = rsqrtf(fmaf(ss, inv, eps * st.scale * st.scale));
+    const float rstd = rsqrtf(fmaf(ss, inv, eps * scale * scale));
+    const RowStats st{scale * rstd, -mean * rstd};
     if (pass || ((ss >= 1e-30f || eps >= 1e-20f) && ss <= 1e36f)) return st;
     float m = 0.f;
 #pragma unroll
@@ -124,7 +139,7 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kin
     const unsigned e = __float_as_uint(m) >> 23;
     if (e == 0 || e == 255) return st;  // zeros or denormals, or an infinity (the maximum is never NaN)
     // at most 1 / sqrt(eps): eps keeps its place beside the squares
-    st.scale = fminf(__uint_as_float((e < 254 ? 254u - e : 1u) << 23), rsqrtf(eps));
+    scale = fminf(__uint_as_float((e < 254 ? 254u - e : 1u) << 23), rsqrtf(eps));
   }
 }
 
@@ -133,7 +148,7 @@ template <int VEC>
 __device__ __forceinline__ void apply_norm(float (&v)[VEC], const RowStats& st, const void* weight, const void* bias,
                                            bool w_bf16, float offset, int col) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], st.scale, -st.mean) * st.rstd;
+  for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], st.a, st.b);
   if (weight != nullptr) {
     float w[VEC];
     load_weights(weight, w_bf16, col, w);
@@ -148,13 +163,12 @@ __device__ __forceinline__ void apply_norm(float (&v)[VEC], const RowStats& st, 
   }
 }
 
-// One row at a time per warp or CTA; the next row's loads are issued before this
-// row's reductions.
+// One row at a time per warp or CTA: the loads of the AHEAD next rows are in flight, in registers, through this row's reductions.
 template <typename T, bool WARP, int CH>
-__global__ void __launch_bounds__(max_threads<WARP, CH>())
-norm_kernel(const T* x, int T_, int H, NormArgs n, T* out) {
+__global__ void __launch_bounds__(max_threads<WARP, CH>(), norm_ctas<WARP, CH>())
+norm_kernel(const T* x, int T_, int H, const __grid_constant__ NormArgs n, T* out) {
   using V = Vec16<T>;
-  constexpr int VEC = V::N;
+  constexpr int VEC = V::N, AHEAD = CH == 1 ? 2 : 1;
   __shared__ float part[2][kMaxWarps];
   RowReduce red{part, 0};
   pdl_trigger();
@@ -162,127 +176,200 @@ norm_kernel(const T* x, int T_, int H, NormArgs n, T* out) {
   const int tid = WARP ? threadIdx.x % 32 : threadIdx.x, per = WARP ? 32 : blockDim.x;
   const int rows = WARP ? kWarpRows : 1, row_of = WARP ? threadIdx.x / 32 : 0;
   const int col0 = tid * VEC, step = per * VEC;
-  uint4 raw[CH];
-  auto fetch = [&](long long t) {
+  uint4 raw[AHEAD][CH];
+  auto fetch = [&](long long t, uint4 (&r)[CH]) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = col0 + c * step;
-      raw[c] = t < T_ && col < H ? *reinterpret_cast<const uint4*>(x + (size_t)t * H + col) : make_uint4(0, 0, 0, 0);
+      r[c] = t < T_ && col < H ? *reinterpret_cast<const uint4*>(x + (size_t)t * H + col) : make_uint4(0, 0, 0, 0);
     }
   };
   long long t = (long long)blockIdx.x * rows + row_of;
   const long long stride = (long long)gridDim.x * rows;
-  fetch(t);
-  for (; t < T_; t += stride) {
-    float v[CH][VEC];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) V::unpack(raw[c], v[c]);
-    fetch(t + stride);
-    const RowStats st = row_stats<WARP, CH, VEC>(v, n.kind, H, n.eps, col0, step, red);
+  for (int i = 0; i < AHEAD; ++i) fetch(t + i * stride, raw[i]);
+  while (t < T_) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      if (col < H) {
-        apply_norm<VEC>(v[c], st, n.weight, n.bias, n.w_bf16, n.offset, col);
-        V::store(out + (size_t)t * H + col, v[c]);
+    for (int i = 0; i < AHEAD; ++i) {
+      if (t >= T_) break;
+      float v[CH][VEC];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) V::unpack(raw[i][c], v[c]);
+      fetch(t + AHEAD * stride, raw[i]);
+      const RowStats st = row_stats<WARP, CH, VEC>(v, n.kind, H, n.eps, col0, step, red);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = col0 + c * step;
+        if (col < H) {
+          apply_norm<VEC>(v[c], st, n.weight, n.bias, n.w_bf16, n.offset, col);
+          V::store(out + (size_t)t * H + col, v[c]);
+        }
       }
+      t += stride;
     }
   }
 }
 
-// As norm_kernel, with the row summed from the token's expert rows (JB slots' loads in
-// flight at a time; lane j of each warp holds slot j's sorted row and gate).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The rows that a token needs, in the order in which they are used, as a warp's lanes write them down when the copies come
+// to it: the shared experts', its slots', a gate's own, the residual's.  At most 32 slots; an empty list has one item, NULL.
+struct Token {
+  const void* row[36];
+  float weight[32];  // of the slots
+  int items, slots;
+};
+
+// One row at a time per warp or CTA.  The rows that a token needs -- the shared experts', its slots', a gate's, the residual's
+// -- pass one after the other through a ring of RING of them in shared memory: a thread copies its own pieces of the next
+// RING - 1 rows asynchronously, into the next tokens' too, so that bytes stay in flight through the reductions and nothing is
+// waited for but its own copies.
+// Lane j of each warp reads slot j's sorted row and gate, one token ahead of the copies (up to 32 slots; the ones behind
+// are read where they are used).
 template <typename T, bool WARP, int CH>
-__global__ void __launch_bounds__(max_threads<WARP, CH>(), WARP ? (CH == 1 ? 8 : 4) : CH == 1 ? 4 : CH == 2 ? 2 : 1)
-combine_norm_kernel(const T* y_perm, const int32_t* __restrict__ pair_to_sorted, const float* __restrict__ topk_w,
-                    const T* y_shared, int T_, int H, int k_max, int P, NormArgs post, NormArgs next, const void* gate,
-                    bool gate_bf16, bool gate_per_row, float block_scale, const T* residual, float residual_scale, T* out,
-                    T* next_out) {
+__global__ void __launch_bounds__(max_threads<WARP, CH>(), min_ctas<WARP, CH>())
+combine_norm_kernel(const __grid_constant__ CombineNorm a) {
   using V = Vec16<T>;
-  constexpr int VEC = V::N, JB = CH == 1 ? 4 : CH == 2 ? 3 : 2;
+  constexpr int VEC = V::N;
+  extern __shared__ uint4 ring[];  // [RING][CH][threads], then the lists of RING tokens a warp
   __shared__ float part[2][kMaxWarps];
   RowReduce red{part, 0};
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, T_ = a.T, H = a.H;
   const int tid = WARP ? lane : threadIdx.x, per = WARP ? 32 : blockDim.x;
-  const int rows = WARP ? kWarpRows : 1, row_of = WARP ? threadIdx.x / 32 : 0;
+  const int rows = WARP ? kWarpRows : 1, row_of = WARP ? warp : 0;
   const int col0 = tid * VEC, step = per * VEC;
-  const bool dense = pair_to_sorted == nullptr;
-  const int kk = dense ? 1 : k_max < 32 ? k_max : 32;
-  int q_l = -1;
+  const bool dense = a.pair_to_sorted == nullptr;
+  const int kk = dense ? 1 : a.k_max < 32 ? a.k_max : 32;
+  const T *y_perm = static_cast<const T*>(a.y_perm), *y_shared = static_cast<const T*>(a.y_shared),
+          *residual = static_cast<const T*>(a.residual), *gate_rows = static_cast<const T*>(a.gate);
+  const bool own_gate = a.gate != nullptr && a.gate_rows > 1 && a.gate_bf16 == (sizeof(T) == 2);  // a row of its own, of type T
+  const int first_slot = y_shared != nullptr ? 1 : 0;
+  const uint32_t piece = blockDim.x * 16, base = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  Token* tokens = reinterpret_cast<Token*>(ring + RING * CH * blockDim.x) + warp * RING;
+
+  int q_l = -1;  // slot `lane` of the token after the copies' one
   float w_l = 0.f;
-  auto fetch_slots = [&](long long t) {
+  auto read_slots = [&](long long t) {
     q_l = -1, w_l = 0.f;
     if (t >= T_ || lane >= kk) return;
     if (dense) {
       q_l = (int)t, w_l = 1.f;
     } else {
-      q_l = pair_to_sorted[(size_t)t * k_max + lane];
-      w_l = topk_w[(size_t)t * k_max + lane];
+      q_l = a.pair_to_sorted[(size_t)t * a.k_max + lane];
+      w_l = a.topk_w[(size_t)t * a.k_max + lane];
     }
   };
-  long long t = (long long)blockIdx.x * rows + row_of;
   const long long stride = (long long)gridDim.x * rows;
-  fetch_slots(t);
-  for (; t < T_; t += stride) {
-    if (!dense && q_l >= P) {
+  // the copies' place: a token, its list (kept for the sums, RING of them in turn), the next item of it
+  long long t_c = (long long)blockIdx.x * rows + row_of;
+  int turn_c = 0, next = 0, items = 0, to = 0;
+  auto enter = [&]() {
+    if (!dense && q_l >= a.P) {
       flag(SEMMOE_DEVERR_PAIRS);
       q_l = -1;
     }
-    uint4 res[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      res[c] = residual != nullptr && col < H ? *reinterpret_cast<const uint4*>(residual + (size_t)t * H + col)
-                                              : make_uint4(0, 0, 0, 0);
+    Token& tk = tokens[turn_c];
+    const unsigned live = __ballot_sync(kAll, q_l >= 0);
+    const int n = __popc(live);
+    items = first_slot + n;
+    if (q_l >= 0) {
+      const int j = __popc(live & lanemask_lt());
+      tk.row[first_slot + j] = y_perm + (size_t)q_l * H;
+      tk.weight[j] = w_l;
     }
-    float v[CH][VEC];
+    if (first_slot && lane == 0) tk.row[0] = y_shared + (size_t)t_c * H;
+    if (own_gate) {
+      if (lane == 0) tk.row[items] = gate_rows + (size_t)t_c * H;
+      ++items;
+    }
+    if (residual != nullptr) {
+      if (lane == 0) tk.row[items] = residual + (size_t)t_c * H;
+      ++items;
+    }
+    if (items == 0) {
+      if (lane == 0) tk.row[0] = nullptr;
+      items = 1;
+    }
+    if (lane == 0) tk.items = items, tk.slots = n;
+    next = 0;
+    __syncwarp();
+    read_slots(t_c + stride);
+  };
+  auto copy_next = [&]() {
+    if (next == items && t_c < T_) {
+      t_c += stride;
+      turn_c = (turn_c + 1) % RING;
+      if (t_c < T_) enter();
+    }
+    if (t_c < T_) {
+      const T* src = static_cast<const T*>(tokens[turn_c].row[next++]);
+      if (src != nullptr) {
+        src += col0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      if (y_shared != nullptr && col < H) {
-        V::load(y_shared + (size_t)t * H + col, v[c]);
-      } else {
+        for (int c = 0; c < CH; ++c)
+          if (col0 + c * step < H) cp_async16(base + (to * CH + c) * piece, src + c * step);
+      }
+      to = (to + 1) % RING;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int from = 0;
+  auto next_item = [&]() {  // the ring's place of the next item, once its pieces are there
+    copy_next();
+    asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+    const int at = from;
+    from = (from + 1) % RING;
+    return at;
+  };
+  auto values = [&](int at, int c, float (&v)[VEC]) { V::unpack(ring[(at * CH + c) * blockDim.x + threadIdx.x], v); };
+
+  long long t = t_c;
+  if (t < T_) {
+    read_slots(t);
+    enter();
+  }
+#pragma unroll
+  for (int i = 0; i < RING - 1; ++i) copy_next();
+  for (int turn = 0; t < T_; t += stride, turn = (turn + 1) % RING) {
+    __syncwarp();
+    float v[CH][VEC];
+    if (y_shared != nullptr) {
+      const int at = next_item();
+#pragma unroll
+      for (int c = 0; c < CH; ++c) values(at, c, v[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[c][i] = 0.f;
+    }
+    const Token& tk = tokens[turn];
+    const int n = tk.slots;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float w = tk.weight[j];
+      const int at = next_item();
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float r[VEC];
+        values(at, c, r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(w, r[i], v[c][i]);
       }
     }
-    for (int j0 = 0; j0 < kk; j0 += JB) {
-      uint4 raw[JB][CH];
-      float wj[JB];
-      bool ok[JB];
-#pragma unroll
-      for (int b = 0; b < JB; ++b) {
-        const int q = __shfl_sync(kAll, q_l, (j0 + b) & 31);
-        wj[b] = __shfl_sync(kAll, w_l, (j0 + b) & 31);
-        ok[b] = j0 + b < kk && q >= 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int col = col0 + c * step;
-          raw[b][c] = ok[b] && col < H ? *reinterpret_cast<const uint4*>(y_perm + (size_t)q * H + col) : make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < JB; ++b) {
-        if (!ok[b]) continue;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float r[VEC];
-          V::unpack(raw[b][c], r);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(wj[b], r[i], v[c][i]);
-        }
-      }
-    }
-    for (int j = 32; !dense && j < k_max; ++j) {  // budgets above 32 experts: read the slot directly
-      const int q = pair_to_sorted[(size_t)t * k_max + j];
+    if (tk.row[0] == nullptr) next_item();  // the list's only item, which holds nothing
+    for (int j = 32; !dense && j < a.k_max; ++j) {  // budgets above 32 experts: read the slot directly
+      const int q = a.pair_to_sorted[(size_t)t * a.k_max + j];
       if (q < 0) continue;
-      if (q >= P) {
+      if (q >= a.P) {
         flag(SEMMOE_DEVERR_PAIRS);
         continue;
       }
-      const float w = topk_w[(size_t)t * k_max + j];
+      const float w = a.topk_w[(size_t)t * a.k_max + j];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = col0 + c * step;
@@ -294,41 +381,67 @@ combine_norm_kernel(const T* y_perm, const int32_t* __restrict__ pair_to_sorted,
         }
       }
     }
-    fetch_slots(t + stride);
-    RowStats st{1.f, 0.f, 1.f};
-    if (post.kind != SEMMOE_NORM_NONE) st = row_stats<WARP, CH, VEC>(v, post.kind, H, post.eps, col0, step, red);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      if (col < H) {
-        if (post.kind != SEMMOE_NORM_NONE) apply_norm<VEC>(v[c], st, post.weight, post.bias, post.w_bf16, post.offset, col);
-        if (gate != nullptr) {
+    for (int c = 0; c < CH; ++c) {  // columns past the row's end hold 0
+      if (col0 + c * step >= H) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] = 0.f;
+      }
+    }
+    if (a.post.kind != SEMMOE_NORM_NONE) {
+      const RowStats st = row_stats<WARP, CH, VEC>(v, a.post.kind, H, a.post.eps, col0, step, red);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = col0 + c * step;
+        if (col < H) apply_norm<VEC>(v[c], st, a.post.weight, a.post.bias, a.post.w_bf16, a.post.offset, col);
+      }
+    }
+    if (a.gate != nullptr) {
+      const int at = own_gate ? next_item() : 0;
+      const size_t row = a.gate_rows > 1 ? (size_t)t * H : 0;
+      const void* p = a.gate_bf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.gate) + row)
+                                  : static_cast<const void*>(static_cast<const float*>(a.gate) + row);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = col0 + c * step;
+        if (col < H) {
           float g[VEC];
-          const size_t at = gate_per_row ? (size_t)t * H : 0;
-          load_weights(gate_bf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(gate) + at)
-                                 : static_cast<const void*>(static_cast<const float*>(gate) + at),
-                       gate_bf16, col, g);
+          if (own_gate) values(at, c, g);
+          else load_weights(p, a.gate_bf16, col, g);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) v[c][i] *= g[i];
         }
-        float r[VEC];
-        V::unpack(res[c], r);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[c][i] = residual != nullptr ? fmaf(residual_scale, r[i], block_scale * v[c][i]) : block_scale * v[c][i];
-        V::store(out + (size_t)t * H + col, v[c]);
       }
     }
-    if (next.kind == SEMMOE_NORM_NONE) continue;
-    st = row_stats<WARP, CH, VEC>(v, next.kind, H, next.eps, col0, step, red);
+    const int at = residual != nullptr ? next_item() : 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = col0 + c * step;
       if (col < H) {
-        apply_norm<VEC>(v[c], st, next.weight, next.bias, next.w_bf16, next.offset, col);
-        V::store(next_out + (size_t)t * H + col, v[c]);
+        if (residual != nullptr) {
+          float r[VEC];
+          values(at, c, r);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(a.residual_scale, r[i], a.block_scale * v[c][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[c][i] *= a.block_scale;
+        }
+        V::store(static_cast<T*>(a.out) + (size_t)t * H + col, v[c]);
+      }
+    }
+    if (a.next.kind == SEMMOE_NORM_NONE) continue;
+    const RowStats st = row_stats<WARP, CH, VEC>(v, a.next.kind, H, a.next.eps, col0, step, red);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = col0 + c * step;
+      if (col < H) {
+        apply_norm<VEC>(v[c], st, a.next.weight, a.next.bias, a.next.w_bf16, a.next.offset, col);
+        V::store(static_cast<T*>(a.next_out) + (size_t)t * H + col, v[c]);
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // How the rows are spread: a warp or a CTA of `threads` for each, `pieces` of 16 bytes a thread.
@@ -336,44 +449,46 @@ struct RowPlan {
   bool warp;
   int pieces, threads;
 };
-RowPlan plan(int H, int vec) {
+// Many rows: two pieces a thread, so that reductions and loop are shared by more bytes (with one piece the norm of 16384 x
+// 2048 took 33 us where two take 29, the combine 170 and 135; with four 33 and 141: fewer warps at a time).  Few rows,
+// whose time is one row's: as many threads as there are pieces.
+RowPlan plan(int H, int vec, int T) {
   const int n = ceil_div(H, vec);
-  if (n <= 128) return RowPlan{true, n <= 32 ? 1 : n <= 64 ? 2 : 4, 32 * kWarpRows};
-  const int pieces = n <= 256 ? 1 : n <= 512 ? 2 : 4;
+  if (T >= 4 * sm_count() && n <= 128) return RowPlan{true, n <= 32 ? 1 : n <= 64 ? 2 : 4, 32 * kWarpRows};
+  const int few = n <= 256 ? 1 : n <= 512 ? 2 : 4, pieces = T < 4 * sm_count() || few > PIECES ? few : PIECES;
   return RowPlan{false, pieces, ceil_div(ceil_div(n, pieces), 32) * 32};
 }
 
 // CTAs that are resident at once, for a grid whose CTAs take rows in turn.
-template <typename K>
-cudaError_t resident_grid(K kern, int threads, long long want, unsigned* grid) {
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
-  if (e != cudaSuccess) return e;
-  const long long cap = (long long)(per_sm > 0 ? per_sm : 1) * sm_count();
-  *grid = (unsigned)(want < cap ? want : cap);
-  return cudaSuccess;
+unsigned resident_grid(const RowPlan& p, int T, int per_sm) {
+  const long long want = p.warp ? ceil_div(T, kWarpRows) : T, cap = (long long)per_sm * sm_count();
+  return (unsigned)(want < cap ? want : cap);
+}
+// What registers (as the launch bounds have it) and shared memory let an SM hold.
+int ctas_per_sm(const RowPlan& p, int by_bounds, int bound_threads, int smem) {
+  int n = by_bounds * bound_threads / p.threads;
+  const int by_smem = 233472 / (smem + 1024 + 256), by_threads = 2048 / p.threads;
+  if (n > by_smem) n = by_smem;
+  if (n > by_threads) n = by_threads;
+  return n > 0 ? n : 1;
 }
 
 template <typename T, bool WARP, int CH>
 cudaError_t launch_norm_t(const RowPlan& p, const void* x, int T_, int H, const NormArgs& n, void* out, cudaStream_t s) {
-  auto kern = norm_kernel<T, WARP, CH>;
-  unsigned grid;
-  cudaError_t e = resident_grid(kern, p.threads, WARP ? ceil_div(T_, kWarpRows) : T_, &grid);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(grid), dim3(p.threads), 0, s, 1, true, static_cast<const T*>(x), T_, H, n,
-                       static_cast<T*>(out));
+  const int per_sm = ctas_per_sm(p, norm_ctas<WARP, CH>(), max_threads<WARP, CH>(), 0);
+  return launch_kernel(norm_kernel<T, WARP, CH>, dim3(resident_grid(p, T_, per_sm)), dim3(p.threads), 0, s, 1, true,
+                       static_cast<const T*>(x), T_, H, n, static_cast<T*>(out));
 }
 
 template <typename T, bool WARP, int CH>
-cudaError_t launch_combine_norm_t(const RowPlan& p, const CombineNorm& a, cudaStream_t s) {
+cudaError_t launch_t(const RowPlan& p, const CombineNorm& a, cudaStream_t s) {
   auto kern = combine_norm_kernel<T, WARP, CH>;
-  unsigned grid;
-  cudaError_t e = resident_grid(kern, p.threads, WARP ? ceil_div(a.T, kWarpRows) : a.T, &grid);
+  const int smem = RING * (CH * p.threads * 16 + p.threads / 32 * (int)sizeof(Token));
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = ensure_smem_limit(kern, RING * (CH * max_threads<WARP, CH>() * 16 + max_threads<WARP, CH>() / 32 * (int)sizeof(Token)), smem_set);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(grid), dim3(p.threads), 0, s, 1, true, static_cast<const T*>(a.y_perm),
-                       a.pair_to_sorted, a.topk_w, static_cast<const T*>(a.y_shared), a.T, a.H, a.k_max, a.P, a.post,
-                       a.next, a.gate, a.gate_bf16, a.gate_rows > 1, a.block_scale, static_cast<const T*>(a.residual),
-                       a.residual_scale, static_cast<T*>(a.out), static_cast<T*>(a.next_out));
+  const int per_sm = ctas_per_sm(p, min_ctas<WARP, CH>(), max_threads<WARP, CH>(), smem);
+  return launch_kernel(kern, dim3(resident_grid(p, a.T, per_sm)), dim3(p.threads), (size_t)smem, s, 1, true, a);
 }
 
 template <typename F>
@@ -395,28 +510,27 @@ cudaError_t by_plan(const RowPlan& p, F&& f) {
 
 int norm_take_errors(cudaStream_t s, int* bits) { return take_error_word(g_err, s, bits); }
 
-cudaError_t launch_norm(const void* x, int dtype, int T, int H, const NormArgs& n, void* out, cudaStream_t s) {
-  if (T == 0) return cudaSuccess;
-  const RowPlan p = plan(H, dtype == SEMMOE_BF16 ? 8 : 4);
+cudaError_t launch_combine_norm(const CombineNorm& a, int dtype, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const RowPlan p = plan(a.H, dtype == SEMMOE_BF16 ? 8 : 4, a.T);
   cudaError_t e = by_plan(p, [&](auto warp, auto ch) {
     constexpr bool W = decltype(warp)::value;
     constexpr int C = decltype(ch)::value;
-    return dtype == SEMMOE_BF16 ? launch_norm_t<__nv_bfloat16, W, C>(p, x, T, H, n, out, s)
-                                : launch_norm_t<float, W, C>(p, x, T, H, n, out, s);
+    return dtype == SEMMOE_BF16 ? launch_t<__nv_bfloat16, W, C>(p, a, s) : launch_t<float, W, C>(p, a, s);
   });
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
 }
 
-cudaError_t launch_combine_norm(const CombineNorm& a, int dtype, cudaStream_t s) {
-  if (a.T == 0) return cudaSuccess;
-  const RowPlan p = plan(a.H, dtype == SEMMOE_BF16 ? 8 : 4);
+cudaError_t launch_norm(const void* x, int dtype, int T, int H, const NormArgs& n, void* out, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  const RowPlan p = plan(H, dtype == SEMMOE_BF16 ? 8 : 4, T);
   cudaError_t e = by_plan(p, [&](auto warp, auto ch) {
     constexpr bool W = decltype(warp)::value;
     constexpr int C = decltype(ch)::value;
-    return dtype == SEMMOE_BF16 ? launch_combine_norm_t<__nv_bfloat16, W, C>(p, a, s)
-                                : launch_combine_norm_t<float, W, C>(p, a, s);
+    return dtype == SEMMOE_BF16 ? launch_norm_t<__nv_bfloat16, W, C>(p, x, T, H, n, out, s)
+                                : launch_norm_t<float, W, C>(p, x, T, H, n, out, s);
   });
   if (e != cudaSuccess) return e;
   count_launches(1);

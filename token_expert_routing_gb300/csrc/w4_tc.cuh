@@ -539,15 +539,15 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
           }
         };
         // The issue of an MMA waits for the ones before it, and a look at a barrier takes as long as one or two of
-        // them, so the next k-block's barriers are looked at between this one's MMAs.
-        if (elect_one()) issue(0, BK / UK / 2);
+        // them, so the next k-block's barriers are looked at before this one's last MMAs.
+        if (elect_one()) issue(0, BK / UK - 1);
         __syncwarp();
         const uint32_t done = it++ % DONES;
         if (++s == XD) s = 0, s_phase ^= 1;
         if (++a == AD) a = 0, a_phase ^= 1;
         const bool next_x = mbar_test(&sh.xfull[s], s_phase), next_a = mbar_test(&sh.afull[a], a_phase);
         if (elect_one()) {
-          issue(BK / UK / 2, BK / UK);
+          issue(BK / UK - 1, BK / UK);
           commit(&sh.done[done]);
           if (kb == kb_n - 1) {
             commit(&sh.tfull[half % ACCS]);
