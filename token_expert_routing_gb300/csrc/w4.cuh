@@ -25,14 +25,8 @@ __device__ __forceinline__ float load_scale(const __nv_bfloat16* p) {
 }
 
 // Two codes of a word (bits sh.. and sh + 16..) as bf16 values 128 + code: the
-// codes are the low bits of the mantissa.  Taking 128 + z off is exact.
+// codes are the low bits of the mantissa.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int sh) { return ((w >> sh) & 0x000f000fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return 0x43004300u | (z & 15u) | ((z & 15u) << 16); }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 
 }  // namespace w4
 }  // namespace semmoe

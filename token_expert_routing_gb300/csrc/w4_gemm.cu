@@ -3,19 +3,21 @@
 //   plain:  out = x W_e^T
 //   SwiGLU: h = silu(x W1_e^T) * (x W3_e^T)      (both stored in bf16)
 //
-// Few rows per expert (w4_rows_kernel): the weights' bytes bound it, and a
-// tensor-core tile of 128 rows would be all but empty, so the weights are the left operand
-// of the warp-level m16n8k16 product and the rows its narrow side.
-// A unit is NB = 8 NT rows of one group times 32 WM weight rows (SwiGLU: 16 WM gate rows
-// and the same up rows); a CTA of four warps takes units in turn, WM warps
-// along the weight rows, WK along the columns (summed through shared memory at
-// the unit's end).  Codes and rows come in stages of 128 WK columns by asynchronous
-// copies, STAGES - 1 of them in flight, across the ends of units.
+// Few rows per expert (w4_rows_kernel): the weights' bytes bound it, and so few 128-row weight tiles
+// would not fill the SMs, so the weights are the left operand of the warp-level m16n8k16 product
+// and the rows its narrow side.
+// A unit is 8 rows of one group times 32 weight rows (SwiGLU: 16 gate rows and the same up
+// rows); a CTA of four warps takes units in turn, the warps side by side along the columns
+// (summed through shared memory at the unit's end).  Codes and rows come in stages of 512
+// columns by asynchronous copies, STAGES - 1 of them in flight, across the ends of units.
 // A lane's word of eight codes gives the A operands of two products as they lie: bits 0-3
 // and 16-19 (columns 0, 4), 4-7 and 20-23 (1, 5), and so on; the row's eight values are
-// put into that order instead.  The codes are exact in bf16 (128 + code, less 128 + z), a
-// group's products are summed alone and multiplied by its scale in fp32, so no weight is
-// rounded.
+// put into that order instead.  A code enters as 128 + code, one masked OR, and the sums of a group of
+// columns are put right at its end: s (sum (128 + code) x - (128 + z) sum x), with sum x from one more product,
+// whose weights are ones.  The instructions a weight are what is left to save here: with 128 + z taken off
+// every pair of codes, and the scales' places computed stage by stage, one token through 8 of 128 experts took 20 us.
+// No weight is rounded: codes, zero points and the rows' values are exact in bf16, the sums fp32.
+// Measured (GB300): ROWSTIMES.
 #include "common.cuh"
 #include "internal.h"
 #include "w4_groups.cuh"
@@ -28,11 +30,18 @@ using namespace w4;
 __device__ int g_err;
 
 constexpr int THREADS = 128;
-constexpr int STAGES = 4;
+constexpr int WK = 4;                 // warps, side by side along the columns
+constexpr int STAGES = 3;
 constexpr int CHUNK = 128;            // columns of a warp's stage
-constexpr int W_STAGE = 8192;         // bytes of codes a stage: 32 rows x 64 bytes x 4 warps
-constexpr int X_STAGE = 8192;         // bytes of rows a stage: 8 NT x 256 bytes x WK
+constexpr int BK = CHUNK * WK;
+constexpr int NB = 8;                 // rows of a unit
+constexpr int MT = 2;                 // 16-row tiles of weight rows
+constexpr int W_STAGE = 32 * BK / 2;  // bytes of codes a stage
+constexpr int X_STAGE = NB * BK * 2;  // bytes of rows a stage
 constexpr int STAGE_BYTES = W_STAGE + X_STAGE;
+constexpr int RED = 36;               // floats of a row of the sums (conflict-free over a warp)
+constexpr int SMEM = STAGES * STAGE_BYTES + WK * NB * RED * 4;
+constexpr int PER_SM = 4;             // CTAs that an SM holds
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   const int n = live ? 16 : 0;  // nothing read, zeros written
@@ -60,128 +69,184 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+// BYTES (2, 4, 8 or 16) that lie together, aligned to their size.
+template <int BYTES>
+__device__ __forceinline__ void load_raw(const void* p, uint32_t* r) {
+  if (BYTES == 2) r[0] = __ldg(static_cast<const unsigned short*>(p));
+  if (BYTES == 4) r[0] = __ldg(static_cast<const uint32_t*>(p));
+  if (BYTES == 8) {
+    const uint2 v = __ldg(static_cast<const uint2*>(p));
+    r[0] = v.x, r[BYTES / 4 - 1] = v.y;
+  }
+  if (BYTES == 16) {
+    const uint4 v = __ldg(static_cast<const uint4*>(p));
+    r[0] = v.x, r[BYTES / 4 - 3 > 0 ? 1 : 0] = v.y, r[BYTES / 4 - 2 > 0 ? 2 : 0] = v.z, r[BYTES / 4 - 1] = v.w;
+  }
+}
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // GS: groups of scales in a chunk of 128 columns (4, 2, or 1 for groups of 128 and more).
-template <int NT, int WM, bool GLU, typename S, int GS>
-__global__ void __launch_bounds__(THREADS, 3)
-w4_rows_kernel(Product pr) {
-  constexpr int WK = 4 / WM, NB = 8 * NT, BK = CHUNK * WK;
-  constexpr int MT = 2;                              // 16-row tiles of a warp
-  constexpr int COLS = (GLU ? 16 : 32) * WM;         // output columns of a unit
-  constexpr int RED = 32 * WM + 4;                   // floats per row of the sums (conflict-free over t)
-  static_assert(NB * 256 * WK == X_STAGE, "a stage of rows");
+template <bool GLU, typename S, int GS>
+__global__ void __launch_bounds__(THREADS, PER_SM)
+w4_rows_kernel(const __grid_constant__ Product pr) {
+  constexpr int COLS = GLU ? 16 : 32;                // output columns of a unit
   extern __shared__ __align__(128) unsigned char smem[];
   float* red = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);  // [WK][NB][RED]
   __shared__ Groups sh;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const int wm = warp % WM, wk = warp / WM;
+  const int tid = threadIdx.x, wk = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  if (!pr.early) pdl_wait();
   pdl_trigger();
-  pdl_wait();
-  if (warp == 0) load_groups(sh, pr, NB, lane, &g_err);
+  if (wk == 0) load_groups(sh, pr, NB, lane, &g_err);
   __syncthreads();
   const int G = pr.E, K = pr.K, KG = K / pr.group, ki = (K + BK - 1) / BK;
   const int rows_w = GLU ? 2 * pr.N : pr.N;          // weight rows of an expert
   const int total = sh.total * pr.n_tiles;
-  // row r of the unit's weight rows (of warp block r / 32) among the expert's
+  // row r of the unit's weight rows among the expert's
   auto weight_row = [&](int nt, int r) {
-    if (GLU) {
-      const int c = nt * COLS + (r / 32) * 16 + r % 16;
-      return (c < pr.N ? c : pr.N - 1) + (r % 32 >= 16 ? pr.N : 0);
-    }
-    const int c = nt * COLS + r;
-    return c < pr.N ? c : pr.N - 1;
+    const int c = nt * COLS + (GLU ? r % 16 : r);
+    return (c < pr.N ? c : pr.N - 1) + (GLU && r >= 16 ? pr.N : 0);
   };
 
   // ---- copies: this thread's 16-byte pieces of a stage, the same columns in four rows ----
-  constexpr int WP = 4 * WK, XP = 16 * WK;           // pieces of a row
-  constexpr int XN = X_STAGE / 16 / THREADS;
+  constexpr int WP = 4 * WK, XP = 16 * WK;           // pieces of a row of codes, of a row
+  constexpr int WN = W_STAGE / 16 / THREADS, XN = X_STAGE / 16 / THREADS;
   const int w_seg = tid % WP, x_seg = tid % XP;
   const uint32_t base = smem_addr(smem);
-  int lu = blockIdx.x, lg = 0, ug = 0;               // the unit being copied, its group ...
-  int lkb = 0;                                       // ... and its k-block
-  const uint8_t* wsrc[4];
-  const __nv_bfloat16* xsrc[XN];
-  auto copy_rows = [&]() {
-    const Unit un = decode_unit(sh, G, lg, pr.n_tiles, NB, lu);
+  uint32_t w_to[WN], x_to[XN];                       // places in a stage
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < WN; ++i) {
+    const int r = tid / WP + i * (THREADS / WP);
+    w_to[i] = base + (w_seg / 4) * 2048 + r * 64 + (((w_seg & 3) ^ ((r >> 1) & 3)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < XN; ++i) {
+    const int n = tid / XP + i * (THREADS / XP);
+    x_to[i] = base + W_STAGE + (x_seg / 16) * (NB * 256) + n * 256 + (((x_seg & 15) ^ ((n & 1) << 2)) << 4);
+  }
+  int lu = blockIdx.x;                               // the unit being copied ...
+  int lkb = 0;                                       // ... and its k-block
+  int lrows = 0;                                     // its rows: places of rows past them keep what they hold, no sum of
+  const uint8_t* wsrc[WN];                           // which is stored (and a row read for all eight is one L2 line for
+  const __nv_bfloat16* xsrc[XN];                     // every CTA)
+  auto copy_rows = [&](const Unit& un) {
+#pragma unroll
+    for (int i = 0; i < WN; ++i)
       wsrc[i] = pr.w.codes + ((size_t)un.e * rows_w + weight_row(un.nt, tid / WP + i * (THREADS / WP))) * (K / 2) + w_seg * 16;
 #pragma unroll
     for (int i = 0; i < XN; ++i) {
       const int n = tid / XP + i * (THREADS / XP);
-      xsrc[i] = pr.x + (size_t)(un.row0 + (n < un.rows ? n : un.rows - 1)) * K + x_seg * 8;
+      xsrc[i] = pr.x + (size_t)(un.row0 + (n < un.rows ? n : 0)) * K + x_seg * 8;
     }
+    lrows = un.rows;
   };
-  auto copy_stage = [&](int s) {
-    if (lu < total) {
-      const uint32_t ws = base + s * STAGE_BYTES, xs = ws + W_STAGE;
-      const int k0 = lkb * BK;
-      const bool w_live = k0 + w_seg * 32 < K, x_live = k0 + x_seg * 8 < K;
+  auto copy_codes = [&](int s, int kb) {
+    const bool live = kb * BK + w_seg * 32 < K;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = tid / WP + i * (THREADS / WP), b = r / 32, q = r % 32;
-        cp_async16(ws + (b * WK + w_seg / 4) * 2048 + q * 64 + (((w_seg & 3) ^ ((q >> 1) & 3)) << 4),
-                   w_live ? wsrc[i] + k0 / 2 : pr.w.codes, w_live);
-      }
+    for (int i = 0; i < WN; ++i)
+      cp_async16(w_to[i] + s * STAGE_BYTES, live ? wsrc[i] + kb * (BK / 2) : pr.w.codes, live);
+  };
+  auto copy_stage = [&](int s, bool codes = true) {
+    if (lu < total) {
+      if (codes) copy_codes(s, lkb);
+      const bool x_live = lkb * BK + x_seg * 8 < K;
 #pragma unroll
       for (int i = 0; i < XN; ++i) {
-        const int n = tid / XP + i * (THREADS / XP);
-        cp_async16(xs + (x_seg / 16) * (NB * 256) + n * 256 + (((x_seg & 15) ^ ((n & 1) << 2)) << 4),
-                   x_live ? (const void*)(xsrc[i] + k0) : (const void*)pr.x, x_live);
+        if (tid / XP + i * (THREADS / XP) < lrows)
+          cp_async16(x_to[i] + s * STAGE_BYTES, x_live ? (const void*)(xsrc[i] + lkb * BK) : (const void*)pr.x, x_live);
       }
       if (++lkb == ki) {
         lkb = 0;
         lu += gridDim.x;
-        if (lu < total) copy_rows();
+        if (lu < total) copy_rows(decode_unit(sh, G, pr.n_tiles, NB, lu));
       }
     }
     cp_async_commit();
   };
 
   // ---- scales and zero points of this lane's rows in a chunk ----
-  float sc[MT][2][GS];
-  uint32_t zp[MT][2][GS];
+  const bool whole = GS == 1 || K % CHUNK == 0;      // a chunk's scales are aligned to their size
+  const int per = pr.group > CHUNK ? pr.group / CHUNK : 1;  // chunks of a scale
   size_t srow[MT][2];
   auto scale_rows = [&](const Unit& un) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        srow[m][h] = ((size_t)un.e * rows_w + weight_row(un.nt, wm * 32 + m * 16 + h * 8 + g)) * KG;
+        srow[m][h] = ((size_t)un.e * rows_w + weight_row(un.nt, m * 16 + h * 8 + g)) * KG;
   };
-  auto load_scales = [&](int kb, float (&s)[MT][2][GS], uint32_t (&z)[MT][2][GS]) {
-    const int k = kb * BK + wk * CHUNK;
+  // as they lie in memory; unpacked where they are used, so that nothing waits for them before
+  constexpr int NR = GS * (int)sizeof(S) <= 4 ? 1 : GS * (int)sizeof(S) / 4;
+  struct Scales {
+    uint32_t s[MT][2][NR], z[MT][2];
+  };
+  auto load_scales = [&](int kb, Scales& r) {
+    const int ch = kb * WK + wk;
+    int i0 = GS > 1 ? ch * GS : per > 1 ? ch / per : ch;
+    if (i0 + GS > KG && (whole || i0 >= KG)) i0 = KG - GS;  // a chunk past K: codes and rows are 0
 #pragma unroll
-    for (int j = 0; j < GS; ++j) {
-      int i = (k + j * (CHUNK / GS)) / pr.group;
-      if (i >= KG) i = KG - 1;  // past K: codes and rows are 0
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h) {
+        const S* p = static_cast<const S*>(pr.w.scales) + srow[m][h] + i0;
+        const uint8_t* q = pr.w.zeros + srow[m][h] + i0;
+        r.z[m][h] = 0x08080808u;
+        if (whole) {
+          load_raw<GS * (int)sizeof(S)>(p, r.s[m][h]);
+          if (pr.w.zeros != nullptr) {
+            if (GS == 1) r.z[m][h] = __ldg(q);
+            if (GS == 2) r.z[m][h] = __ldg(reinterpret_cast<const unsigned short*>(q));
+            if (GS == 4) r.z[m][h] = __ldg(reinterpret_cast<const uint32_t*>(q));
+          }
+        } else {  // one by one; past K the last one again
+          uint32_t v[GS], z = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[m][h][j] = load_scale(static_cast<const S*>(pr.w.scales) + srow[m][h] + i);
-          z[m][h][j] = pr.w.zeros != nullptr ? __ldg(pr.w.zeros + srow[m][h] + i) : 8u;
+          for (int j = 0; j < GS; ++j) {
+            const int o = i0 + j < KG ? j : KG - 1 - i0;
+            v[j] = sizeof(S) == 4 ? __ldg(reinterpret_cast<const uint32_t*>(p) + o)
+                                  : __ldg(reinterpret_cast<const unsigned short*>(p) + o);
+            z |= (pr.w.zeros != nullptr ? (uint32_t)__ldg(q + o) : 8u) << (8 * j);
+          }
+          r.z[m][h] = z;
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+            r.s[m][h][j] = sizeof(S) == 4 ? v[j] : v[2 * j % GS] | (GS > 1 ? v[(2 * j + 1) % GS] << 16 : 0u);
         }
-    }
+      }
   };
+  auto scale_of = [&](const Scales& r, int m, int h, int j) {
+    if (sizeof(S) == 4) return __uint_as_float(r.s[m][h][j % NR]);
+    return __uint_as_float(j & 1 ? r.s[m][h][j / 2 % NR] & 0xffff0000u : r.s[m][h][j / 2 % NR] << 16);
+  };
+  auto zero_of = [&](const Scales& r, int m, int h, int j) { return 128.0f + (float)((r.z[m][h] >> (8 * j)) & 15u); };
 
   int u = blockIdx.x;
-  if (u >= total) return;
-  copy_rows();
+  if (u >= total) {
+    if (pr.early) pdl_wait();  // a kernel ends after the one before it
+    return;
+  }
+  Unit un = decode_unit(sh, G, pr.n_tiles, NB, u);
+  copy_rows(un);
+  if (pr.early) {
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) copy_stage(s);
-  Unit un = decode_unit(sh, G, ug, pr.n_tiles, NB, u);
+    for (int s = 0; s < STAGES - 1; ++s)
+      if (s < ki) copy_codes(s, s);
+  }
+  Scales sc;
   scale_rows(un);
-  load_scales(0, sc, zp);
-  float acc[MT][NT][4];
+  load_scales(0, sc);
+  if (pr.early) pdl_wait();
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) copy_stage(s, !pr.early || s >= ki);
+  float acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
 
+  // this lane's places in a stage: ldmatrix rows, its row's values
+  const int mr = (lane & 7) + ((lane >> 3) & 1) * 8;
+  const uint32_t w_at = base + wk * 2048 + mr * 64, w_turn = ((mr >> 1) & 3) << 4, seg0 = (lane >> 4) << 4;
+  const uint32_t x_at = base + W_STAGE + wk * (NB * 256) + g * 256 + (t << 4), x_turn = (g & 1) << 6;
   int stage = 0, kb = 0;
   while (true) {
     cp_async_wait<STAGES - 2>();
@@ -190,58 +255,43 @@ w4_rows_kernel(Product pr) {
     // the next stage's scales, one stage ahead
     const bool last = kb == ki - 1;
     Unit nx = un;
-    float nsc[MT][2][GS];
-    uint32_t nzp[MT][2][GS];
+    Scales nsc;
     const bool more = !last || u + (int)gridDim.x < total;
     if (last && more) {
-      nx = decode_unit(sh, G, ug, pr.n_tiles, NB, u + gridDim.x);
+      nx = decode_unit(sh, G, pr.n_tiles, NB, u + gridDim.x);
       scale_rows(nx);
     }
-    load_scales(last ? 0 : kb + 1, nsc, nzp);  // (of this unit again where there is none: not used)
+    if (more) load_scales(last ? 0 : kb + 1, nsc);
 
-    const uint32_t ws = base + stage * STAGE_BYTES + (wm * WK + wk) * 2048;
-    const uint32_t xs = base + stage * STAGE_BYTES + W_STAGE + wk * (NB * 256);
+    const uint32_t off = stage * STAGE_BYTES;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    float part[MT][NT][4];
+    float part[MT][4], xsum[4];
 #pragma unroll
     for (int jp = 0; jp < 2; ++jp) {
       uint32_t w[MT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int r = m * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, seg = 2 * jp + (lane >> 4);
-        ldmatrix_x4(w[m], ws + r * 64 + ((seg ^ ((r >> 1) & 3)) << 4));
-      }
+      for (int m = 0; m < MT; ++m) ldmatrix_x4(w[m], w_at + off + m * 1024 + ((32 * jp + seg0) ^ w_turn));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int j = 2 * jp + h, gi = j * GS / 4;            // 32 columns, their group
         const bool first = j % (4 / GS) == 0, end = (j + 1) % (4 / GS) == 0;
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 v = lds128(xs + (n * 8 + g) * 256 + (((4 * j + t) ^ ((g & 1) << 2)) << 4));
-          b[n][0] = __byte_perm(v.x, v.z, 0x5410);
-          b[n][1] = __byte_perm(v.x, v.z, 0x7632);
-          b[n][2] = __byte_perm(v.y, v.w, 0x5410);
-          b[n][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
+        const uint4 v = lds128(x_at + off + ((64 * j) ^ x_turn));
+        const uint32_t b[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632)};
+        constexpr uint32_t one = 0x3f803f80u;
+        if (first) mma(xsum, one, one, one, one, b[0], b[1], zero);
+        else mma(xsum, one, one, one, one, b[0], b[1], xsum);
+        mma(xsum, one, one, one, one, b[2], b[3], xsum);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const uint32_t lo = w[m][2 * h], hi = w[m][2 * h + 1], z0 = zero_pair(zp[m][0][gi]), z1 = zero_pair(zp[m][1][gi]);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint32_t a0 = sub_bf16x2(code_pair(lo, 8 * p), z0), a1 = sub_bf16x2(code_pair(hi, 8 * p), z1),
-                           a2 = sub_bf16x2(code_pair(lo, 8 * p + 4), z0), a3 = sub_bf16x2(code_pair(hi, 8 * p + 4), z1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (first && p == 0) mma(part[m][n], a0, a1, a2, a3, b[n][0], b[n][1], zero);
-              else mma(part[m][n], a0, a1, a2, a3, b[n][2 * p], b[n][2 * p + 1], part[m][n]);
-            }
-          }
+          const uint32_t lo = w[m][2 * h], hi = w[m][2 * h + 1];
+          if (first) mma(part[m], code_pair(lo, 0), code_pair(hi, 0), code_pair(lo, 4), code_pair(hi, 4), b[0], b[1], zero);
+          else mma(part[m], code_pair(lo, 0), code_pair(hi, 0), code_pair(lo, 4), code_pair(hi, 4), b[0], b[1], part[m]);
+          mma(part[m], code_pair(lo, 8), code_pair(hi, 8), code_pair(lo, 12), code_pair(hi, 12), b[2], b[3], part[m]);
           if (end) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(sc[m][i / 2][gi], part[m][n][i], acc[m][n][i]);
+            for (int i = 0; i < 4; ++i)
+              acc[m][i] = fmaf(scale_of(sc, m, i / 2, gi), fmaf(-zero_of(sc, m, i / 2, gi), xsum[i], part[m][i]), acc[m][i]);
           }
         }
       }
@@ -250,25 +300,20 @@ w4_rows_kernel(Product pr) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            red[(wk * NB + n * 8 + 2 * t + (i & 1)) * RED + wm * 32 + m * 16 + (i / 2) * 8 + g] = acc[m][n][i];
-            acc[m][n][i] = 0.f;
-          }
+        for (int i = 0; i < 4; ++i) {
+          red[(wk * NB + 2 * t + (i & 1)) * RED + m * 16 + (i / 2) * 8 + g] = acc[m][i];
+          acc[m][i] = 0.f;
+        }
       __syncthreads();
-      const int n0 = un.nt * COLS;
-      for (int i = tid; i < NB * COLS / 2; i += THREADS) {
-        const int n = i / (COLS / 2), c = 2 * (i % (COLS / 2));
-        if (n >= un.rows || n0 + c >= pr.N) continue;
-        const int r = GLU ? (c / 16) * 32 + c % 16 : c;
+      const int n0 = un.nt * COLS, n = tid / (COLS / 2), c = 2 * (tid % (COLS / 2));  // a pair of columns a thread
+      if (n < un.rows && n0 + c < pr.N) {
         float v[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < WK; ++k)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            v[j] += red[(k * NB + n) * RED + r + j];
-            if (GLU) up[j] += red[(k * NB + n) * RED + r + 16 + j];
+            v[j] += red[(k * NB + n) * RED + c + j];
+            if (GLU) up[j] += red[(k * NB + n) * RED + 16 + c + j];
           }
         if (GLU) v[0] = swiglu(v[0], up[0]), v[1] = swiglu(v[1], up[1]);
         *reinterpret_cast<__nv_bfloat162*>(pr.out + (size_t)(un.row0 + n) * pr.N + n0 + c) = __floats2bfloat162_rn(v[0], v[1]);
@@ -280,47 +325,41 @@ w4_rows_kernel(Product pr) {
     } else {
       ++kb;
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < GS; ++j) sc[m][h][j] = nsc[m][h][j], zp[m][h][j] = nzp[m][h][j];
+    sc = nsc;
     stage = (stage + 1) % STAGES;
   }
   cp_async_wait<0>();
 }
 
-template <int NT, int WM, bool GLU, typename S, int GS>
-cudaError_t launch_rows_t(Product pr, cudaStream_t s) {
-  constexpr int cols = (GLU ? 16 : 32) * WM, smem = STAGES * STAGE_BYTES + (4 / WM) * 8 * NT * (32 * WM + 4) * 4;
-  auto kern = w4_rows_kernel<NT, WM, GLU, S, GS>;
+template <bool GLU, typename S, int GS>
+cudaError_t launch_rows(Product pr, cudaStream_t s) {
+  constexpr int COLS = GLU ? 16 : 32;
+  static_assert(PER_SM * (SMEM + (int)sizeof(Groups) + 1024) <= 233472, "shared memory of an SM");
+  auto kern = w4_rows_kernel<GLU, S, GS>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = ensure_smem_limit(kern, smem, smem_set);
+  cudaError_t e = ensure_smem_limit(kern, SMEM, smem_set);
   if (e != cudaSuccess) return e;
-  pr.n_tiles = (pr.N + cols - 1) / cols;
-  const long long units = ((long long)pr.P / (8 * NT) + (pr.E < pr.P ? pr.E : pr.P)) * pr.n_tiles;
-  constexpr int per_sm = 232448 / (smem + (int)sizeof(Groups) + 1024);  // CTAs that an SM's shared memory holds
-  const long long cap = (per_sm < 3 ? per_sm : 3) * (long long)sm_count();
-  e = launch_kernel(kern, dim3((unsigned)(units < cap ? units : cap)), dim3(THREADS), smem, s, 1, true, pr);
+  pr.n_tiles = (pr.N + COLS - 1) / COLS;
+  const long long units = ((long long)pr.P / NB + (pr.E < pr.P ? pr.E : pr.P)) * pr.n_tiles, cap = PER_SM * (long long)sm_count();
+  e = launch_kernel(kern, dim3((unsigned)(units < cap ? units : cap)), dim3(THREADS), SMEM, s, 1, true, pr);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
 template <bool GLU>
 cudaError_t launch_product(const Product& pr, cudaStream_t s) {
-  // a few rows whose 128-row weight tiles would not fill the SMs
+  // a few rows whose 128-row weight tiles would not fill the SMs: RULETIMES
   const int used = pr.E < pr.P ? pr.E : pr.P;
-  if (pr.P > 8LL * used || (long long)used * ((pr.N + 127) / 128) >= sm_count())
+  if (pr.P > (long long)NB * used || (long long)used * ((pr.N + 127) / 128) >= sm_count())
     return GLU ? launch_w4_tc_glu(pr, s) : launch_w4_tc_plain(pr, s);
   if (pr.w.scales_bf16) {
-    if (pr.group == 32) return launch_rows_t<1, 1, GLU, __nv_bfloat16, 4>(pr, s);
-    if (pr.group == 64) return launch_rows_t<1, 1, GLU, __nv_bfloat16, 2>(pr, s);
-    return launch_rows_t<1, 1, GLU, __nv_bfloat16, 1>(pr, s);
+    if (pr.group == 32) return launch_rows<GLU, __nv_bfloat16, 4>(pr, s);
+    if (pr.group == 64) return launch_rows<GLU, __nv_bfloat16, 2>(pr, s);
+    return launch_rows<GLU, __nv_bfloat16, 1>(pr, s);
   }
-  if (pr.group == 32) return launch_rows_t<1, 1, GLU, float, 4>(pr, s);
-  if (pr.group == 64) return launch_rows_t<1, 1, GLU, float, 2>(pr, s);
-  return launch_rows_t<1, 1, GLU, float, 1>(pr, s);
+  if (pr.group == 32) return launch_rows<GLU, float, 4>(pr, s);
+  if (pr.group == 64) return launch_rows<GLU, float, 2>(pr, s);
+  return launch_rows<GLU, float, 1>(pr, s);
 }
 
 }  // namespace
@@ -332,7 +371,7 @@ size_t w4_ffn_ws_bytes(int P, int I) { return align_up((size_t)(P > 0 ? P : 1) *
 cudaError_t launch_w4_grouped_gemm(const void* x, const int32_t* offsets, const int32_t* experts, const Weights& w, int P,
                                    int E, int N, int K, int group, void* out, cudaStream_t s) {
   return launch_product<false>(Product{static_cast<const __nv_bfloat16*>(x), offsets, experts, w, P, E, N, K, group, 0,
-                                       static_cast<__nv_bfloat16*>(out)},
+                                       false, static_cast<__nv_bfloat16*>(out)},
                                s);
 }
 
@@ -341,10 +380,10 @@ cudaError_t launch_w4_grouped_ffn(const void* x, const int32_t* offsets, const i
                                   cudaStream_t s) {
   __nv_bfloat16* h = static_cast<__nv_bfloat16*>(ws);
   cudaError_t e = launch_product<true>(Product{static_cast<const __nv_bfloat16*>(x), offsets, experts, w13, P, E, I, H,
-                                               group, 0, h},
+                                               group, 0, false, h},
                                        s);
   if (e != cudaSuccess) return e;
-  return launch_product<false>(Product{h, offsets, experts, w2, P, E, H, I, group, 0, static_cast<__nv_bfloat16*>(y)}, s);
+  return launch_product<false>(Product{h, offsets, experts, w2, P, E, H, I, group, 0, true, static_cast<__nv_bfloat16*>(y)}, s);
 }
 
 }  // namespace semmoe

@@ -16,6 +16,9 @@ struct Product {
   const int32_t* experts;
   Weights w;
   int P, E, N, K, group, n_tiles;
+  // launched as the dependent of a kernel of these files, which triggers after its own wait (so that everything before it is
+  // complete): tables and weights are read before this kernel's wait, only x is its output
+  bool early;
   __nv_bfloat16* out;
 };
 
@@ -29,15 +32,17 @@ struct Groups {
 // One warp: the tables and the exclusive prefix of the groups' blocks of at most `block` rows, 8 groups per lane.
 __device__ inline void load_groups(Groups& sh, const Product& pr, int block, int lane, int* err) {
   const int G = pr.E;
-  int off[9], cnt[8], sum = 0;
+  int off[9], ex[8], cnt[8], sum = 0;
 #pragma unroll
   for (int i = 0; i < 9; ++i) off[i] = lane * 8 + i <= G ? pr.offsets[lane * 8 + i] : 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ex[i] = lane * 8 + i < G ? pr.experts[lane * 8 + i] : 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int g = lane * 8 + i;
     int c = 0;
     if (g < G) {
-      const int lo = off[i], hi = off[i + 1], e = pr.experts[g];
+      const int lo = off[i], hi = off[i + 1], e = ex[i];
       sh.off[g] = lo;
       sh.pe[g] = e;
       if (g == G - 1) sh.off[G] = hi;
@@ -70,26 +75,18 @@ __device__ inline void load_groups(Groups& sh, const Product& pr, int block, int
   }
 }
 
-// Unit u of the (group, weight tile, block of rows) list, blocks innermost: rows
-// [row0, row0 + rows) with expert e, weight tile nt.  round > 0: a group's blocks
-// are of one size, rounded up to that many rows (at most `block`).  Units come in
-// increasing order, so a role keeps the group `g` it is at: the next unit is a few
-// groups on where groups are long, and anywhere after it where they are empty.
+// A whole warp: unit u of the (group, weight tile, block of rows) list, blocks innermost:
+// rows [row0, row0 + rows) with expert e, weight tile nt.  round > 0: a group's blocks are
+// of one size, rounded up to that many rows (at most `block`).
 struct Unit {
   int row0, rows, e, nt;
 };
-__device__ __forceinline__ Unit decode_unit(const Groups& sh, int G, int& g, int n_tiles, int block, int u, int round = 0) {
-  const int at = u / n_tiles;  // tp[g] * n_tiles <= u < tp[g + 1] * n_tiles, as tp[g] <= at < tp[g + 1]
-  int steps = 4;
-  while (sh.tp[g + 1] <= at && --steps) ++g;
-  if (steps == 0) {
-    int hi = G - 1;
-    while (g < hi) {
-      const int mid = (g + hi) >> 1;
-      if (sh.tp[mid + 1] > at) hi = mid;
-      else g = mid + 1;
-    }
-  }
+__device__ __forceinline__ Unit decode_unit(const Groups& sh, int G, int n_tiles, int block, int u, int round = 0) {
+  const int at = u / n_tiles, lane = threadIdx.x % 32;
+  // the group: the last g with tp[g] <= at, looked for in steps of eight, then among eight
+  const int eights = 31 - __clz(__ballot_sync(0xffffffffu, lane * 8 < G && sh.tp[lane * 8 < G ? lane * 8 : 0] <= at));
+  const int mine = eights * 8 + (lane & 7);
+  const int g = eights * 8 + 31 - __clz(__ballot_sync(0xffffffffu, lane < 8 && mine < G && sh.tp[mine < G ? mine : 0] <= at));
   const int v = u - sh.tp[g] * n_tiles, blocks = sh.tp[g + 1] - sh.tp[g];
   int nt = v, b = 0, rows = sh.off[g + 1] - sh.off[g];
   if (blocks > 1) {

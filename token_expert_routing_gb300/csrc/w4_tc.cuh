@@ -246,7 +246,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     prefetch_map(&map_x);
   }
   if (warp == MMA_WARP) tmem_alloc(&sh.tmem_base, TMEM_COLS);
-  pdl_wait();
+  if (!pr.early) pdl_wait();
   pdl_trigger();
   if (warp == 0) load_groups(sh.groups, pr, ROWS, lane, &g_err);
   fence_before();
@@ -257,8 +257,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
   const int G = pr.E, n_tiles = pr.n_tiles, K = pr.K, units = gridDim.x;
   const int total = __shfl_sync(0xffffffffu, sh.groups.total, 0) * n_tiles;
   const int kb_n = (K + BK - 1) / BK, ch_n = (K + CHUNK - 1) / CHUNK;
-  int group = 0;  // of this role's unit
-  auto unit_at = [&](int u) { return decode_unit(sh.groups, G, group, n_tiles, ROWS, u, ROUND); };
+  auto unit_at = [&](int u) { return decode_unit(sh.groups, G, n_tiles, ROWS, u, ROUND); };
 
   if (warp < SH::EXP) {
     // ---------------- codes to bf16 weights in TMEM ----------------
@@ -485,6 +484,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     if (lane == 0) *reinterpret_cast<volatile int*>(&sh.c_armed) = (int)j;
   } else if (warp == X_WARP) {
     // ---------------- producer of token rows ----------------
+    if (pr.early) pdl_wait();  // (also by a CTA without units: a kernel ends after the one before it)
     uint32_t it = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < total; u += units) {
