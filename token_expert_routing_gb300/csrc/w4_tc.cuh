@@ -98,14 +98,34 @@ struct Shared {
   Groups groups;
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]^T.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// A k-block's places in the rings of token rows and A blocks, and the phases of their barriers.
+struct Turn {
+  uint32_t s, s_phase, a, a_phase;
+  __device__ __forceinline__ void step(uint32_t stages, uint32_t blocks) {
+    if (++s == stages) s = 0, s_phase ^= 1;
+    if (++a == blocks) a = 0, a_phase ^= 1;
+  }
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]^T.  b: the low word of B's descriptor, which holds its address; the high word is that of
+// every K-major tile with 128-byte swizzle (sw128_desc).  Few instructions an MMA: with few columns they take longer than it.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate = 1) {
+  if (ACCUMULATE)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 d;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\tmov.b64 d, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], d, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "n"(kDescHigh)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 d;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tmov.b64 d, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], d, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "n"(kDescHigh), "r"(accumulate)
+        : "memory");
 }
 
 // 32 columns of this warp's 32 TMEM lanes.
@@ -507,9 +527,10 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     if (lane == 0) *reinterpret_cast<volatile int*>(&sh.x_armed) = (int)it;
   } else {
     // ---------------- MMA issuer ----------------
-    uint32_t it = 0, half = 0, s = 0, s_phase = 0, a = 0, a_phase = 0;  // k-block, half tile; places and phases
-    bool ok = true, ready = false;  // ready: this k-block's operands have been seen
-    const uint64_t desc_x = sw128_desc(smem_u32(xs));  // its address field counts 16 bytes
+    uint32_t it = 0, half = 0;      // k-block, half tile
+    Turn next{0, 0, 0, 0};
+    bool ok = true, ready = false;  // ready: the next operands have been seen
+    const uint32_t desc_x = (uint32_t)sw128_desc(smem_u32(xs));  // its address field counts 16 bytes
     for (int u = blockIdx.x; ok && u < total; u += units) {
       const Unit un = unit_at(u);
       const int n = (un.rows + ROUND - 1) / ROUND * ROUND;
@@ -520,42 +541,56 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
       fence_after();
       const uint32_t d0 = tmem + (half % ACCS) * HN, d1 = tmem + ((half + 1) % ACCS) * HN;
       const uint32_t id0 = idesc_bf16_f32(BM, n < HN ? n : HN), id1 = idesc_bf16_f32(BM, GLU ? n : n - HN);
-      for (int kb = 0; kb < kb_n; ++kb) {
-        if (!ready) {
-          if (!(ok = wait_warp(&sh.xfull[s], s_phase, abort_flag))) break;
-          if (!(ok = wait_warp(&sh.afull[a], a_phase, abort_flag))) break;
-        }
-        fence_after();
-        const uint64_t dx = desc_x + s * (SH::X_BYTES / 16);
-        const uint32_t ta = tmem + A_COL + a * SH::A_COLS;
-        auto issue = [&](int k0, int k1) {
+      // `turn`: a k-block's places in the rings
+      auto issue = [&](int kb, const Turn& turn, int k0, int k1) {
+        const uint32_t dx = desc_x + turn.s * (SH::X_BYTES / 16), ta = tmem + A_COL + turn.a * SH::A_COLS;
 #pragma unroll
-          for (int k = k0; k < k1; ++k) {
-            const uint32_t acc = (kb | k) != 0;
-            const uint64_t b = dx + (k / 4) * (ROWS * XC * 2 / 16) + (k % 4) * (UK * 2 / 16);
-            mma_ts(d0, ta + k * (UK / 2), b, id0, acc);
-            if (GLU) mma_ts(d1, ta + BK / 2 + k * (UK / 2), b, id1, acc);
-            else if (nh == 2) mma_ts(d1, ta + k * (UK / 2), b + HN * XC * 2 / 16, id1, acc);
-          }
-        };
-        // The issue of an MMA waits for the ones before it, and a look at a barrier takes as long as one or two of
-        // them, so the next k-block's barriers are looked at before this one's last MMAs.
-        if (elect_one()) issue(0, BK / UK - 1);
-        __syncwarp();
-        const uint32_t done = it++ % DONES;
-        if (++s == XD) s = 0, s_phase ^= 1;
-        if (++a == AD) a = 0, a_phase ^= 1;
-        const bool next_x = mbar_test(&sh.xfull[s], s_phase), next_a = mbar_test(&sh.afull[a], a_phase);
+        for (int k = k0; k < k1; ++k) {
+          const uint32_t b = dx + (k / 4) * (ROWS * XC * 2 / 16) + (k % 4) * (UK * 2 / 16);
+          auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+            if (k > 0) mma_ts<true>(d, a, b, id);
+            else mma_ts<false>(d, a, b, id, kb);
+          };
+          mma(d0, ta + k * (UK / 2), b, id0);
+          if (GLU) mma(d1, ta + BK / 2 + k * (UK / 2), b, id1);
+          else if (nh == 2) mma(d1, ta + k * (UK / 2), b + HN * XC * 2 / 16, id1);
+        }
+      };
+      auto finish = [&](int kb) {
+        commit(&sh.done[it % DONES]);
+        if (kb == kb_n - 1) {
+          commit(&sh.tfull[half % ACCS]);
+          if (nh == 2) commit(&sh.tfull[(half + 1) % ACCS]);
+        }
+      };
+      auto wait_for = [&](const Turn& turn) {
+        return wait_warp(&sh.xfull[turn.s], turn.s_phase, abort_flag) && wait_warp(&sh.afull[turn.a], turn.a_phase, abort_flag);
+      };
+      auto seen = [&](const Turn& turn) { return mbar_test(&sh.xfull[turn.s], turn.s_phase) & mbar_test(&sh.afull[turn.a], turn.a_phase); };
+      // The issue of a long MMA waits for the ones before it, and a look at a barrier takes as long as one or two of them,
+      // so the next k-block's barriers are looked at before this one's last MMAs; short ones are issued at once.
+      constexpr int FIRST = SH::few ? BK / UK : BK / UK - 1;
+      for (int kb = 0; kb < kb_n; ++kb) {
+        if (!ready && !(ok = wait_for(next))) break;
+        fence_after();
         if (elect_one()) {
-          issue(BK / UK - 1, BK / UK);
-          commit(&sh.done[done]);
-          if (kb == kb_n - 1) {
-            commit(&sh.tfull[half % ACCS]);
-            if (nh == 2) commit(&sh.tfull[(half + 1) % ACCS]);
-          }
+          issue(kb, next, 0, FIRST);
+          if (FIRST == BK / UK) finish(kb);
         }
         __syncwarp();
-        ready = __all_sync(0xffffffffu, next_x && next_a);
+        Turn after = next;
+        after.step(XD, AD);
+        const bool look = seen(after);
+        if (FIRST < BK / UK) {
+          if (elect_one()) {
+            issue(kb, next, FIRST, BK / UK);
+            finish(kb);
+          }
+          __syncwarp();
+        }
+        ++it;
+        next = after;
+        ready = __all_sync(0xffffffffu, look);
       }
       half += nh;
     }
