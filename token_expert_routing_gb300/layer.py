@@ -37,6 +37,8 @@ class LayerOutput:
     y_shared: Optional[torch.Tensor]
     schedule: Optional[dict] = None      # semmoe_dp_schedule outputs (when req_offsets is given)
     pred_next: Optional[torch.Tensor] = None  # next-layer rank per token (when trans is held)
+    x_norm: Optional[torch.Tensor] = None     # what the layer's steps read, when it holds a norm before them
+    next_out: Optional[torch.Tensor] = None   # out, normalised for the next block (when the layer holds that norm)
 
 
 def fuse_combine_default(I: int, dtype, shared: bool) -> bool:
@@ -90,6 +92,105 @@ class RouteSelect:
         return abi.SEMMOE_SCORE_SIGMOID if self.score == "sigmoid" else abi.SEMMOE_SCORE_SOFTMAX
 
 
+_NORMS = {"": abi.SEMMOE_NORM_NONE, "rms": abi.SEMMOE_NORM_RMS, "layer": abi.SEMMOE_NORM_LAYER}
+
+
+@dataclass(frozen=True)
+class BlockNorm:
+    """What stands between the residual stream and a layer (semmoe_norm, semmoe_combine_norm).
+
+    The layer's steps read before(x); its output is
+    out = residual_scale * x + block_scale * gate * after(y), and next_out = next(out).
+    before, after, next: "rms", "layer" or "" (none), with weight and bias [H] each (fp32 or bf16, None: 1 and 0; all of
+    after's and next's of one type), weight_offset added to the weights; gate [H] or None (forward takes one per token).
+    """
+    before: str = "rms"
+    before_weight: Optional[torch.Tensor] = None
+    before_bias: Optional[torch.Tensor] = None
+    after: str = ""
+    after_weight: Optional[torch.Tensor] = None
+    after_bias: Optional[torch.Tensor] = None
+    next: str = ""
+    next_weight: Optional[torch.Tensor] = None
+    next_bias: Optional[torch.Tensor] = None
+    weight_offset: float = 0.0
+    eps: float = 1e-6
+    gate: Optional[torch.Tensor] = None
+    block_scale: float = 1.0
+    residual_scale: float = 1.0
+
+    def __post_init__(self):
+        for name in ("before", "after", "next"):
+            if getattr(self, name) not in _NORMS:
+                raise ValueError(f"{name} is 'rms', 'layer' or ''")
+
+    def to(self, convert, H: int) -> "BlockNorm":
+        """This with every tensor converted; ValueError for one that is not of H values."""
+        out = {}
+        for f in dataclasses.fields(self):
+            t = getattr(self, f.name)
+            if torch.is_tensor(t):
+                if t.numel() != H:
+                    raise ValueError(f"{f.name} needs {H} values, has {t.numel()}")
+                out[f.name] = convert(t)
+        return dataclasses.replace(self, **out)
+
+
+@dataclass(frozen=True)
+class W4Experts:
+    """A layer's experts in 4-bit weights with group scales (semmoe_w4_grouped_ffn).
+
+    w13 [E,2I,H/2] and w2 [E,H,I/2] uint8 codes, two a byte; scales [E,2I,H/group] and [E,H,I/group] (fp32 or bf16);
+    zeros (uint8) of the same shapes, or None for 8 everywhere.
+    """
+    w13: torch.Tensor
+    w13_scales: torch.Tensor
+    w2: torch.Tensor
+    w2_scales: torch.Tensor
+    group: int
+    w13_zeros: Optional[torch.Tensor] = None
+    w2_zeros: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        E, I2, Hh = self.w13.shape
+        I, g = I2 // 2, self.group
+        if g not in (32, 64) and (g < 128 or g % 128):
+            raise ValueError("group is 32, 64 or a multiple of 128")
+        if 2 * Hh % g or I % g or I2 % 2 or tuple(self.w2.shape) != (E, 2 * Hh, I // 2):
+            raise ValueError("w13 [E, 2I, H / 2] and w2 [E, H, I / 2] need H and I in whole groups")
+        shapes = (E, I2, 2 * Hh // g), (E, 2 * Hh, I // g)
+        if (self.w13_zeros is None) != (self.w2_zeros is None):
+            raise ValueError("zeros of both weights or of none")
+        for name, t, shape in (("w13_scales", self.w13_scales, shapes[0]), ("w2_scales", self.w2_scales, shapes[1]),
+                               ("w13_zeros", self.w13_zeros, shapes[0]), ("w2_zeros", self.w2_zeros, shapes[1])):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name} needs shape {shape}, has {tuple(t.shape)}")
+
+    @classmethod
+    def quantize(cls, w13, w2, group: int = 128, zeros: bool = False, scale_dtype=torch.bfloat16, device="cuda") -> "W4Experts":
+        """Of w13 [E,2I,H] and w2 [E,H,I] (fp32 or bf16), by semmoe_w4_quantize on the device."""
+        def one(w):
+            w = w.to(device).contiguous()
+            E, n, K = w.shape
+            if K % group:
+                raise ValueError(f"{K} columns are not in groups of {group}")
+            codes = torch.empty(E, n, K // 2, dtype=torch.uint8, device=w.device)
+            scales = torch.empty(E, n, K // group, dtype=scale_dtype, device=w.device)
+            z = torch.empty(E, n, K // group, dtype=torch.uint8, device=w.device) if zeros else None
+            abi.semmoe_w4_quantize(w, E * n, K, group, codes, scales, z)
+            return codes, scales, z
+        a, b = one(w13), one(w2)
+        return cls(a[0], a[1], b[0], b[1], group, a[2], b[2])
+
+    def to(self, convert) -> "W4Experts":
+        return dataclasses.replace(self, **{f.name: convert(getattr(self, f.name)) for f in dataclasses.fields(self) if f.name != "group"})
+
+    @property
+    def args(self) -> tuple:
+        """The weights in the order of semmoe_w4_grouped_ffn."""
+        return self.w13, self.w13_scales, self.w13_zeros, self.w2, self.w2_scales, self.w2_zeros
+
+
 class MoELayer:
     """Weights and tables of one MoE layer, resident on a CUDA device.
 
@@ -103,16 +204,30 @@ class MoELayer:
     groups.  ``mx4``: the experts' weights are quantised here to 4-bit
     microscaled values (the originals are not kept) and forward quantises the
     token rows into expert order and runs semmoe_mx4_grouped_ffn; bf16 layers
-    with H % 32 == 0 and I % 32 == 0 (shared experts stay bf16).
+    with H % 32 == 0 and I % 32 == 0 (shared experts stay bf16).  ``w4`` (a
+    W4Experts): the experts as 4-bit weights with group scales, instead of w13 and
+    w2 (both None then); activations are bf16.  ``norm`` (a BlockNorm): x is the residual
+    stream, and the layer takes its norm, gate and residual with it.
     """
 
     def __init__(self, w_router, w13, w2, expert_rank, lut, R: int, k_max: int, ws13=None, ws2=None,
                  trans=None, sub_logw=None, fused_gather: Optional[bool] = None,
                  fused_combine: Optional[bool] = None, overlap: bool = True,
                  overlap_shared: bool = True, shared_at: str = "start", device="cuda",
-                 select: Optional[RouteSelect] = None, mx4: bool = False):
+                 select: Optional[RouteSelect] = None, mx4: bool = False, w4: Optional[W4Experts] = None,
+                 norm: Optional[BlockNorm] = None):
         if select is not None and sub_logw is not None:
             raise ValueError("select and sub_logw are two ways to route: give one")
+        if w4 is not None:
+            if w13 is not None or w2 is not None or mx4:
+                raise ValueError("w4 holds the experts: give w13 and w2 as None, and no mx4")
+            if fused_gather or fused_combine:
+                raise ValueError("w4 experts read x_perm and write y_perm: no fused_gather or fused_combine")
+            if any(t is not None and t.dtype != torch.bfloat16 for t in (ws13, ws2)):
+                raise ValueError("w4 needs bf16 shared experts")
+            fused_gather, fused_combine = False, False
+        elif w13 is None or w2 is None:
+            raise ValueError("give w13 and w2, or w4")
         if mx4:
             if w13.dtype != torch.bfloat16 or w2.dtype != torch.bfloat16:
                 raise ValueError("mx4 needs bf16 experts")
@@ -121,8 +236,11 @@ class MoELayer:
             if fused_gather or fused_combine:
                 raise ValueError("mx4 quantises the rows into expert order: no fused_gather or fused_combine")
             fused_gather, fused_combine = False, False
+        if norm is not None and fused_combine:
+            raise ValueError("norm ends the layer with semmoe_combine_norm: no fused_combine")
         dev = torch.device(device)
         c = lambda t: None if t is None else t.to(dev).contiguous()  # noqa: E731
+        self.w4 = None if w4 is None else w4.to(c)
         self.w_router, self.w13, self.w2 = c(w_router), c(w13), c(w2)
         self.expert_rank = c(expert_rank).to(torch.int32)
         self.lut = c(lut).to(torch.int32)
@@ -141,18 +259,23 @@ class MoELayer:
             raise ValueError("shared_at is 'start', 'route' or 'permute'")
         self.shared_at = shared_at  # where the shared experts' FFN forks off: before the router, or after the permute
         self._side = None
-        self.E, twoI, self.H = self.w13.shape
+        if self.w4 is not None:
+            self.E, twoI, self.H = self.w4.w13.shape[0], self.w4.w13.shape[1], 2 * self.w4.w13.shape[2]
+        else:
+            self.E, twoI, self.H = self.w13.shape
         self.I = twoI // 2
+        self.norm = None if norm is None else norm.to(c, self.H)
+        self.dtype = torch.bfloat16 if self.w4 is not None else self.w13.dtype
         # fused_gather: GEMM1 gathers its rows of x through the permutation and
         # no x_perm is written (bit-identical); None = fuse_gather_default
         if fused_gather is None:
-            fused_gather = fuse_gather_default(self.I, self.w13.dtype)
+            fused_gather = fuse_gather_default(self.I, self.dtype)
         self.fused_gather = bool(fused_gather)
         # fused_combine: GEMM2 adds its gate-weighted rows into an fp32 token-order
         # accumulator (no y_perm); bf16 experts only; None = fuse_combine_default
         if fused_combine is None:
-            fused_combine = fuse_combine_default(self.I, self.w13.dtype, ws13 is not None)
-        if fused_combine and self.w13.dtype != torch.bfloat16:
+            fused_combine = fuse_combine_default(self.I, self.dtype, ws13 is not None) and norm is None
+        if fused_combine and self.dtype != torch.bfloat16:
             raise ValueError("fused_combine needs bf16 experts")
         self.fused_combine = bool(fused_combine)
         self.I_s = 0 if ws13 is None else self.ws13.shape[0] // 2
@@ -160,7 +283,7 @@ class MoELayer:
         self.Ep = self.w_router.shape[0]          # router rows: experts, or parents (hierarchical)
         if self.sub_logw is not None and (self.E % self.Ep or self.sub_logw.numel() != self.E):
             raise ValueError("hierarchical gating needs E = Ep * N and sub_logw of E values")
-        self.dtype, self.dcode = self.w13.dtype, abi.dtype_code(self.w13)
+        self.dcode = abi.SEMMOE_BF16 if self.w4 is not None else abi.dtype_code(self.w13)
         self.device = dev
         self._ws = {}
         self._before = self._last = None  # the streams of the last forward but one, and of the last
@@ -211,7 +334,7 @@ class MoELayer:
 
     def forward(self, x, token_ids, k_per_token=None, k: Optional[int] = None, P: Optional[int] = None,
                 logits_in=None, keep_logits: bool = False, stream=None, marks=None,
-                req_offsets=None, side_marks=None, mark_external: bool = False) -> LayerOutput:
+                req_offsets=None, side_marks=None, mark_external: bool = False, gate=None) -> LayerOutput:
         """x [T,H] (activation type) and token_ids [T] int32 on the device.
 
         Budgets: ``k`` for every token, or ``k_per_token`` [T] int32 on the device
@@ -224,14 +347,15 @@ class MoELayer:
         ``side_marks`` gets (step name, start event, end event) for the steps
         run on the second stream.  ``mark_external``: the marks' events are
         recorded as event nodes when the forward is captured in a CUDA graph
-        (so each replay times its steps).  Every step has finished on ``stream``
+        (so each replay times its steps).  ``gate`` [T,H] (activation type or fp32): a gate per
+        token and channel in place of the one that the layer's ``norm`` holds.  Every step has finished on ``stream``
         when the work enqueued by this call has.  All memory of the call, the
         outputs' too, is taken from ``stream``'s.
         """
         if stream is not None and stream != torch.cuda.current_stream():
             with torch.cuda.stream(stream):
                 return self.forward(x, token_ids, k_per_token, k, P, logits_in, keep_logits, stream, marks,
-                                    req_offsets, side_marks, mark_external)
+                                    req_offsets, side_marks, mark_external, gate)
         s = torch.cuda.current_stream() if stream is None else stream
         self._before, self._last = self._last, s
         side = self._side_stream() if (self.overlap or self.overlap_shared) else None
@@ -283,6 +407,15 @@ class MoELayer:
             if side_marks is not None:
                 side_marks.append(("shared_ffn", ev1, side_event()))
 
+        if gate is not None and (self.norm is None or tuple(gate.shape) != (T, H)):
+            raise ValueError("gate [T, H] belongs to a layer that holds a norm")
+        stream_x, x_norm = x, None  # the residual stream
+        if self.norm is not None and self.norm.before:
+            nm = self.norm
+            x = x_norm = torch.empty_like(x)
+            abi.semmoe_norm(stream_x, T, H, _NORMS[nm.before], nm.before_weight, nm.before_bias, nm.weight_offset, nm.eps, x,
+                            stream)
+            mark("norm")
         has_shared = self.ws13 is not None
         if has_shared and self.shared_at == "start":
             run_shared()
@@ -369,11 +502,16 @@ class MoELayer:
         acc = torch.empty(T, H, dtype=torch.float32, device=dev) if self.fused_combine else None
         if has_shared and self.shared_at == "permute":  # the shared experts beside the routed FFN
             run_shared()
-        if self.mx4 is not None:
+        if self.w4 is not None:
+            ws = self._workspace("ffn", abi.semmoe_w4_grouped_ffn_workspace_size(P, I))
+        elif self.mx4 is not None:
             ws = self._workspace("ffn", abi.semmoe_mx4_grouped_ffn_workspace_size(P, E, I))
         else:
             ws = self._workspace("ffn", abi.semmoe_grouped_ffn_workspace_size(P, I, dcode))
-        if self.mx4 is not None:
+        if self.w4 is not None:
+            abi.semmoe_w4_grouped_ffn(x_perm, expert_offsets, phys_to_expert, *self.w4.args, P, E, H, I, self.w4.group, y_perm,
+                                      ws, stream)
+        elif self.mx4 is not None:
             xq = self._workspace("mx4_rows", P * (H // 2))
             xs = self._workspace("mx4_scales", abi.semmoe_mx4_scales_size(P, H, E))
             abi.semmoe_mx4_quantize_rows(x, T, H, pair_to_sorted, k_max, P, expert_offsets, E, xq, xs, stream)
@@ -393,14 +531,23 @@ class MoELayer:
         if forked:
             join()  # the second stream's steps are done before the combine (and the call's end)
         out = torch.empty(T, H, dtype=x.dtype, device=dev)
-        if self.fused_combine:
+        next_out = None
+        if self.norm is not None:
+            nm = self.norm
+            gate = nm.gate if gate is None else gate
+            next_out = torch.empty(T, H, dtype=x.dtype, device=dev) if nm.next else None
+            abi.semmoe_combine_norm(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, _NORMS[nm.after], nm.after_weight,
+                                    nm.after_bias, _NORMS[nm.next], nm.next_weight, nm.next_bias, nm.weight_offset, nm.eps,
+                                    gate, 0 if gate is None else gate.numel() // H, nm.block_scale, stream_x,
+                                    nm.residual_scale, out, next_out, stream)
+        elif self.fused_combine:
             abi.semmoe_combine_finish(acc, y_shared, T, H, out, stream)
         else:
             abi.semmoe_combine(y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P, out, stream)
         mark("combine")
         return LayerOutput(out, logits, topk_idx, topk_w, pred, counts, remote, expert_offsets,
                            rank_offsets, phys_to_expert, expert_counts, sorted_to_pair[:P],
-                           pair_to_sorted, x_perm, y_perm, y_shared, sched, pred_next)
+                           pair_to_sorted, x_perm, y_perm, y_shared, sched, pred_next, x_norm, next_out)
 
     def forward_host(self, x_host, ids_host, k_host=None, k: Optional[int] = None, out_host=None,
                      stream=None) -> torch.Tensor:
