@@ -217,19 +217,30 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Two tokens' columns of a warp's 32 weight rows (v0, v1: this lane's row): even lanes
-// store the first token's pair of rows, odd lanes the second's.
-__device__ __forceinline__ void store_pair(float v0, float v1, __nv_bfloat16* first, size_t stride, int left, bool live, int lane) {
-  const __nv_bfloat162 own2 = __floats2bfloat162_rn(v0, v1);
-  const uint32_t own = *reinterpret_cast<const uint32_t*>(&own2);
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+// 2 N tokens' columns of a warp's 32 weight rows, v[i]: this lane's row of tokens 2 i and 2 i + 1 in bf16.  Even lanes store
+// the first token's pair of rows, odd lanes the second's.  left: tokens from the first one on that are the unit's.
+// All exchanges come before the first store, and the stores are predicated: one after the other, with a branch each, they made
+// the epilogue four times as long.
+template <int N>
+__device__ __forceinline__ void store_pairs(const uint32_t (&v)[N], __nv_bfloat16* first, size_t stride, int left, bool live, int lane) {
   const int odd = lane & 1;
-  const uint32_t v = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-  // (predicated: as a branch it cost four times the epilogue's time)
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(
-                   (int)(live && odd < left)),
-               "l"(first + (odd ? stride : 0)), "r"(v)
-               : "memory");
+  uint32_t out[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[i], 1);
+    out[i] = odd ? __byte_perm(other, v[i], 0x7632) : __byte_perm(v[i], other, 0x5410);
+  }
+  if (odd) first += stride;
+  const int mine = live ? left - odd : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %0, %3;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(mine),
+                 "l"(first + 2 * i * stride), "r"(out[i]), "r"(2 * i)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <bool GLU, int ROWS, int MODE>
@@ -449,12 +460,12 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
           tmem_ld16(tu + c, up);
           tmem_ld_wait();
           if (c + 16 >= PART || left <= c + 16) leave_acc(half), leave_acc(half + 1);
+          uint32_t v[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float v0 = unscaled_swiglu(__uint_as_float(g[i]), __uint_as_float(up[i]));
-            const float v1 = unscaled_swiglu(__uint_as_float(g[i + 1]), __uint_as_float(up[i + 1]));
-            store_pair(v0, v1, col + (size_t)(PART * w + c + i) * pr.N, pr.N, left - c - i, live, lane);
-          }
+          for (int i = 0; i < 8; ++i)
+            v[i] = pack_bf16x2(unscaled_swiglu(__uint_as_float(g[2 * i]), __uint_as_float(up[2 * i])),
+                               unscaled_swiglu(__uint_as_float(g[2 * i + 1]), __uint_as_float(up[2 * i + 1])));
+          store_pairs(v, col + (size_t)(PART * w + c) * pr.N, pr.N, left - c, live, lane);
         }
         if (left <= 0) leave_acc(half), leave_acc(half + 1);
         half += 2;
@@ -473,10 +484,11 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
             tmem_ld32(ty + c, y);
             tmem_ld_wait();
             if (c + 32 >= PART || left <= c + 32) leave_acc(half);
+            uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              store_pair(__uint_as_float(y[i]) * kUnscale, __uint_as_float(y[i + 1]) * kUnscale,
-                         col + (size_t)(t0 + c + i) * pr.N, pr.N, left - c - i, live, lane);
+            for (int i = 0; i < 16; ++i)
+              v[i] = pack_bf16x2(__uint_as_float(y[2 * i]) * kUnscale, __uint_as_float(y[2 * i + 1]) * kUnscale);
+            store_pairs(v, col + (size_t)(t0 + c) * pr.N, pr.N, left - c, live, lane);
           }
           if (left <= 0) leave_acc(half);
         }
