@@ -9,8 +9,9 @@
 // stores, so every input is read once and y never reaches memory; the squares are taken
 // about the mean in a second sweep over the registers, not as a difference of sums.
 // A row belongs to one warp while it fits 32 lanes x 4 pieces of 16 bytes, else to one CTA.
-// Measured (GB300): the norm of 16384 x 2048 bf16, 23.4 us (5.7 TB/s); the combine of 8 rows a token with both norms, a gate
-// per channel and the residual, 16384 x 2048 bf16, 139 us (5.3 TB/s).
+// Measured (GB300, calls of a captured graph): the norm of 16384 x 2048 bf16, 23.0 us (5.8 TB/s); the combine of 8 rows a token
+// with both norms, a gate per channel and the residual, 16384 x 2048 bf16, 134 us (5.5 TB/s); a dense block's row with a gate a
+// token, the residual and one norm, 4096 x 2048 bf16, 16.8 us (5.0 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -27,13 +28,18 @@ constexpr int RING = 4;          // rows on their way to a row's threads, and th
 constexpr int kMaxWarps = 32;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Threads of a CTA (plan below), and CTAs that an SM's registers have to hold.
+// Threads of a CTA (plan below), and CTAs that an SM's registers have to hold: as many as come without spills that matter
+// (4 CTAs of the combine's two-piece form 134 us at 16384 x 2048, 3 of them 141, 5 143; 4 of the dense one's 25 us at
+// 4096 x 2048, 3 of them 16.8).
 template <bool WARP, int CH>
 constexpr int max_threads() { return WARP ? 32 * kWarpRows : CH == 4 ? 512 : 256; }
 template <bool WARP, int CH>
 constexpr int norm_ctas() { return WARP ? (CH == 4 ? 6 : 8) : CH == 1 ? 5 : CH == 2 ? 4 : 1; }
 template <bool WARP, int CH>
-constexpr int min_ctas() { return WARP ? (CH == 4 ? 6 : 8) : CH == 1 ? 4 : CH == 2 ? 3 : 1; }
+constexpr int min_ctas() { return WARP ? (CH == 4 ? 6 : 8) : CH == 1 ? 4 : CH == 2 ? 4 : 1; }
+
+template <bool WARP, int CH>
+constexpr int dense_ctas() { return WARP ? (CH == 4 ? 3 : CH == 2 ? 6 : 8) : CH == 1 ? 4 : CH == 2 ? 3 : 1; }
 
 // VEC weights from `col` on, fp32 or bf16 (16-byte aligned base; col a multiple of VEC).
 template <int VEC>
@@ -210,6 +216,128 @@ norm_kernel(const T* x, int T_, int H, const __grid_constant__ NormArgs n, T* ou
   }
 }
 
+// From the block's row on: norm, gate, residual, the sum's row stored, the next block's norm, its row stored.  `next` comes to
+// the gate's own row (of type T), then the residual's; `piece` reads 16 bytes a thread of it.
+template <typename T, bool WARP, int CH, typename Next, typename Piece>
+__device__ __forceinline__ void finish_row(const CombineNorm& a, long long t, float (&v)[CH][Vec16<T>::N], int col0, int step,
+                                           RowReduce& red, bool own_gate, Next&& next, Piece&& piece) {
+  using V = Vec16<T>;
+  constexpr int VEC = V::N;
+  const int H = a.H;
+  if (a.post.kind != SEMMOE_NORM_NONE) {
+    const RowStats st = row_stats<WARP, CH, VEC>(v, a.post.kind, H, a.post.eps, col0, step, red);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = col0 + c * step;
+      if (col < H) apply_norm<VEC>(v[c], st, a.post.weight, a.post.bias, a.post.w_bf16, a.post.offset, col);
+    }
+  }
+  if (a.gate != nullptr) {
+    const int at = own_gate ? next(true) : 0;
+    const size_t row = a.gate_rows > 1 ? (size_t)t * H : 0;
+    const void* p = a.gate_bf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.gate) + row)
+                                : static_cast<const void*>(static_cast<const float*>(a.gate) + row);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = col0 + c * step;
+      if (col < H) {
+        float g[VEC];
+        if (own_gate) piece(true, at, c, g);
+        else load_weights(p, a.gate_bf16, col, g);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] *= g[i];
+      }
+    }
+  }
+  const int at = a.residual != nullptr ? next(false) : 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = col0 + c * step;
+    if (col < H) {
+      if (a.residual != nullptr) {
+        float r[VEC];
+        piece(false, at, c, r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(a.residual_scale, r[i], a.block_scale * v[c][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[c][i] *= a.block_scale;
+      }
+      V::store(static_cast<T*>(a.out) + (size_t)t * H + col, v[c]);
+    }
+  }
+  if (a.next.kind == SEMMOE_NORM_NONE) return;
+  const RowStats st = row_stats<WARP, CH, VEC>(v, a.next.kind, H, a.next.eps, col0, step, red);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = col0 + c * step;
+    if (col < H) {
+      apply_norm<VEC>(v[c], st, a.next.weight, a.next.bias, a.next.w_bf16, a.next.offset, col);
+      V::store(static_cast<T*>(a.next_out) + (size_t)t * H + col, v[c]);
+    }
+  }
+}
+
+// A dense block's row (no slots).  A token needs the same two or three rows each time, so they need no list and no ring: their
+// next pieces are fetched into registers as soon as this token's have been used (16.8 us at 4096 x 2048 bf16, 23.9 through
+// the ring below).  A shared row, which a dense block seldom has, is read where it is added.
+template <typename T, bool WARP, int CH>
+__global__ void __launch_bounds__(max_threads<WARP, CH>(), dense_ctas<WARP, CH>())
+dense_norm_kernel(const __grid_constant__ CombineNorm a) {
+  using V = Vec16<T>;
+  constexpr int VEC = V::N;
+  __shared__ float part[2][kMaxWarps];
+  RowReduce red{part, 0};
+  pdl_trigger();
+  pdl_wait();
+  const int tid = WARP ? threadIdx.x % 32 : threadIdx.x, per = WARP ? 32 : blockDim.x;
+  const int rows = WARP ? kWarpRows : 1, row_of = WARP ? threadIdx.x / 32 : 0;
+  const int col0 = tid * VEC, step = per * VEC, T_ = a.T, H = a.H;
+  const T *y = static_cast<const T*>(a.y_perm), *y_shared = static_cast<const T*>(a.y_shared),
+          *residual = static_cast<const T*>(a.residual),
+          *gate_rows = a.gate_rows > 1 && a.gate_bf16 == (sizeof(T) == 2) ? static_cast<const T*>(a.gate) : nullptr;
+  uint4 raw[3][CH];  // pieces of the block's row, the gate's, the residual's
+  auto fetch = [&](long long t, int c, const T* p, uint4& r) {
+    const int col = col0 + c * step;
+    r = p != nullptr && t < T_ && col < H ? *reinterpret_cast<const uint4*>(p + (size_t)t * H + col) : make_uint4(0, 0, 0, 0);
+  };
+  long long t = (long long)blockIdx.x * rows + row_of;
+  const long long stride = (long long)gridDim.x * rows;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    fetch(t, c, y, raw[0][c]);
+    fetch(t, c, gate_rows, raw[1][c]);
+    fetch(t, c, residual, raw[2][c]);
+  }
+  for (; t < T_; t += stride) {
+    float v[CH][VEC];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      V::unpack(raw[0][c], v[c]);
+      fetch(t + stride, c, y, raw[0][c]);
+    }
+    if (y_shared != nullptr) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = col0 + c * step;
+        if (col < H) {
+          float r[VEC];
+          V::load(y_shared + (size_t)t * H + col, r);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[c][i] += r[i];
+        }
+      }
+    }
+    finish_row<T, WARP, CH>(
+        a, t, v, col0, step, red, gate_rows != nullptr, [&](bool) { return 0; },
+        [&](bool gate, int, int c, float (&r)[VEC]) {
+          uint4& mine = gate ? raw[1][c] : raw[2][c];
+          V::unpack(mine, r);
+          fetch(t + stride, c, gate ? gate_rows : residual, mine);
+        });
+  }
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -242,8 +370,7 @@ combine_norm_kernel(const __grid_constant__ CombineNorm a) {
   const int tid = WARP ? lane : threadIdx.x, per = WARP ? 32 : blockDim.x;
   const int rows = WARP ? kWarpRows : 1, row_of = WARP ? warp : 0;
   const int col0 = tid * VEC, step = per * VEC;
-  const bool dense = a.pair_to_sorted == nullptr;
-  const int kk = dense ? 1 : a.k_max < 32 ? a.k_max : 32;
+  const int kk = a.k_max < 32 ? a.k_max : 32;
   const T *y_perm = static_cast<const T*>(a.y_perm), *y_shared = static_cast<const T*>(a.y_shared),
           *residual = static_cast<const T*>(a.residual), *gate_rows = static_cast<const T*>(a.gate);
   const bool own_gate = a.gate != nullptr && a.gate_rows > 1 && a.gate_bf16 == (sizeof(T) == 2);  // a row of its own, of type T
@@ -256,19 +383,15 @@ combine_norm_kernel(const __grid_constant__ CombineNorm a) {
   auto read_slots = [&](long long t) {
     q_l = -1, w_l = 0.f;
     if (t >= T_ || lane >= kk) return;
-    if (dense) {
-      q_l = (int)t, w_l = 1.f;
-    } else {
-      q_l = a.pair_to_sorted[(size_t)t * a.k_max + lane];
-      w_l = a.topk_w[(size_t)t * a.k_max + lane];
-    }
+    q_l = a.pair_to_sorted[(size_t)t * a.k_max + lane];
+    w_l = a.topk_w[(size_t)t * a.k_max + lane];
   };
   const long long stride = (long long)gridDim.x * rows;
   // the copies' place: a token, its list (kept for the sums, RING of them in turn), the next item of it
   long long t_c = (long long)blockIdx.x * rows + row_of;
   int turn_c = 0, next = 0, items = 0, to = 0;
   auto enter = [&]() {
-    if (!dense && q_l >= a.P) {
+    if (q_l >= a.P) {
       flag(SEMMOE_DEVERR_PAIRS);
       q_l = -1;
     }
@@ -362,7 +485,7 @@ combine_norm_kernel(const __grid_constant__ CombineNorm a) {
       }
     }
     if (tk.row[0] == nullptr) next_item();  // the list's only item, which holds nothing
-    for (int j = 32; !dense && j < a.k_max; ++j) {  // budgets above 32 experts: read the slot directly
+    for (int j = 32; j < a.k_max; ++j) {  // budgets above 32 experts: read the slot directly
       const int q = a.pair_to_sorted[(size_t)t * a.k_max + j];
       if (q < 0) continue;
       if (q >= a.P) {
@@ -388,58 +511,9 @@ combine_norm_kernel(const __grid_constant__ CombineNorm a) {
         for (int i = 0; i < VEC; ++i) v[c][i] = 0.f;
       }
     }
-    if (a.post.kind != SEMMOE_NORM_NONE) {
-      const RowStats st = row_stats<WARP, CH, VEC>(v, a.post.kind, H, a.post.eps, col0, step, red);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = col0 + c * step;
-        if (col < H) apply_norm<VEC>(v[c], st, a.post.weight, a.post.bias, a.post.w_bf16, a.post.offset, col);
-      }
-    }
-    if (a.gate != nullptr) {
-      const int at = own_gate ? next_item() : 0;
-      const size_t row = a.gate_rows > 1 ? (size_t)t * H : 0;
-      const void* p = a.gate_bf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.gate) + row)
-                                  : static_cast<const void*>(static_cast<const float*>(a.gate) + row);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = col0 + c * step;
-        if (col < H) {
-          float g[VEC];
-          if (own_gate) values(at, c, g);
-          else load_weights(p, a.gate_bf16, col, g);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c][i] *= g[i];
-        }
-      }
-    }
-    const int at = residual != nullptr ? next_item() : 0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      if (col < H) {
-        if (residual != nullptr) {
-          float r[VEC];
-          values(at, c, r);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c][i] = fmaf(a.residual_scale, r[i], a.block_scale * v[c][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[c][i] *= a.block_scale;
-        }
-        V::store(static_cast<T*>(a.out) + (size_t)t * H + col, v[c]);
-      }
-    }
-    if (a.next.kind == SEMMOE_NORM_NONE) continue;
-    const RowStats st = row_stats<WARP, CH, VEC>(v, a.next.kind, H, a.next.eps, col0, step, red);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = col0 + c * step;
-      if (col < H) {
-        apply_norm<VEC>(v[c], st, a.next.weight, a.next.bias, a.next.w_bf16, a.next.offset, col);
-        V::store(static_cast<T*>(a.next_out) + (size_t)t * H + col, v[c]);
-      }
-    }
+    finish_row<T, WARP, CH>(
+        a, t, v, col0, step, red, own_gate, [&](bool) { return next_item(); },
+        [&](bool, int at, int c, float (&r)[VEC]) { values(at, c, r); });
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -449,9 +523,9 @@ struct RowPlan {
   bool warp;
   int pieces, threads;
 };
-// Many rows: two pieces a thread, so that reductions and loop are shared by more bytes (with one piece the norm of 16384 x
-// 2048 took 33 us where two take 29, the combine 170 and 135; with four 33 and 141: fewer warps at a time).  Few rows,
-// whose time is one row's: as many threads as there are pieces.
+// Many rows: two pieces a thread, so that reductions and loop are shared by more bytes (the combine of 16384 x 2048 takes 169 us
+// with one piece and 134 with two; four mean fewer warps at a time).  Few rows, whose time is one row's: as many threads as
+// there are pieces.
 RowPlan plan(int H, int vec, int T) {
   const int n = ceil_div(H, vec);
   if (T >= 4 * sm_count() && n <= 128) return RowPlan{true, n <= 32 ? 1 : n <= 64 ? 2 : 4, 32 * kWarpRows};
@@ -482,6 +556,10 @@ cudaError_t launch_norm_t(const RowPlan& p, const void* x, int T_, int H, const 
 
 template <typename T, bool WARP, int CH>
 cudaError_t launch_t(const RowPlan& p, const CombineNorm& a, cudaStream_t s) {
+  if (a.pair_to_sorted == nullptr) {
+    const int n = ctas_per_sm(p, dense_ctas<WARP, CH>(), max_threads<WARP, CH>(), 0);
+    return launch_kernel(dense_norm_kernel<T, WARP, CH>, dim3(resident_grid(p, a.T, n)), dim3(p.threads), 0, s, 1, true, a);
+  }
   auto kern = combine_norm_kernel<T, WARP, CH>;
   const int smem = RING * (CH * p.threads * 16 + p.threads / 32 * (int)sizeof(Token));
   static std::atomic<unsigned long long> smem_set{0};
