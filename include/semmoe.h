@@ -683,8 +683,10 @@ int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dty
  * x       [device] [P,K] bf16
  * codes, scales, zeros  [device] E matrices of N rows
  * out     [device] [P,N] bf16
- * Limits: N % 8 == 0, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn (a group that is skipped leaves its rows of
- * out as they were).
+ * A weight is used exactly or rounded once to bf16, as the sizes have it; bf16 scales without zeros: magnitudes below 2^34;
+ * rows' values: below 2^100 (sums of up to 143 x are held on the way).
+ * Limits: N % 8 == 0, 1 <= E <= 256, (P / 8 + E) ceil(N / 16) <= 2^31 - 2^16.  Device checks as semmoe_grouped_ffn (a
+ * group that is skipped leaves its rows of out as they were).
  */
 int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert,
                            const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros, int P, int E,
@@ -699,7 +701,8 @@ int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const i
  *         (both with zeros or both without, one scale_dtype, one group)
  * y_perm  [device] [P,H] bf16 out
  * ws      [device] workspace of semmoe_w4_grouped_ffn_workspace_size() bytes (256-byte aligned)
- * Limits: H and I multiples of group, 1 <= E <= 256.  Device checks as semmoe_grouped_ffn.
+ * Weights and limits as semmoe_w4_grouped_gemm, for N = H and for N = I; H and I multiples of group.  Calls that run at the same
+ * time need workspaces of their own.
  */
 size_t semmoe_w4_grouped_ffn_workspace_size(int P, int I);
 int semmoe_w4_grouped_ffn(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert,

@@ -206,6 +206,33 @@ def test_combine_norm_without_norms_is_the_combine():
     assert abi().semmoe_check_errors() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(2, 264), (2500, 136), (2500, 264), (2500, 1032), (2100, 2056), (1300, 4104), (700, 16384 // 2)])
+def test_dense_rows_are_one_slot_of_weight_one(T, H, dtype):
+    """A dense block's rows, the residual's buffer written over, against the same sums by way of the maps: equal bit for bit."""
+    rng = np.random.default_rng(T + H)
+    y, shared, residual, gates = (cuda(rng.standard_normal((T, H)), dtype) for _ in range(4))
+    post, nxt, bias, row = (cuda(rng.standard_normal(H), torch.float32) for _ in range(4))
+    ident = torch.arange(T, dtype=torch.int32, device="cuda")
+    ones = torch.ones(T, device="cuda")
+    other = gates.to(torch.float32 if dtype == torch.bfloat16 else torch.bfloat16)
+    for s, g, pk, nk in ((None, gates, 1, 2), (shared, other, 0, 1), (shared, row, 2, 0), (None, None, 0, 2)):
+        got = []
+        for maps in (False, True):
+            out, z = residual.clone(), torch.zeros_like(residual)
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                abi().semmoe_combine_norm(y, ident if maps else None, ones if maps else None, s, T, H, 1 if maps else 0, T,
+                                          pk, post if pk else None, None, nk, nxt if nk else None, bias if nk == 2 else None, 0.5, 1e-6,
+                                          g, 0 if g is None else 1 if g is row else T, 0.75, out, 1.25, out, z if nk else None)
+            torch.cuda.current_stream().wait_stream(stream)
+            got.append((out, z))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert not torch.equal(got[0][0], residual)
+    assert abi().semmoe_check_errors() == 0
+
+
 def test_a_bad_sorted_row_is_flagged_and_skipped():
     rng = np.random.default_rng(6)
     T, H, k = 5, 256, 2

@@ -83,7 +83,8 @@ def test_conversion_refusals(abi, call, kw, word):
     (dict(N=4), "N = 4"), (dict(N=60), "N = 60"), (dict(x=None), "null"), (dict(off=None), "null"), (dict(pe=None), "null"),
     (dict(codes=None), "null"), (dict(scales=None), "null"), (dict(out=None), "null"), (dict(x=BAD8), "misaligned"),
     (dict(out=BAD8), "misaligned"), (dict(codes=BAD8), "misaligned"), (dict(scales=ctypes.c_void_p(2), sd=0), "misaligned"),
-    (dict(off=ctypes.c_void_p(2)), "misaligned")])
+    (dict(off=ctypes.c_void_p(2)), "misaligned"), (dict(n=1 << 30, N=256), "P * N too large"), (dict(N=1 << 30), "N or K"),
+    (dict(n=2 ** 31 - 2 ** 16, E=256, N=120), "P * N too large")])
 def test_product_refusals(abi, kw, word):
     assert gemm(abi.lib(), **kw) == 1
     assert word in _err(abi.lib())
@@ -93,7 +94,8 @@ def test_product_refusals(abi, kw, word):
     (dict(H=192), "192 columns"), (dict(I=64), "64 columns"), (dict(E=0), "E = 0"), (dict(n=-1), "P = -1"), (dict(sd=5), "scale_dtype 5"),
     (dict(b=None), "null"), (dict(sb=None), "null"), (dict(a=None), "null"), (dict(y=None), "null"), (dict(za=None), "go together"),
     (dict(zb=None), "go together"), (dict(ws=None), "workspace"), (dict(ws=ctypes.c_void_p(4112)), "workspace"),
-    (dict(ws_bytes=100), "workspace"), (dict(b=BAD8), "misaligned"), (dict(y=BAD8), "misaligned")])
+    (dict(ws_bytes=100), "workspace"), (dict(n=1 << 30, H=256), "P * N too large"), (dict(n=1 << 28, I=1024), "P * I too large"),
+    (dict(I=1 << 30), "I or P * I"), (dict(b=BAD8), "misaligned"), (dict(y=BAD8), "misaligned")])
 def test_ffn_refusals(abi, kw, word):
     assert ffn(abi.lib(), **kw) == 1
     assert word in _err(abi.lib())

@@ -1,5 +1,5 @@
 // Grouped products of bf16 rows with 4-bit weights (w4.cuh) on the 5th-generation
-// tensor cores, for experts with more than a few rows.
+// tensor cores, for all but a few rows.
 //
 // The weights are the left operand (M = 128 weight rows), held in tensor memory: a
 // thread turns the codes of its row into bf16 in registers and writes them to its
@@ -19,8 +19,17 @@
 //   epilogue    EPI / 4 groups of four, the columns of an accumulator divided between them
 //   producers   one warp for codes ([128 rows x 128 columns] a slot), one for token rows
 //   issuer      allocates TMEM, issues the MMAs (M128 N16..128 K16)
-// Units of few token rows are bound by the expansion: 16 warps of it, k-blocks of 128 columns
-// (fewer barriers a weight); units of many by the MMAs: 8 and 8 warps, k-blocks of 64.
+// 16 warps expand; four (few token rows a unit) or eight read the accumulators.  With few rows a k-block has 128
+// columns, which halves the barriers a weight, else 64, so that more A blocks are on their way.
+//
+// What bounds it.  Many rows: the MMAs (a SwiGLU k-block of 128 rows takes 630 to 650 clocks of MMAs and 850 to 900 in
+// all; the rest is waited for accumulators, token rows and A blocks in turn).  A decode batch: neither the bytes nor the
+// expansion (the ALUs work half of the time) but the hand-overs between the roles, some 450 clocks a k-block with the
+// work left out.  Measured (GB300, 128 experts of 2048 x 768 or 64 of 2048 x 1408, groups of 128, bf16 scales): 131072 rows
+// through the FFN 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 74 us (4.3 TB/s of weights; 92 with groups of 64 and zero
+// points), 384 rows through one 1408 x 2048 product 34.5 us.
+// Tried and slower: 24 expansion warps; accumulators split by k-step; a single lane for the issuer's whole loop; decode
+// batches on the warp-level product with codes straight into registers (48.6 us where this takes 34.5, its loads alone 33).
 //
 // Expansion of a word of eight codes: two masked halves (codes of even and odd columns), then
 // one byte permutation a pair of columns, whose result reads as two bf16 denormals
@@ -219,8 +228,8 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // 2 N tokens' columns of a warp's 32 weight rows, v[i]: this lane's row of tokens 2 i and 2 i + 1 in bf16.  Even lanes store
 // the first token's pair of rows, odd lanes the second's.  left: tokens from the first one on that are the unit's.
-// All exchanges come before the first store, and the stores are predicated: one after the other, with a branch each, they made
-// the epilogue four times as long.
+// All exchanges come before the first store, and the stores are predicated: a branch around each one made the epilogue nearly
+// twice as long (4465 clocks a SwiGLU unit's half, 2381 without).
 template <int N>
 __device__ __forceinline__ void store_pairs(const uint32_t (&v)[N], __nv_bfloat16* first, size_t stride, int left, bool live, int lane) {
   const int odd = lane & 1;
