@@ -82,6 +82,8 @@ Q = ctypes.c_void_p(8192)
     (after, dict(nxt=1, no=P), "of its own"), (after, dict(ys=ctypes.c_void_p(8)), "aligned"),
     (after, dict(r=ctypes.c_void_p(4)), "aligned"), (after, dict(g=ctypes.c_void_p(8), gr=1), "aligned"),
     (after, dict(q=ctypes.c_void_p(2)), "misaligned"), (after, dict(pw=ctypes.c_void_p(8)), "aligned"),
+    (after, dict(), "out is neither"), (after, dict(q=None, g=P, gr=1), "out is neither"),
+    (after, dict(y=Q, g=ctypes.c_void_p(16384), gr=4, nxt=1, no=ctypes.c_void_p(16384)), "next_out no gate"),
 ])
 def test_refusals(abi, call, kw, word):
     lib = abi.lib()
