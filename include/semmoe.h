@@ -801,6 +801,14 @@ int semmoe_selftest_mx4_wait(const uint8_t* a, const uint8_t* a_scales, const in
                              const int32_t* phys_to_expert, const uint8_t* b, const uint8_t* b_scales, int P, int E,
                              int N, int K, float* out, void* stream);
 
+/*
+ * semmoe_selftest_w4_wait -- the same for semmoe_w4_grouped_gemm (0 < P <= 4096) on the tensor cores: the issuing warp
+ * of every CTA first waits for a barrier that only it could complete.  Ends as semmoe_selftest_mx4_wait does.
+ */
+int semmoe_selftest_w4_wait(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert, const uint8_t* codes,
+                            const void* scales, int scale_dtype, const uint8_t* zeros, int P, int E, int N, int K, int group,
+                            void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -284,3 +284,28 @@ def test_ffn_in_graphs_that_run_at_once(P):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ys, want))
     assert abi().semmoe_check_errors() == 0
+
+
+def test_product_whose_wait_runs_out_ends_and_the_next_is_right():
+    """Every CTA's issuer waits for a barrier that only it could complete, for its 2 s; all other roles then stop."""
+    import time
+    a = abi()
+    rng = np.random.default_rng(17)
+    E, N, K, group = 3, 264, 1408, 128
+    for P in (40, 700):  # k-blocks of 128 and of 64 columns
+        dev, w = weights(rng, E, N, K, group, "bf16", False, exact=True)
+        x = rng.integers(-4, 5, (P, K)).astype(np.float64)
+        off, pe = split(rng, P, E)
+        out = torch.full((P, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        xt, ot, pt = cuda(x, torch.bfloat16), cuda(off, torch.int32), cuda(pe, torch.int32)
+        t0 = time.perf_counter()
+        a.semmoe_selftest_w4_wait(xt, ot, pt, *dev, P, E, N, K, group, out)
+        with pytest.raises(a.SemMoEError) as ei:
+            a.semmoe_check_errors()
+        assert ei.value.code == a.SEMMOE_ERR_DEVICE_TIMEOUT and ei.value.bits & a.SEMMOE_DEVERR_TIMEOUT
+        assert 0.1 < time.perf_counter() - t0 < 60
+        assert bool((out == 7).all())
+        assert a.semmoe_check_errors() == 0
+        a.semmoe_w4_grouped_gemm(xt, ot, pt, *dev, P, E, N, K, group, out)
+        np.testing.assert_array_equal(np_(out), oracle.bf16_round(oracle.w4_grouped_product(x, w, off, pe)))
+        assert a.semmoe_check_errors() == 0

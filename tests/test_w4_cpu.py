@@ -151,3 +151,10 @@ def test_scales_of_one_type(abi):
     good["w2s"] = good["w2s"].float()
     with pytest.raises(ValueError, match="one type"):
         call(abi, good)
+
+
+@pytest.mark.parametrize("n,kw,word", [(0, {}, "P=0"), (4097, {}, "P=4097"), (8, dict(x=None), "null"), (8, dict(K=192), "192 columns")])
+def test_wait_selftest_refusals(abi, n, kw, word):
+    a = {**dict(x=P, K=256), **kw}
+    assert abi.lib().semmoe_selftest_w4_wait(a["x"], P, P, P, P, 1, P, n, 4, 64, a["K"], 128, P, None) == 1
+    assert word in _err(abi.lib())

@@ -845,6 +845,20 @@ int semmoe_selftest_mx4_wait(const uint8_t* a, const uint8_t* a_scales, const in
                      fn);
 }
 
+int semmoe_selftest_w4_wait(const void* x, const int32_t* expert_offsets, const int32_t* phys_to_expert, const uint8_t* codes,
+                            const void* scales, int scale_dtype, const uint8_t* zeros, int P, int E, int N, int K, int group,
+                            void* out, void* stream) {
+  const char* fn = "semmoe_selftest_w4_wait";
+  int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, codes, scales, scale_dtype, zeros, P, E, N, K, group, out);
+  if (rc != SEMMOE_OK) return rc;
+  REQUIRE(P > 0 && P <= 4096, "%s: need 0 < P <= 4096 (P=%d)", fn, P);
+  CHECK_DEVICE(fn);
+  return cuda_status(launch_selftest_w4_wait(x, expert_offsets, phys_to_expert,
+                                             w4::Weights{codes, scales, zeros, scale_dtype == SEMMOE_BF16}, P, E, N, K, group, out,
+                                             static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
 int semmoe_selftest_fused_ready_wait(const void* x_perm, const void* w13, const void* w2, int P, int H, int I,
                                      void* y_perm, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_ffn_args("semmoe_selftest_fused_ready_wait", x_perm, w13, w2, SEMMOE_BF16, P, H, I, y_perm, ws,

@@ -208,6 +208,8 @@ cudaError_t launch_w4_dequantize(const w4::Weights& w, long long rows, int K, in
 cudaError_t launch_w4_grouped_gemm(const void* x, const int32_t* offsets, const int32_t* experts, const w4::Weights& w,
                                    int P, int E, int N, int K, int group, void* out, cudaStream_t s);
 size_t w4_ffn_ws_bytes(int P, int I);
+cudaError_t launch_selftest_w4_wait(const void* x, const int32_t* offsets, const int32_t* experts, const w4::Weights& w, int P,
+                                    int E, int N, int K, int group, void* out, cudaStream_t s);
 cudaError_t launch_w4_grouped_ffn(const void* x, const int32_t* offsets, const int32_t* experts, const w4::Weights& w13,
                                   const w4::Weights& w2, int P, int E, int H, int I, int group, void* y, void* ws,
                                   cudaStream_t s);

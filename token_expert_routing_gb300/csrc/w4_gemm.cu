@@ -379,6 +379,13 @@ cudaError_t launch_w4_grouped_gemm(const void* x, const int32_t* offsets, const 
                                s);
 }
 
+cudaError_t launch_selftest_w4_wait(const void* x, const int32_t* offsets, const int32_t* experts, const Weights& w, int P,
+                                    int E, int N, int K, int group, void* out, cudaStream_t s) {
+  return launch_w4_tc_plain(Product{static_cast<const __nv_bfloat16*>(x), offsets, experts, w, P, E, N, K, group, 0, false,
+                                    static_cast<__nv_bfloat16*>(out), true},
+                            s);
+}
+
 cudaError_t launch_w4_grouped_ffn(const void* x, const int32_t* offsets, const int32_t* experts, const Weights& w13,
                                   const Weights& w2, int P, int E, int H, int I, int group, void* y, void* ws,
                                   cudaStream_t s) {

@@ -20,6 +20,7 @@ struct Product {
   // complete): tables and weights are read before this kernel's wait, only x is its output
   bool early;
   __nv_bfloat16* out;
+  bool stall = false;  // failure-path self-test only: the issuer first waits for what never comes (w4_tc.cuh)
 };
 
 struct Groups {

@@ -550,7 +550,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
     // ---------------- MMA issuer ----------------
     uint32_t it = 0, half = 0;      // k-block, half tile
     Turn next{0, 0, 0, 0};
-    bool ok = true, ready = false;  // ready: the next operands have been seen
+    bool ready = false;             // the next operands have been seen
+    bool ok = !pr.stall || wait_warp(&sh.last, 0, abort_flag);
     const uint32_t desc_x = (uint32_t)sw128_desc(smem_u32(xs));  // its address field counts 16 bytes
     for (int u = blockIdx.x; ok && u < total; u += units) {
       const Unit un = unit_at(u);
