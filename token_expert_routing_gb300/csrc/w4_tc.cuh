@@ -25,9 +25,10 @@
 // What bounds it.  Many rows: the MMAs (a SwiGLU k-block of 128 rows takes 630 to 650 clocks of MMAs and 850 to 900 in
 // all; the rest is waited for accumulators, token rows and A blocks in turn).  A decode batch: neither the bytes nor the
 // expansion (the ALUs work half of the time, issue slots are two thirds full) but the chain codes, registers, tensor memory,
-// MMA, place free again: with the expansion left out half of the time remains, and a second issuing warp changes nothing.  Measured (GB300, 128 experts of 2048 x 768 or 64 of 2048 x 1408, groups of 128, bf16 scales): 131072 rows
-// through the FFN 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 74 us (4.3 TB/s of weights; 92 with groups of 64 and zero
-// points), 384 rows through one 1408 x 2048 product 34.5 us.
+// MMA, place free again: with the expansion left out half of the time remains, and a second issuing warp changes nothing.
+// Measured (GB300, 128 experts of 2048 x 768 or 64 of 2048 x 1408, groups of 128, bf16 scales): 131072 rows through the FFN
+// 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 74 us (4.3 TB/s of weights; 92 with groups of 64 and zero points), 384 rows
+// through one 1408 x 2048 product 34.5 us.
 // Tried and slower: 24 expansion warps; accumulators split by k-step; a single lane for the issuer's whole loop; decode
 // batches on the warp-level product with codes straight into registers (48.6 us where this takes 34.5, its loads alone 33).
 //
