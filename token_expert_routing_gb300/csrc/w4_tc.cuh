@@ -23,21 +23,23 @@
 // columns, which halves the barriers a weight, else 64, so that more A blocks are on their way.
 //
 // What bounds it.  Many rows: the MMAs (a SwiGLU k-block of 128 rows takes 630 to 650 clocks of MMAs and 850 to 900 in
-// all; the rest is waited for accumulators, token rows and A blocks in turn).  A decode batch: neither the bytes nor the
-// expansion (the ALUs work half of the time, issue slots are two thirds full) but the chain codes, registers, tensor memory,
-// MMA, place free again: with the expansion left out half of the time remains, and a second issuing warp changes nothing.
+// all; the rest is waited for accumulators, token rows and A blocks in turn).  A decode batch: half of the time the
+// expansion's instructions (their count times two clocks, whichever pipe they use), half the chain codes, registers, tensor
+// memory, MMA, place free again; a second issuing warp changes nothing.
 // Measured (GB300, 128 experts of 2048 x 768 or 64 of 2048 x 1408, groups of 128, bf16 scales): 131072 rows through the FFN
-// 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 74 us (4.3 TB/s of weights; 92 with groups of 64 and zero points), 384 rows
-// through one 1408 x 2048 product 34.5 us.
+// 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 72 us (4.4 TB/s of weights; 88 with groups of 64 and zero points, 102 with
+// fp32 scales), 384 rows through one 1408 x 2048 product with zero points 34 us.
 // Tried and slower: 24 expansion warps; accumulators split by k-step; a single lane for the issuer's whole loop; decode
-// batches on the warp-level product with codes straight into registers (48.6 us where this takes 34.5, its loads alone 33).
+// batches on the warp-level product with codes straight into registers (48.6 us where this took 34.5, its loads alone 33).
 //
-// Expansion of a word of eight codes: two masked halves (codes of even and odd columns), then
-// one byte permutation a pair of columns, whose result reads as two bf16 denormals
-// code * 2^-133, and
+// Expansion of a word of eight codes: two masked halves (codes of even columns, and of odd ones as they lie, 16 times
+// as large), then one byte permutation a pair of columns, whose result reads as bf16 numbers: integers below 256 times
+// 2^-133, since the exponents 0 and 1 have the same steps.  Then, factors of odd columns a sixteenth of those of even ones,
 //   without zero points, bf16 scales:  w = code * (s 2^93) - 8 s 2^-40      one fused operation, one rounding
-//   else: d = code * 2^127 - z 2^-6 (exact),  w = d * (s 2^-34), an fp32 scale as the sum of two bf16 numbers, the
+//   with zero points, bf16 scales:  16 - z is added to the codes, four bytes an addition; then the same with 16 s
+//   fp32 scales: d = code * 2^127 - z 2^-6 (exact),  w = d * (s 2^-34) with the scale as the sum of two bf16 numbers, the
 //   smaller product first
+// That is 10, 13 and 18 instructions a word, and each of them adds some 3 us to the FFN of 384 rows below.
 // so a weight is held as w 2^-40 (the sums are multiplied by 2^40), rounded once to bf16: at most half a
 // step off, as in any bf16 copy of the weights.
 //
@@ -167,17 +169,22 @@ __device__ __forceinline__ uint32_t both(float v) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ uint32_t pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // What a group's codes are expanded with.
 struct Factors {
   uint32_t f[3];
 };
 template <int MODE>
 __device__ __forceinline__ Factors factors(float s, uint32_t z) {
-  constexpr float k93 = 9903520314283042199192993792.0f, k40 = 9.094947017729282379150390625e-13f,
+  constexpr float k93 = 9903520314283042199192993792.0f, k89 = k93 / 16, k40 = 9.094947017729282379150390625e-13f,
                   k34 = 5.82076609134674072265625e-11f;  // 2^93, 2^-40, 2^-34
-  if (MODE == SYM) return Factors{{both(s * k93), both(-8.0f * k40 * s), 0u}};
+  if (MODE == SYM) return Factors{{pair(s * k93, s * k89), both(-8.0f * k40 * s), 0u}};
+  if (MODE == ZEROS) return Factors{{both(s * k93), both(-16.0f * k40 * s), (16u - (z & 15u)) * 0x01010101u}};
   const uint32_t zero = both(-0.015625f * (float)(z & 15u));
-  if (MODE == ZEROS) return Factors{{zero, both(s * k34), 0u}};
   const float hi = __bfloat162float(__float2bfloat16_rn(s)), rest = s - hi;
   return Factors{{zero, both(hi * k34), both(rest == rest ? rest * k34 : 0.0f)}};  // (an infinite scale has no rest)
 }
@@ -185,16 +192,17 @@ __device__ __forceinline__ Factors factors(float s, uint32_t z) {
 // The eight codes of a word as bf16 weights, in column order.
 template <int MODE>
 __device__ __forceinline__ void expand(uint32_t w, const Factors& f, uint32_t* r) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+  uint32_t even = w & 0x0f0f0f0fu, odd = w & 0xf0f0f0f0u;
+  if (MODE == ZEROS) even += f.f[2], odd = (odd >> 4) + f.f[2];  // code - z + 16, 1 to 31 in each byte
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
-    uint32_t q;  // byte i of each, with its sign bit's copies, 0, above
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(even), "r"(odd), "r"(i | ((8 + i) << 4) | ((4 + i) << 8) | ((12 + i) << 12)));
-    if (MODE == SYM) {
+    uint32_t q;  // byte i of each, with copies of the even one's sign bit, 0, above
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(even), "r"(odd), "r"(i | ((8 + i) << 4) | ((4 + i) << 8) | ((8 + i) << 12)));
+    if (MODE != F32) {
       r[i] = fma_bf16x2(q, f.f[0], f.f[1]);
     } else {
-      const uint32_t d = fma_bf16x2(q, 0x7f007f00u, f.f[0]);
-      r[i] = MODE == ZEROS ? mul_bf16x2(d, f.f[1]) : fma_bf16x2(d, f.f[1], mul_bf16x2(d, f.f[2]));
+      const uint32_t d = fma_bf16x2(q, 0x7d007f00u, f.f[0]);
+      r[i] = fma_bf16x2(d, f.f[1], mul_bf16x2(d, f.f[2]));
     }
   }
 }
