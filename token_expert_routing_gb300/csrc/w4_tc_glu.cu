@@ -7,9 +7,6 @@ int w4_tc_glu_take_errors(cudaStream_t s, int* bits) { return take_error_word(g_
 
 cudaError_t launch_w4_tc_glu(const w4::Product& pr, cudaStream_t s) {
   const int rows = pr.P / (pr.E < pr.P ? pr.E : pr.P);  // of a group, on average
-#ifdef W4_ROWS
-  return launch_mode<true, W4_ROWS <= 128 ? W4_ROWS : 128>(pr, s);
-#endif
   if (rows <= 24) return launch_mode<true, 32>(pr, s);
   return rows <= 48 ? launch_mode<true, 64>(pr, s) : launch_mode<true, 128>(pr, s);
 }

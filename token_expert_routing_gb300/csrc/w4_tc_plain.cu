@@ -7,9 +7,6 @@ int w4_tc_plain_take_errors(cudaStream_t s, int* bits) { return take_error_word(
 
 cudaError_t launch_w4_tc_plain(const w4::Product& pr, cudaStream_t s) {
   const int rows = pr.P / (pr.E < pr.P ? pr.E : pr.P);  // of a group, on average
-#ifdef W4_ROWS
-  return launch_mode<false, W4_ROWS>(pr, s);
-#endif
   if (rows <= 24) return launch_mode<false, 32>(pr, s);
   if (rows <= 48) return launch_mode<false, 64>(pr, s);
   return rows <= 96 ? launch_mode<false, 128>(pr, s) : launch_mode<false, 256>(pr, s);
