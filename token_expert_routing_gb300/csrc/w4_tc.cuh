@@ -32,14 +32,15 @@
 // Tried and slower: 24 expansion warps; accumulators split by k-step; a single lane for the issuer's whole loop; decode
 // batches on the warp-level product with codes straight into registers (48.6 us where this took 34.5, its loads alone 33).
 //
-// Expansion of a word of eight codes: two masked halves (codes of even columns, and of odd ones as they lie, 16 times
-// as large), then one byte permutation a pair of columns, whose result reads as bf16 numbers: integers below 256 times
-// 2^-133, since the exponents 0 and 1 have the same steps.  Then, factors of odd columns a sixteenth of those of even ones,
+// Expansion of a word of eight codes: two masked halves (codes of even columns, and of odd ones, shifted or as they lie, 16
+// times as large), then one byte permutation a pair of columns, whose result reads as bf16 numbers: integers below 256 times
+// 2^-133, since the exponents 0 and 1 have the same steps.  Then, where odd columns' are 16 times as large with a sixteenth
+// of the factor,
 //   without zero points, bf16 scales:  w = code * (s 2^93) - 8 s 2^-40      one fused operation, one rounding
 //   with zero points, bf16 scales:  16 - z is added to the codes, four bytes an addition; then the same with 16 s
 //   fp32 scales: d = code * 2^127 - z 2^-6 (exact),  w = d * (s 2^-34) with the scale as the sum of two bf16 numbers, the
 //   smaller product first
-// That is 10, 13 and 18 instructions a word, and each of them adds some 3 us to the FFN of 384 rows below.
+// That is 10 (shifted 11), 13 and 18 instructions a word, and each of them adds some 3 us to the FFN of 384 rows below.
 // so a weight is held as w 2^-40 (the sums are multiplied by 2^40), rounded once to bf16: at most half a
 // step off, as in any bf16 copy of the weights.
 //
@@ -174,15 +175,21 @@ __device__ __forceinline__ uint32_t pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// Whether odd columns' codes are shifted into place, or taken where they lie, 16 times as large.  Shifted: with zero points,
+// which need the byte's upper bits, and in units of many rows without them (131072 rows through the FFN 862 us, 872 with the
+// codes where they lie; 384 rows 74.6 and 71.6; fp32 scales 1069 and 1047, 107 and 102).
+template <int MODE, bool FEW>
+constexpr bool shifted() { return MODE == ZEROS || (MODE == SYM && !FEW); }
+
 // What a group's codes are expanded with.
 struct Factors {
   uint32_t f[3];
 };
-template <int MODE>
+template <int MODE, bool FEW>
 __device__ __forceinline__ Factors factors(float s, uint32_t z) {
   constexpr float k93 = 9903520314283042199192993792.0f, k89 = k93 / 16, k40 = 9.094947017729282379150390625e-13f,
                   k34 = 5.82076609134674072265625e-11f;  // 2^93, 2^-40, 2^-34
-  if (MODE == SYM) return Factors{{pair(s * k93, s * k89), both(-8.0f * k40 * s), 0u}};
+  if (MODE == SYM) return Factors{{pair(s * k93, shifted<MODE, FEW>() ? s * k93 : s * k89), both(-8.0f * k40 * s), 0u}};
   if (MODE == ZEROS) return Factors{{both(s * k93), both(-16.0f * k40 * s), (16u - (z & 15u)) * 0x01010101u}};
   const uint32_t zero = both(-0.015625f * (float)(z & 15u));
   const float hi = __bfloat162float(__float2bfloat16_rn(s)), rest = s - hi;
@@ -190,10 +197,10 @@ __device__ __forceinline__ Factors factors(float s, uint32_t z) {
 }
 
 // The eight codes of a word as bf16 weights, in column order.
-template <int MODE>
+template <int MODE, bool FEW>
 __device__ __forceinline__ void expand(uint32_t w, const Factors& f, uint32_t* r) {
-  uint32_t even = w & 0x0f0f0f0fu, odd = w & 0xf0f0f0f0u;
-  if (MODE == ZEROS) even += f.f[2], odd = (odd >> 4) + f.f[2];  // code - z + 16, 1 to 31 in each byte
+  uint32_t even = w & 0x0f0f0f0fu, odd = shifted<MODE, FEW>() ? (w >> 4) & 0x0f0f0f0fu : w & 0xf0f0f0f0u;
+  if (MODE == ZEROS) even += f.f[2], odd += f.f[2];  // code - z + 16, 1 to 31 in each byte
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) {
     uint32_t q;  // byte i of each, with copies of the even one's sign bit, 0, above
@@ -371,7 +378,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
       uint32_t s;
       if (MODE == F32) s = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[NR - 2] : v[NR - 1];
       else s = j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16;
-      return factors<MODE>(__uint_as_float(s), z >> (8 * j));
+      return factors<MODE, SH::few>(__uint_as_float(s), z >> (8 * j));
     };
     // this group's place: unit u, chunk ch of it; its slot of codes and first k-block, counted from the start
     int u = blockIdx.x, ch = GLU ? wg >> 1 : wg;
@@ -419,14 +426,14 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
           fb = fa = factors_of(now, nowz, h);
         }
         uint32_t w[32];
-        expand<MODE>(c[0].x, fa, w);
-        expand<MODE>(c[0].y, fa, w + 4);
-        expand<MODE>(c[0].z, fa, w + 8);
-        expand<MODE>(c[0].w, fa, w + 12);
-        expand<MODE>(c[1].x, fb, w + 16);
-        expand<MODE>(c[1].y, fb, w + 20);
-        expand<MODE>(c[1].z, fb, w + 24);
-        expand<MODE>(c[1].w, fb, w + 28);
+        expand<MODE, SH::few>(c[0].x, fa, w);
+        expand<MODE, SH::few>(c[0].y, fa, w + 4);
+        expand<MODE, SH::few>(c[0].z, fa, w + 8);
+        expand<MODE, SH::few>(c[0].w, fa, w + 12);
+        expand<MODE, SH::few>(c[1].x, fb, w + 16);
+        expand<MODE, SH::few>(c[1].y, fb, w + 20);
+        expand<MODE, SH::few>(c[1].z, fb, w + 24);
+        expand<MODE, SH::few>(c[1].w, fb, w + 28);
         const uint32_t it = it0 + (BK == 64 ? h : 0), place = it % AD;
         if ((BK == 64 || h == 0) && it >= AD) {  // the MMAs that read this place
           if (!(ok = wait_warp(&sh.done[(it - AD) % DONES], ((it - AD) / DONES) & 1, abort_flag))) break;
