@@ -176,7 +176,7 @@ __device__ __forceinline__ uint32_t pair(float lo, float hi) {
 }
 
 // Whether odd columns' codes are shifted into place, or taken where they lie, 16 times as large.  Shifted: with zero points,
-// which need the byte's upper bits, and in units of many rows without them (131072 rows through the FFN 862 us, 872 with the
+// which need the byte's upper bits, and in units of many rows without them (131072 rows through the FFN 862 to 868 us, 872 with the
 // codes where they lie; 384 rows 74.6 and 71.6; fp32 scales 1069 and 1047, 107 and 102).
 template <int MODE, bool FEW>
 constexpr bool shifted() { return MODE == ZEROS || (MODE == SYM && !FEW); }
