@@ -184,26 +184,26 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
   auto load_scales = [&](int kb, Scales& r) {
     const int ch = kb * WK + wk;
     int i0 = GS > 1 ? ch * GS : per > 1 ? ch / per : ch;
-    if (i0 + GS > KG && (whole || i0 >= KG)) i0 = KG - GS;  // a chunk past K: codes and rows are 0
+    if (whole && i0 + GS > KG) i0 = KG - GS;  // a chunk past K: codes and rows are 0
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const S* p = static_cast<const S*>(pr.w.scales) + srow[m][h] + i0;
-        const uint8_t* q = pr.w.zeros + srow[m][h] + i0;
+        const S* p = static_cast<const S*>(pr.w.scales) + srow[m][h];
+        const uint8_t* q = pr.w.zeros + srow[m][h];
         r.z[m][h] = 0x08080808u;
         if (whole) {
-          load_raw<GS * (int)sizeof(S)>(p, r.s[m][h]);
+          load_raw<GS * (int)sizeof(S)>(p + i0, r.s[m][h]);
           if (pr.w.zeros != nullptr) {
-            if (GS == 1) r.z[m][h] = __ldg(q);
-            if (GS == 2) r.z[m][h] = __ldg(reinterpret_cast<const unsigned short*>(q));
-            if (GS == 4) r.z[m][h] = __ldg(reinterpret_cast<const uint32_t*>(q));
+            if (GS == 1) r.z[m][h] = __ldg(q + i0);
+            if (GS == 2) r.z[m][h] = __ldg(reinterpret_cast<const unsigned short*>(q + i0));
+            if (GS == 4) r.z[m][h] = __ldg(reinterpret_cast<const uint32_t*>(q + i0));
           }
-        } else {  // one by one; past K the last one again
+        } else {  // one by one; past K, which a whole chunk may be, the row's last one again
           uint32_t v[GS], z = 0;
 #pragma unroll
           for (int j = 0; j < GS; ++j) {
-            const int o = i0 + j < KG ? j : KG - 1 - i0;
+            const int o = i0 + j < KG ? i0 + j : KG - 1;
             v[j] = sizeof(S) == 4 ? __ldg(reinterpret_cast<const uint32_t*>(p) + o)
                                   : __ldg(reinterpret_cast<const unsigned short*>(p) + o);
             z |= (pr.w.zeros != nullptr ? (uint32_t)__ldg(q + o) : 8u) << (8 * j);
