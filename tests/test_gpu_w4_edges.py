@@ -82,3 +82,26 @@ def test_ffn_reads_its_own_scales(H, I, group, zeros, P, E):
     assert bool(torch.isfinite(y).all())
     assert torch.equal(y, got[0]) and torch.equal(y, got[1])
     assert abi().semmoe_check_errors() == 0
+
+
+@pytest.mark.parametrize("zeros", [True, False], ids=["zeros", "symmetric"])
+@pytest.mark.parametrize("P,E,N", SIZES)
+@pytest.mark.parametrize("group,K", [(32, 96), (32, 160), (32, 512), (64, 704), (128, 640), (128, 1024), (256, 256)])
+def test_an_infinite_scale_of_the_last_group(group, K, P, E, N, zeros):
+    """Codes above the zero point and rows of one sign: the sums are infinite, of the row's sign, wherever the columns end."""
+    rng = np.random.default_rng(K + P)
+    off, pe = split(rng, P, E)
+    code = rng.integers(9, 16, (E, N, K))
+    s = np.exp2(rng.integers(-3, 2, (E, N, K // group)))
+    z = rng.integers(0, 8, (E, N, K // group)) if zeros else None
+    w = oracle.w4_values(code, s, z, group)
+    s[:, 5, -1] = np.inf
+    dev = cuda(pack(code), torch.uint8), cuda(s, torch.float32), None if z is None else cuda(z, torch.uint8)
+    sign = np.where(np.arange(P) % 2, -1, 1)
+    x = rng.integers(1, 3, (P, K)) * sign[:, None].astype(np.float64)
+    out = torch.empty(P, N, dtype=torch.bfloat16, device="cuda")
+    product(cuda(x, torch.bfloat16), dev, off, pe, P, E, N, K, group, out)
+    ref = oracle.bf16_round(oracle.w4_grouped_product(x, w, off, pe))
+    ref[:, 5] = np.inf * sign
+    np.testing.assert_array_equal(np_(out), ref)
+    assert abi().semmoe_check_errors() == 0

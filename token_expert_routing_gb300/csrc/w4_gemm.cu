@@ -181,10 +181,9 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
   struct Scales {
     uint32_t s[MT][2][NR], z[MT][2];
   };
+  // a group past K, as those of a whole chunk may be, has scale 0: its sums are 0, which no scale that is not finite may meet
   auto load_scales = [&](int kb, Scales& r) {
-    const int ch = kb * WK + wk;
-    int i0 = GS > 1 ? ch * GS : per > 1 ? ch / per : ch;
-    if (whole && i0 + GS > KG) i0 = KG - GS;  // a chunk past K: codes and rows are 0
+    const int ch = kb * WK + wk, i0 = GS > 1 ? ch * GS : per > 1 ? ch / per : ch;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -192,20 +191,24 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
         const S* p = static_cast<const S*>(pr.w.scales) + srow[m][h];
         const uint8_t* q = pr.w.zeros + srow[m][h];
         r.z[m][h] = 0x08080808u;
-        if (whole) {
+        if (i0 >= KG) {
+#pragma unroll
+          for (int j = 0; j < NR; ++j) r.s[m][h][j] = 0;
+        } else if (whole) {
           load_raw<GS * (int)sizeof(S)>(p + i0, r.s[m][h]);
           if (pr.w.zeros != nullptr) {
             if (GS == 1) r.z[m][h] = __ldg(q + i0);
             if (GS == 2) r.z[m][h] = __ldg(reinterpret_cast<const unsigned short*>(q + i0));
             if (GS == 4) r.z[m][h] = __ldg(reinterpret_cast<const uint32_t*>(q + i0));
           }
-        } else {  // one by one; past K, which a whole chunk may be, the row's last one again
+        } else {  // one by one
           uint32_t v[GS], z = 0;
 #pragma unroll
           for (int j = 0; j < GS; ++j) {
             const int o = i0 + j < KG ? i0 + j : KG - 1;
             v[j] = sizeof(S) == 4 ? __ldg(reinterpret_cast<const uint32_t*>(p) + o)
                                   : __ldg(reinterpret_cast<const unsigned short*>(p) + o);
+            if (i0 + j >= KG) v[j] = 0;
             z |= (pr.w.zeros != nullptr ? (uint32_t)__ldg(q + o) : 8u) << (8 * j);
           }
           r.z[m][h] = z;

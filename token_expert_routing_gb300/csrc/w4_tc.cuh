@@ -358,12 +358,13 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ 
         }
         return;
       }
-      uint32_t v[4], z = 0;  // scale by scale; past K the last one again (codes and token rows are 0 there)
+      uint32_t v[4], z = 0;  // scale by scale; past K, where token rows are 0, a scale of 0 (an infinite one would give NaN)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = i0 + i < KG ? i0 + i : KG - 1;
         v[i] = MODE == F32 ? __ldg(reinterpret_cast<const uint32_t*>(srow) + j)
                            : __ldg(reinterpret_cast<const unsigned short*>(srow) + j);
+        if (i0 + i >= KG) v[i] = 0;
         if (MODE != SYM) z |= (zrow != nullptr ? (uint32_t)__ldg(zrow + j) : 8u) << (8 * i);
       }
       if (MODE != SYM) rawz = z;
