@@ -556,7 +556,8 @@ int semmoe_norm(const void* x, int dtype, int T, int H, int kind, const void* we
  * gate         [device] [gate_rows,H] gate_dtype (SEMMOE_F32 or SEMMOE_BF16) or NULL (1);
  *              gate_rows 1 (a value per channel) or T (per token and channel)
  * residual     [device] [T,H] dtype, or NULL for none
- * out          [device] [T,H] dtype, which may be the residual's own buffer, but not that of sorted rows or of a gate per channel
+ * out          [device] [T,H] dtype, which may be the residual's own buffer, but not that of sorted rows, of a gate per channel
+ *              or of a gate of another type
  * next_out     [device] [T,H] dtype, apart from every other buffer; NULL if next_kind is SEMMOE_NORM_NONE
  * Limits: H * element size a multiple of 16 and at most 32768; pointers 16-byte aligned; scales finite.
  * A sorted row >= P sets SEMMOE_DEVERR_PAIRS and its slot is skipped.

@@ -564,9 +564,10 @@ int semmoe_combine_norm(const void* y_perm, const int32_t* pair_to_sorted, const
               aligned(next_out, 16),
           "%s: pointers must be 16-byte aligned", fn);
   REQUIRE(aligned(pair_to_sorted, 4) && aligned(topk_w, 4), "%s: misaligned table", fn);
-  // rows of these are read for more than one token
-  REQUIRE((dense || out != y_perm) && (gate == nullptr || (next_out != gate && (gate_rows == T || out != gate))),
-          "%s: out is neither y_perm (unless dense) nor a gate per channel, next_out no gate", fn);
+  // rows of these are read for more than one token, and those of a gate of another type do not lie over out's
+  const bool own_gate = gate_rows == T && gate_dtype == dtype;
+  REQUIRE((dense || out != y_perm) && (gate == nullptr || (next_out != gate && (own_gate || out != gate))),
+          "%s: out is neither y_perm (unless dense) nor a gate per channel or of another type, next_out no gate", fn);
   CHECK_DEVICE(fn);
   const bool wb = w_dtype == SEMMOE_BF16;
   const CombineNorm a{y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P,
