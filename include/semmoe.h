@@ -529,7 +529,7 @@ int semmoe_combine(const void* y_perm, const int32_t* pair_to_sorted, const floa
  *   out[t,h] = (x[t,h] - m) / sqrt(mean_h (x[t,h] - m)^2 + eps) * (weight_offset + weight[h]) + bias[h]
  * in fp32, rounded once.  The pages have no counterpart: models put a norm in front of the layer.
  *
- * x       [device] [T,H] dtype;  out [device] [T,H] dtype, which may be x itself
+ * x       [device] [T,H] dtype;  out [device] [T,H] dtype, which may be x itself (and overlaps nothing otherwise)
  * weight  [device] [H] w_dtype (SEMMOE_F32 or SEMMOE_BF16) or NULL (1; weight_offset is then not used)
  * bias    [device] [H] w_dtype or NULL
  * eps     finite, above 0
@@ -556,8 +556,8 @@ int semmoe_norm(const void* x, int dtype, int T, int H, int kind, const void* we
  * gate         [device] [gate_rows,H] gate_dtype (SEMMOE_F32 or SEMMOE_BF16) or NULL (1);
  *              gate_rows 1 (a value per channel) or T (per token and channel)
  * residual     [device] [T,H] dtype, or NULL for none
- * out          [device] [T,H] dtype, which may be the residual's own buffer, but not that of sorted rows, of a gate per channel
- *              or of a gate of another type
+ * out          [device] [T,H] dtype, which may be the residual's own buffer, that of y_shared, of a dense block's rows or of a
+ *              gate per token of dtype, and overlaps no input otherwise
  * next_out     [device] [T,H] dtype, apart from every other buffer; NULL if next_kind is SEMMOE_NORM_NONE
  * Limits: H * element size a multiple of 16 and at most 32768; pointers 16-byte aligned; scales finite.
  * A sorted row >= P sets SEMMOE_DEVERR_PAIRS and its slot is skipped.

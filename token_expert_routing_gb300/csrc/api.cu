@@ -30,6 +30,11 @@ int cuda_status(cudaError_t e, const char* where) {
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether na bytes from a on and nb from b on share any.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && na > 0 && nb > 0 && (x < y ? y - x < na : x - y < nb);
+}
 bool valid_dtype(int d) { return d == SEMMOE_F32 || d == SEMMOE_BF16; }
 // Router weights may also come as the split of an fp32 weight, for bf16
 // activations with 16-byte rows (the tensor-core router).
@@ -527,6 +532,9 @@ int semmoe_norm(const void* x, int dtype, int T, int H, int kind, const void* we
   if (rc != SEMMOE_OK || T == 0) return rc;
   REQUIRE(x && out, "%s: null pointer", fn);
   REQUIRE(aligned(x, 16) && aligned(out, 16), "%s: pointers must be 16-byte aligned", fn);
+  const size_t bytes = (size_t)T * H * elem_size(dtype), w_bytes = (size_t)H * elem_size(w_dtype);
+  REQUIRE(out == x || !overlap(out, bytes, x, bytes), "%s: out overlaps x", fn);
+  REQUIRE(!overlap(out, bytes, weight, w_bytes) && !overlap(out, bytes, bias, w_bytes), "%s: out overlaps the weight or bias", fn);
   CHECK_DEVICE(fn);
   return cuda_status(launch_norm(x, dtype, T, H, NormArgs{kind, weight, bias, w_dtype == SEMMOE_BF16, weight_offset, eps},
                                  out, static_cast<cudaStream_t>(stream)),
@@ -568,6 +576,28 @@ int semmoe_combine_norm(const void* y_perm, const int32_t* pair_to_sorted, const
   const bool own_gate = gate_rows == T && gate_dtype == dtype;
   REQUIRE((dense || out != y_perm) && (gate == nullptr || (next_out != gate && (own_gate || out != gate))),
           "%s: out is neither y_perm (unless dense) nor a gate per channel or of another type, next_out no gate", fn);
+  // beside those: a thread reads its pieces of a token's rows before it writes them, but those of no other token
+  const size_t bytes = (size_t)T * H * elem_size(dtype), w_bytes = (size_t)H * elem_size(w_dtype);
+  const size_t pairs = dense ? 0 : (size_t)T * k_max * 4;
+  const struct {
+    const char* name;
+    const void* p;
+    size_t n;
+  } in[] = {{"y_perm", y_perm, dense ? bytes : (size_t)P * H * elem_size(dtype)},
+            {"y_shared", y_shared, bytes},
+            {"residual", residual, bytes},
+            {"gate", gate, (size_t)gate_rows * H * elem_size(gate_dtype)},
+            {"pair_to_sorted", pair_to_sorted, pairs},
+            {"topk_w", dense ? nullptr : topk_w, pairs},
+            {"post_weight", post_weight, w_bytes},
+            {"post_bias", post_bias, w_bytes},
+            {"next_weight", next_weight, w_bytes},
+            {"next_bias", next_bias, w_bytes}};
+  for (int i = 0; i < 10; ++i) {
+    REQUIRE((i < 4 && out == in[i].p) || !overlap(out, bytes, in[i].p, in[i].n), "%s: out overlaps %s", fn, in[i].name);
+    REQUIRE(!overlap(next_out, bytes, in[i].p, in[i].n), "%s: next_out overlaps %s", fn, in[i].name);
+  }
+  REQUIRE(!overlap(next_out, bytes, out, bytes), "%s: next_out overlaps out", fn);
   CHECK_DEVICE(fn);
   const bool wb = w_dtype == SEMMOE_BF16;
   const CombineNorm a{y_perm, pair_to_sorted, topk_w, y_shared, T, H, k_max, P,
