@@ -683,7 +683,7 @@ int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dty
  *
  * x       [device] [P,K] bf16
  * codes, scales, zeros  [device] E matrices of N rows
- * out     [device] [P,N] bf16
+ * out     [device] [P,N] bf16, apart from x
  * A weight is used exactly or rounded once to bf16, as the sizes have it; bf16 scales: magnitudes below 2^34;
  * rows' values: below 2^100 (sums of up to 143 x are held on the way).  A scale that is not finite
  * gives infinities or NaN in its row's column of out, and there alone.
@@ -701,8 +701,8 @@ int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const i
  * x       [device] [P,H] bf16
  * w13, w13_scales, w13_zeros  [device] [E,2I,H] (gate rows, then up rows);  w2 ...  [device] [E,H,I]
  *         (both with zeros or both without, one scale_dtype, one group)
- * y_perm  [device] [P,H] bf16 out
- * ws      [device] workspace of semmoe_w4_grouped_ffn_workspace_size() bytes (256-byte aligned)
+ * y_perm  [device] [P,H] bf16 out, which may be x itself
+ * ws      [device] workspace of semmoe_w4_grouped_ffn_workspace_size() bytes (256-byte aligned), apart from x and y_perm
  * Weights and limits as semmoe_w4_grouped_gemm, for N = H and for N = I; H and I multiples of group.  Calls that run at the same
  * time need workspaces of their own.
  */

@@ -822,6 +822,7 @@ int semmoe_w4_grouped_gemm(const void* x, const int32_t* expert_offsets, const i
   const char* fn = "semmoe_w4_grouped_gemm";
   int rc = check_w4_product(fn, x, expert_offsets, phys_to_expert, codes, scales, scale_dtype, zeros, P, E, N, K, group, out);
   if (rc != SEMMOE_OK || P == 0) return rc;
+  REQUIRE(!overlap(out, (size_t)P * N * 2, x, (size_t)P * K * 2), "%s: out overlaps x, of which all columns are read for each of out's", fn);
   CHECK_DEVICE(fn);
   return cuda_status(launch_w4_grouped_gemm(x, expert_offsets, phys_to_expert,
                                             w4::Weights{codes, scales, zeros, scale_dtype == SEMMOE_BF16}, P, E, N, K,
@@ -850,6 +851,8 @@ int semmoe_w4_grouped_ffn(const void* x, const int32_t* expert_offsets, const in
   REQUIRE(aligned(w2, 16) && aligned(w2_scales, 16) && aligned(w2_zeros, 16), "%s: misaligned pointer", fn);
   REQUIRE(ws != nullptr && aligned(ws, 256) && ws_bytes >= w4_ffn_ws_bytes(P, I),
           "%s: workspace null, not 256-byte aligned or below %zu bytes", fn, w4_ffn_ws_bytes(P, I));
+  const size_t rows = (size_t)P * H * 2, h = (size_t)P * I * 2;
+  REQUIRE(!overlap(ws, h, x, rows) && !overlap(ws, h, y_perm, rows), "%s: the workspace overlaps x or y_perm", fn);
   CHECK_DEVICE(fn);
   const bool sb = scale_dtype == SEMMOE_BF16;
   return cuda_status(launch_w4_grouped_ffn(x, expert_offsets, phys_to_expert, w4::Weights{w13, w13_scales, w13_zeros, sb},
