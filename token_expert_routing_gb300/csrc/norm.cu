@@ -8,10 +8,12 @@
 // What bounds them: bytes.  A row stays in registers from its loads to its
 // stores, so every input is read once and y never reaches memory; the squares are taken
 // about the mean in a second sweep over the registers, not as a difference of sums.
+// Norms about the mean have kernels of their own (MEAN, MEANS): one for both would slow the others down (the norm of
+// 16384 x 2048 23.7 us where it takes 22.9, the combine below 137 where it takes 129).
 // A row belongs to one warp while it fits 32 lanes x 4 pieces of 16 bytes, else to one CTA.
-// Measured (GB300, calls of a captured graph): the norm of 16384 x 2048 bf16, 23.0 us (5.8 TB/s); the combine of 8 rows a token
-// with both norms, a gate per channel and the residual, 16384 x 2048 bf16, 134 us (5.5 TB/s); a dense block's row with a gate a
-// token, the residual and one norm, 4096 x 2048 bf16, 16.8 us (5.0 TB/s).
+// Measured (GB300, calls of a captured graph): the norm of 16384 x 2048 bf16, 22.9 us (5.9 TB/s); the combine of 8 rows a token
+// with both norms, a gate per channel and the residual, 16384 x 2048 bf16, 129 us (5.7 TB/s); a dense block's row with a gate a
+// token, the residual and one norm about the mean, 4096 x 2048 bf16, 17.0 us (4.9 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -25,12 +27,13 @@ __device__ __forceinline__ void flag(int bit) { atomicOr(&g_err, bit); }
 constexpr int kWarpRows = 4;     // rows of a CTA whose rows belong to warps
 constexpr int PIECES = 2;        // of 16 bytes a thread, of many rows (more only where a CTA's threads would not do)
 constexpr int RING = 4;          // rows on their way to a row's threads, and the one in use
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;    // of a CTA
 constexpr unsigned kAll = 0xffffffffu;
+static_assert(kMaxWarps == 16, "half of a warp's lanes add up one sum of the warps'");
 
 // Threads of a CTA (plan below), and CTAs that an SM's registers have to hold: as many as come without spills that matter
-// (4 CTAs of the combine's two-piece form 134 us at 16384 x 2048, 3 of them 141, 5 143; 4 of the dense one's 25 us at
-// 4096 x 2048, 3 of them 16.8).
+// (4 CTAs of the combine's two-piece form 129 us at 16384 x 2048, 3 of them 139, 5 142; 4 of the dense one's 27 us at
+// 4096 x 2048, 3 of them 17.0).
 template <bool WARP, int CH>
 constexpr int max_threads() { return WARP ? 32 * kWarpRows : CH == 4 ? 512 : 256; }
 template <bool WARP, int CH>
@@ -66,47 +69,67 @@ __device__ __forceinline__ void load_weights(const void* p, bool bf16, int col, 
 // through shared memory.  Two buffers in turn: a thread writes one again only after
 // the barrier of the reduction between, which every reader of it has reached.
 struct RowReduce {
-  float (*part)[kMaxWarps];
+  float (*part)[2 * kMaxWarps];
   int buf;
+  template <bool MAX>
+  static __device__ __forceinline__ float add(float v, float o) { return MAX ? fmaxf(v, o) : v + o; }
+  // over the warps' values, from `from` on in the buffer; each half of a warp
+  template <bool MAX>
+  __device__ __forceinline__ float warps(int from) {
+    const int n = blockDim.x / 32, j = threadIdx.x % kMaxWarps;
+    float v = j < n ? part[buf][from + j] : 0.f;
+    buf ^= 1;
+#pragma unroll
+    for (int d = kMaxWarps / 2; d > 0; d >>= 1) v = add<MAX>(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
   template <bool WARP, bool MAX>
   __device__ __forceinline__ float run(float v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const float o = __shfl_xor_sync(kAll, v, d);
-      v = MAX ? fmaxf(v, o) : v + o;
-    }
+    for (int d = 16; d > 0; d >>= 1) v = add<MAX>(v, __shfl_xor_sync(kAll, v, d));
     if (WARP) return v;
-    const int n = blockDim.x / 32, lane = threadIdx.x % 32;
-    if (lane == 0) part[buf][threadIdx.x / 32] = v;
+    if (threadIdx.x % 32 == 0) part[buf][threadIdx.x / 32] = v;
     __syncthreads();
-    v = lane < n ? part[buf][lane] : 0.f;
-    buf ^= 1;
+    return warps<MAX>(0);
+  }
+  // two sums at once: half of the lanes add up one, half the other
+  template <bool WARP>
+  __device__ __forceinline__ float2 pair(float x, float y) {
+    const bool up = threadIdx.x & 16;
+    float v = (up ? y : x) + __shfl_xor_sync(kAll, up ? x : y, 16);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const float o = __shfl_xor_sync(kAll, v, d);
-      v = MAX ? fmaxf(v, o) : v + o;
+    for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    if (!WARP) {
+      if (threadIdx.x % 16 == 0) part[buf][(up ? kMaxWarps : 0) + threadIdx.x / 32] = v;
+      __syncthreads();
+      v = warps<false>(up ? kMaxWarps : 0);
     }
-    return v;
+    const float o = __shfl_xor_sync(kAll, v, 16);
+    return up ? make_float2(o, v) : make_float2(v, o);
   }
 };
 
-// What turns a row's values into normalised ones: v * a + b.
+// What turns a row's values into normalised ones: v * a, or (v * scale - mean) * a + b about the mean.
 struct RowStats {
-  float a, b;
+  float scale, mean, a, b;
 };
 
 // Columns past the row's end hold 0 and are left out of the squares about the mean.
+// about_mean: SEMMOE_NORM_LAYER, else SEMMOE_NORM_RMS.
 // A row whose squares (or sum) leave fp32's range -- values past 1e18, or rows all
 // below 1e-15 beside a tiny eps -- is taken again with its values scaled so that its
 // largest magnitude comes to [1, 2); the branch is the same for all its threads.
+// The mean, as a sum in fp32 has it, is off by some steps of the largest value, which may be more than the values
+// differ by.  So the differences from it are summed beside their squares: what they come to on average is taken off each of
+// them, and its square off theirs, and no error of the mean is left but that of numbers as small as the differences.
 template <bool WARP, int CH, int VEC>
-__device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kind, int H, float eps, int col0, int step,
+__device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], bool about_mean, int H, float eps, int col0, int step,
                                               RowReduce& red) {
   const float inv = 1.0f / (float)H;
   float scale = 1.0f, mean = 0.0f;
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
-    if (kind == SEMMOE_NORM_LAYER) {
+    if (about_mean) {
       float s = 0.f;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -114,27 +137,37 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kin
         for (int i = 0; i < VEC; ++i) s += pass ? v[c][i] * scale : v[c][i];
       mean = red.run<WARP, false>(s) * inv;
     }
-    float ss = 0.f;
-    if (pass || kind == SEMMOE_NORM_LAYER) {
+    float ss = 0.f, off = 0.f;  // off: the differences' own mean
+    if (pass || about_mean) {
+      float s = 0.f;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (col0 + c * step < H) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             const float d = fmaf(v[c][i], scale, -mean);
+            s += d;
             ss = fmaf(d, d, ss);
           }
         }
+      }
+      if (about_mean) {
+        const float2 both = red.pair<WARP>(ss, s);
+        ss = both.x, off = both.y * inv;
+      } else {
+        ss = red.run<WARP, false>(ss);
       }
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+      ss = red.run<WARP, false>(ss);
     }
-    ss = red.run<WARP, false>(ss);
-    const float rstd = rsqrtf(fmaf(ss, inv, eps * scale * scale));
-    const RowStats st{scale * rstd, -mean * rstd};
+    float var = fmaf(ss, inv, eps * scale * scale);
+    if (about_mean) var = fmaxf(fmaf(-off, off, var), eps * scale * scale);  // (NaN comes through b)
+    const float rstd = rsqrtf(var);
+    const RowStats st{scale, mean, about_mean ? rstd : scale * rstd, -off * rstd};
     if (pass || ((ss >= 1e-30f || eps >= 1e-20f) && ss <= 1e36f)) return st;
     float m = 0.f;
 #pragma unroll
@@ -151,31 +184,36 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], int kin
 
 // v, normalised by st, times (offset + weight) plus bias.
 template <int VEC>
-__device__ __forceinline__ void apply_norm(float (&v)[VEC], const RowStats& st, const void* weight, const void* bias,
-                                           bool w_bf16, float offset, int col) {
+__device__ __forceinline__ void apply_norm(float (&v)[VEC], const RowStats& st, bool about_mean, const NormArgs& n,
+                                           int col) {
+  if (about_mean) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], st.a, st.b);
-  if (weight != nullptr) {
-    float w[VEC];
-    load_weights(weight, w_bf16, col, w);
+    for (int i = 0; i < VEC; ++i) v[i] = fmaf(fmaf(v[i], st.scale, -st.mean), st.a, st.b);
+  } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] *= offset + w[i];
+    for (int i = 0; i < VEC; ++i) v[i] *= st.a;
   }
-  if (bias != nullptr) {
+  if (n.weight != nullptr) {
+    float w[VEC];
+    load_weights(n.weight, n.w_bf16, col, w);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] *= n.offset + w[i];
+  }
+  if (n.bias != nullptr) {
     float b[VEC];
-    load_weights(bias, w_bf16, col, b);
+    load_weights(n.bias, n.w_bf16, col, b);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] += b[i];
   }
 }
 
 // One row at a time per warp or CTA: the loads of the AHEAD next rows are in flight, in registers, through this row's reductions.
-template <typename T, bool WARP, int CH>
+template <typename T, bool WARP, int CH, bool MEAN>
 __global__ void __launch_bounds__(max_threads<WARP, CH>(), norm_ctas<WARP, CH>())
 norm_kernel(const T* x, int T_, int H, const __grid_constant__ NormArgs n, T* out) {
   using V = Vec16<T>;
   constexpr int VEC = V::N, AHEAD = CH == 1 ? 2 : 1;
-  __shared__ float part[2][kMaxWarps];
+  __shared__ float part[2][2 * kMaxWarps];
   RowReduce red{part, 0};
   pdl_trigger();
   pdl_wait();
@@ -202,12 +240,12 @@ norm_kernel(const T* x, int T_, int H, const __grid_constant__ NormArgs n, T* ou
 #pragma unroll
       for (int c = 0; c < CH; ++c) V::unpack(raw[i][c], v[c]);
       fetch(t + AHEAD * stride, raw[i]);
-      const RowStats st = row_stats<WARP, CH, VEC>(v, n.kind, H, n.eps, col0, step, red);
+      const RowStats st = row_stats<WARP, CH, VEC>(v, MEAN, H, n.eps, col0, step, red);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = col0 + c * step;
         if (col < H) {
-          apply_norm<VEC>(v[c], st, n.weight, n.bias, n.w_bf16, n.offset, col);
+          apply_norm<VEC>(v[c], st, MEAN, n, col);
           V::store(out + (size_t)t * H + col, v[c]);
         }
       }
@@ -218,18 +256,19 @@ norm_kernel(const T* x, int T_, int H, const __grid_constant__ NormArgs n, T* ou
 
 // From the block's row on: norm, gate, residual, the sum's row stored, the next block's norm, its row stored.  `next` comes to
 // the gate's own row (of type T), then the residual's; `piece` reads 16 bytes a thread of it.
-template <typename T, bool WARP, int CH, typename Next, typename Piece>
+template <typename T, bool WARP, int CH, bool MEANS, typename Next, typename Piece>
 __device__ __forceinline__ void finish_row(const CombineNorm& a, long long t, float (&v)[CH][Vec16<T>::N], int col0, int step,
                                            RowReduce& red, bool own_gate, Next&& next, Piece&& piece) {
   using V = Vec16<T>;
   constexpr int VEC = V::N;
   const int H = a.H;
+  const bool mean_post = MEANS && a.post.kind == SEMMOE_NORM_LAYER, mean_next = MEANS && a.next.kind == SEMMOE_NORM_LAYER;
   if (a.post.kind != SEMMOE_NORM_NONE) {
-    const RowStats st = row_stats<WARP, CH, VEC>(v, a.post.kind, H, a.post.eps, col0, step, red);
+    const RowStats st = row_stats<WARP, CH, VEC>(v, mean_post, H, a.post.eps, col0, step, red);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = col0 + c * step;
-      if (col < H) apply_norm<VEC>(v[c], st, a.post.weight, a.post.bias, a.post.w_bf16, a.post.offset, col);
+      if (col < H) apply_norm<VEC>(v[c], st, mean_post, a.post, col);
     }
   }
   if (a.gate != nullptr) {
@@ -267,26 +306,26 @@ __device__ __forceinline__ void finish_row(const CombineNorm& a, long long t, fl
     }
   }
   if (a.next.kind == SEMMOE_NORM_NONE) return;
-  const RowStats st = row_stats<WARP, CH, VEC>(v, a.next.kind, H, a.next.eps, col0, step, red);
+  const RowStats st = row_stats<WARP, CH, VEC>(v, mean_next, H, a.next.eps, col0, step, red);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = col0 + c * step;
     if (col < H) {
-      apply_norm<VEC>(v[c], st, a.next.weight, a.next.bias, a.next.w_bf16, a.next.offset, col);
+      apply_norm<VEC>(v[c], st, mean_next, a.next, col);
       V::store(static_cast<T*>(a.next_out) + (size_t)t * H + col, v[c]);
     }
   }
 }
 
 // A dense block's row (no slots).  A token needs the same two or three rows each time, so they need no list and no ring: their
-// next pieces are fetched into registers as soon as this token's have been used (16.8 us at 4096 x 2048 bf16, 23.9 through
+// next pieces are fetched into registers as soon as this token's have been used (17.0 us at 4096 x 2048 bf16, 23.9 through
 // the ring below).  A shared row, which a dense block seldom has, is read where it is added.
-template <typename T, bool WARP, int CH>
+template <typename T, bool WARP, int CH, bool MEANS>
 __global__ void __launch_bounds__(max_threads<WARP, CH>(), dense_ctas<WARP, CH>())
 dense_norm_kernel(const __grid_constant__ CombineNorm a) {
   using V = Vec16<T>;
   constexpr int VEC = V::N;
-  __shared__ float part[2][kMaxWarps];
+  __shared__ float part[2][2 * kMaxWarps];
   RowReduce red{part, 0};
   pdl_trigger();
   pdl_wait();
@@ -328,7 +367,7 @@ dense_norm_kernel(const __grid_constant__ CombineNorm a) {
         }
       }
     }
-    finish_row<T, WARP, CH>(
+    finish_row<T, WARP, CH, MEANS>(
         a, t, v, col0, step, red, gate_rows != nullptr, [&](bool) { return 0; },
         [&](bool gate, int, int c, float (&r)[VEC]) {
           uint4& mine = gate ? raw[1][c] : raw[2][c];
@@ -356,13 +395,13 @@ struct Token {
 // waited for but its own copies.
 // Lane j of each warp reads slot j's sorted row and gate, one token ahead of the copies (up to 32 slots; the ones behind
 // are read where they are used).
-template <typename T, bool WARP, int CH>
+template <typename T, bool WARP, int CH, bool MEANS>
 __global__ void __launch_bounds__(max_threads<WARP, CH>(), min_ctas<WARP, CH>())
 combine_norm_kernel(const __grid_constant__ CombineNorm a) {
   using V = Vec16<T>;
   constexpr int VEC = V::N;
   extern __shared__ uint4 ring[];  // [RING][CH][threads], then the lists of RING tokens a warp
-  __shared__ float part[2][kMaxWarps];
+  __shared__ float part[2][2 * kMaxWarps];
   RowReduce red{part, 0};
   pdl_trigger();
   pdl_wait();
@@ -511,7 +550,7 @@ combine_norm_kernel(const __grid_constant__ CombineNorm a) {
         for (int i = 0; i < VEC; ++i) v[c][i] = 0.f;
       }
     }
-    finish_row<T, WARP, CH>(
+    finish_row<T, WARP, CH, MEANS>(
         a, t, v, col0, step, red, own_gate, [&](bool) { return next_item(); },
         [&](bool, int at, int c, float (&r)[VEC]) { values(at, c, r); });
   }
@@ -523,8 +562,8 @@ struct RowPlan {
   bool warp;
   int pieces, threads;
 };
-// Many rows: two pieces a thread, so that reductions and loop are shared by more bytes (the combine of 16384 x 2048 takes 169 us
-// with one piece and 134 with two; four mean fewer warps at a time).  Few rows, whose time is one row's: as many threads as
+// Many rows: two pieces a thread, so that reductions and loop are shared by more bytes (the combine of 16384 x 2048 takes 166 us
+// with one piece and 129 with two; four mean fewer warps at a time).  Few rows, whose time is one row's: as many threads as
 // there are pieces.
 RowPlan plan(int H, int vec, int T) {
   const int n = ceil_div(H, vec);
@@ -550,17 +589,18 @@ int ctas_per_sm(const RowPlan& p, int by_bounds, int bound_threads, int smem) {
 template <typename T, bool WARP, int CH>
 cudaError_t launch_norm_t(const RowPlan& p, const void* x, int T_, int H, const NormArgs& n, void* out, cudaStream_t s) {
   const int per_sm = ctas_per_sm(p, norm_ctas<WARP, CH>(), max_threads<WARP, CH>(), 0);
-  return launch_kernel(norm_kernel<T, WARP, CH>, dim3(resident_grid(p, T_, per_sm)), dim3(p.threads), 0, s, 1, true,
-                       static_cast<const T*>(x), T_, H, n, static_cast<T*>(out));
+  auto kern = n.kind == SEMMOE_NORM_LAYER ? norm_kernel<T, WARP, CH, true> : norm_kernel<T, WARP, CH, false>;
+  return launch_kernel(kern, dim3(resident_grid(p, T_, per_sm)), dim3(p.threads), 0, s, 1, true, static_cast<const T*>(x), T_, H,
+                       n, static_cast<T*>(out));
 }
 
-template <typename T, bool WARP, int CH>
+template <typename T, bool WARP, int CH, bool MEANS>
 cudaError_t launch_t(const RowPlan& p, const CombineNorm& a, cudaStream_t s) {
   if (a.pair_to_sorted == nullptr) {
     const int n = ctas_per_sm(p, dense_ctas<WARP, CH>(), max_threads<WARP, CH>(), 0);
-    return launch_kernel(dense_norm_kernel<T, WARP, CH>, dim3(resident_grid(p, a.T, n)), dim3(p.threads), 0, s, 1, true, a);
+    return launch_kernel(dense_norm_kernel<T, WARP, CH, MEANS>, dim3(resident_grid(p, a.T, n)), dim3(p.threads), 0, s, 1, true, a);
   }
-  auto kern = combine_norm_kernel<T, WARP, CH>;
+  auto kern = combine_norm_kernel<T, WARP, CH, MEANS>;
   const int smem = RING * (CH * p.threads * 16 + p.threads / 32 * (int)sizeof(Token));
   static std::atomic<unsigned long long> smem_set{0};
   cudaError_t e = ensure_smem_limit(kern, RING * (CH * max_threads<WARP, CH>() * 16 + max_threads<WARP, CH>() / 32 * (int)sizeof(Token)), smem_set);
@@ -594,7 +634,9 @@ cudaError_t launch_combine_norm(const CombineNorm& a, int dtype, cudaStream_t s)
   cudaError_t e = by_plan(p, [&](auto warp, auto ch) {
     constexpr bool W = decltype(warp)::value;
     constexpr int C = decltype(ch)::value;
-    return dtype == SEMMOE_BF16 ? launch_t<__nv_bfloat16, W, C>(p, a, s) : launch_t<float, W, C>(p, a, s);
+    if (a.post.kind == SEMMOE_NORM_LAYER || a.next.kind == SEMMOE_NORM_LAYER)
+      return dtype == SEMMOE_BF16 ? launch_t<__nv_bfloat16, W, C, true>(p, a, s) : launch_t<float, W, C, true>(p, a, s);
+    return dtype == SEMMOE_BF16 ? launch_t<__nv_bfloat16, W, C, false>(p, a, s) : launch_t<float, W, C, false>(p, a, s);
   });
   if (e != cudaSuccess) return e;
   count_launches(1);
