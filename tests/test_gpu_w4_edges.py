@@ -105,3 +105,28 @@ def test_an_infinite_scale_of_the_last_group(group, K, P, E, N, zeros):
     ref[:, 5] = np.inf * sign
     np.testing.assert_array_equal(np_(out), ref)
     assert abi().semmoe_check_errors() == 0
+
+
+@pytest.mark.parametrize("zeros", [True, False], ids=["zeros", "symmetric"])
+@pytest.mark.parametrize("scale", ["bf16", "f32"])
+@pytest.mark.parametrize("P,E,N", SIZES)
+@pytest.mark.parametrize("group,K", [(32, 96), (32, 352), (64, 704), (128, 640), (128, 2048), (256, 1024)])
+def test_large_values_on_weights_of_zero(group, K, P, E, N, scale, zeros):
+    """Rows with values of 2^22 in columns whose codes are the zero point: weights of 0, whatever the value, so the sums stay
+    those of the other columns, whole numbers below 2^24."""
+    rng = np.random.default_rng(K + P)
+    off, pe = split(rng, P, E)
+    code = rng.integers(0, 16, (E, N, K))
+    z = rng.integers(0, 16, (E, N, K // group)) if zeros else None
+    s = np.ones((E, N, K // group))
+    large = [1, K // 2, K - 3]
+    for c in large:
+        code[:, :, c] = 8 if z is None else z[:, :, c // group]
+    w = oracle.w4_values(code, s, z, group)
+    x = rng.integers(-4, 5, (P, K)).astype(np.float64)
+    x[:, large] = 2.0 ** 22 * rng.choice([-1, 1, 0.75], (P, len(large)))
+    dev = cuda(pack(code), torch.uint8), cuda(s, DT[scale]), None if z is None else cuda(z, torch.uint8)
+    out = torch.empty(P, N, dtype=torch.bfloat16, device="cuda")
+    product(cuda(x, torch.bfloat16), dev, off, pe, P, E, N, K, group, out)
+    np.testing.assert_array_equal(np_(out), oracle.bf16_round(oracle.w4_grouped_product(x, w, off, pe)))
+    assert abi().semmoe_check_errors() == 0

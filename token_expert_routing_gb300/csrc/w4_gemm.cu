@@ -12,13 +12,13 @@
 // columns by asynchronous copies, STAGES - 1 of them in flight, across the ends of units.
 // A lane's word of eight codes gives the A operands of two products as they lie: bits 0-3
 // and 16-19 (columns 0, 4), 4-7 and 20-23 (1, 5), and so on; the row's eight values are
-// put into that order instead.  A code enters as 128 + code, one masked OR, and the sums of a group of
-// columns are put right at its end: s (sum (128 + code) x - (128 + z) sum x), with sum x from one more product,
-// whose weights are ones.
-// No weight is rounded: codes, zero points and the rows' values are exact in bf16, the sums fp32.
+// put into that order instead.  A code is made bf16 as 128 + code, one masked OR, and 128 + z is subtracted from a pair of
+// them at once, exactly; the scale is applied to the sums of its group of columns.
+// No weight is rounded: code - z and the rows' values are exact in bf16, the sums fp32.  (Sums of (128 + code) x, put right by
+// the sum of x at a group's end, took as long, and lost what large values on weights of 0 left of the others.)
 // What bounds it: a few microseconds of latency, the tables, the first codes and the unit's end one after the other; the weights
-// of one token take 0.3 to 3 us.  Measured (GB300, calls of a captured graph): one row by 2048 x 2048 4.3 us, by 8192 x 2048 5.8 us;
-// one token through 8 of 128 experts of 2048 x 768 14.1 us, through 6 of 64 of 2048 x 1408 15.9 us (20 us for the first before the
+// of one token take 0.3 to 3 us.  Measured (GB300, calls of a captured graph): one row by 2048 x 2048 4.3 us, by 8192 x 2048 5.7 us;
+// one token through 8 of 128 experts of 2048 x 768 14.3 us, through 6 of 64 of 2048 x 1408 16.6 us (20 us for the first before the
 // second product read its tables and codes while the first one ends).
 #include "common.cuh"
 #include "internal.h"
@@ -70,6 +70,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 // BYTES (2, 4, 8 or 16) that lie together, aligned to their size.
 template <int BYTES>
@@ -219,7 +224,7 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
     if (sizeof(S) == 4) return __uint_as_float(r.s[m][h][j % NR]);
     return __uint_as_float(j & 1 ? r.s[m][h][j / 2 % NR] & 0xffff0000u : r.s[m][h][j / 2 % NR] << 16);
   };
-  auto zero_of = [&](const Scales& r, int m, int h, int j) { return 128.0f + (float)((r.z[m][h] >> (8 * j)) & 15u); };
+  auto zero_of = [&](const Scales& r, int m, int h, int j) { return ((r.z[m][h] >> (8 * j)) & 15u) * 0x00010001u | 0x43004300u; };
 
   int u = blockIdx.x;
   if (u >= total) {
@@ -268,7 +273,7 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
     const uint32_t off = stage * STAGE_BYTES;
     const int left = K - (kb * BK + wk * CHUNK);  // columns from this chunk's first one on
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    float part[MT][4], xsum[4];
+    float part[MT][4];
 #pragma unroll
     for (int jp = 0; jp < 2; ++jp) {
       uint32_t w[MT][4];
@@ -281,23 +286,20 @@ w4_rows_kernel(const __grid_constant__ Product pr) {
         const uint4 v = lds128(x_at + off + ((64 * j) ^ x_turn));
         const uint32_t b[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                                __byte_perm(v.y, v.w, 0x7632)};
-        constexpr uint32_t one = 0x3f803f80u;
-        if (first) mma(xsum, one, one, one, one, b[0], b[1], zero);
-        else mma(xsum, one, one, one, one, b[0], b[1], xsum);
-        mma(xsum, one, one, one, one, b[2], b[3], xsum);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const uint32_t lo = w[m][2 * h], hi = w[m][2 * h + 1];
-          if (first) mma(part[m], code_pair(lo, 0), code_pair(hi, 0), code_pair(lo, 4), code_pair(hi, 4), b[0], b[1], zero);
-          else mma(part[m], code_pair(lo, 0), code_pair(hi, 0), code_pair(lo, 4), code_pair(hi, 4), b[0], b[1], part[m]);
-          mma(part[m], code_pair(lo, 8), code_pair(hi, 8), code_pair(lo, 12), code_pair(hi, 12), b[2], b[3], part[m]);
+          const uint32_t lo = w[m][2 * h], hi = w[m][2 * h + 1], zl = zero_of(sc, m, 0, gi), zh = zero_of(sc, m, 1, gi);
+          auto weight = [](uint32_t c, int sh, uint32_t z) { return sub_bf16x2(code_pair(c, sh), z); };
+          if (first) mma(part[m], weight(lo, 0, zl), weight(hi, 0, zh), weight(lo, 4, zl), weight(hi, 4, zh), b[0], b[1], zero);
+          else mma(part[m], weight(lo, 0, zl), weight(hi, 0, zh), weight(lo, 4, zl), weight(hi, 4, zh), b[0], b[1], part[m]);
+          mma(part[m], weight(lo, 8, zl), weight(hi, 8, zh), weight(lo, 12, zl), weight(hi, 12, zh), b[2], b[3], part[m]);
           if (end) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // a group past K has scale 0: its sums are 0, which an infinite scale would make NaN.  (Put in here rather than at
-              // the loads, which it would delay: one token through 8 of 128 experts 14.2 us, 14.1 without and 14.9 there.)
+              // the loads, which it would delay: one token through 8 of 128 experts 14.3 us here, 14.9 there.)
               const float s = gi * (CHUNK / GS) < left ? scale_of(sc, m, i / 2, gi) : 0.f;
-              acc[m][i] = fmaf(s, fmaf(-zero_of(sc, m, i / 2, gi), xsum[i], part[m][i]), acc[m][i]);
+              acc[m][i] = fmaf(s, part[m][i], acc[m][i]);
             }
           }
         }
@@ -356,7 +358,7 @@ cudaError_t launch_rows(Product pr, cudaStream_t s) {
 template <bool GLU>
 cudaError_t launch_product(const Product& pr, cudaStream_t s) {
   // A few rows, whose 128-row weight tiles would not fill the SMs, by this file's kernel (the other one takes 8.1 us for one row by
-  // 2048 x 2048, this one 4.3; 18.4 and 14.1 for one token through 8 of 128 experts of 768), all else on the tensor cores' own
+  // 2048 x 2048, this one 4.3; 18.4 and 14.3 for one token through 8 of 128 experts of 768), all else on the tensor cores' own
   // path (384 rows through 64 matrices of 1408 x 2048: 34.6 us, 51.6 here).
   const int used = pr.E < pr.P ? pr.E : pr.P;
   if (pr.P > (long long)NB * used || (long long)used * ((pr.N + 127) / 128) >= sm_count())
