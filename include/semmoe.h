@@ -685,8 +685,9 @@ int semmoe_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dty
  * codes, scales, zeros  [device] E matrices of N rows
  * out     [device] [P,N] bf16, apart from x
  * A weight is used exactly or rounded once to bf16, as the sizes have it; bf16 scales: magnitudes below 2^34;
- * rows' values: below 2^100 (sums of up to 15 K x are held on the way).  A scale that is not finite
- * gives infinities or NaN in its row's column of out, and there alone.
+ * rows' values: below 2^100 (sums of up to 15 K x are held on the way); weights below 2^-80 and products
+ * x w below 2^-86 may lose bits.  A scale that is not finite gives infinities or NaN in its row's column
+ * of out, and there alone.
  * Limits: N % 8 == 0, 1 <= E <= 256, (P / 8 + E) ceil(N / 16) <= 2^31 - 2^16.  Device checks as semmoe_grouped_ffn (a
  * group that is skipped leaves its rows of out as they were).
  */

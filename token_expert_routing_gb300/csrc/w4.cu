@@ -1,5 +1,7 @@
 // 4-bit weights with group scales (w4.cuh): quantisation and the values that
-// codes stand for.  Both are load-time steps, bound by the full-size side's bytes.
+// codes stand for.  Load-time steps, of simple form: bound by their small loads and stores (and the quantiser's divisions),
+// not by bytes.  Measured (GB300, 262144 x 768, bf16 scales): from bf16 in groups of 128 262 us (1.9 TB/s), of 32 with zero points
+// 451 (1.2); from fp32 262 and 442; back to bf16 436 and 481 us (1.2 and 1.1 TB/s), to fp32 617 and 665.
 #include "common.cuh"
 #include "internal.h"
 #include "w4.cuh"

@@ -1,4 +1,4 @@
-// What the grouped products of 4-bit weights multiply, and how their rows are split (w4_gemm.cu, w4_tc.cu).
+// What the grouped products of 4-bit weights multiply, and how their rows are split (w4_gemm.cu, w4_tc.cuh).
 #pragma once
 
 #include "common.cuh"

@@ -27,7 +27,7 @@
 // expansion's instructions (their count times two clocks, whichever pipe they use), half the chain codes, registers, tensor
 // memory, MMA, place free again; a second issuing warp changes nothing.
 // Measured (GB300, 128 experts of 2048 x 768 or 64 of 2048 x 1408, groups of 128, bf16 scales): 131072 rows through the FFN
-// 860 to 940 us (1.3 to 1.4 PFLOP/s), 384 rows 72 us (4.4 TB/s of weights; 88 with groups of 64 and zero points, 102 with
+// 923 to 939 us in a captured graph (1.3 PFLOP/s; 860 between flushes of L2, before the power cap), 384 rows 72 us (4.4 TB/s of weights; 88 with groups of 64 and zero points, 102 with
 // fp32 scales), 384 rows through one 1408 x 2048 product with zero points 34 us.
 // Tried and slower: 24 expansion warps; accumulators split by k-step; a single lane for the issuer's whole loop; decode
 // batches on the warp-level product with codes straight into registers (48.6 us where this took 34.5, its loads alone 33).
@@ -40,9 +40,9 @@
 //   with zero points, bf16 scales:  16 - z is added to the codes, four bytes an addition; then the same with 16 s
 //   fp32 scales: d = code * 2^127 - z 2^-6 (exact),  w = d * (s 2^-34) with the scale as the sum of two bf16 numbers, the
 //   smaller product first
-// That is 10 (shifted 11), 13 and 18 instructions a word, and each of them adds some 3 us to the FFN of 384 rows below.
-// so a weight is held as w 2^-40 (the sums are multiplied by 2^40), rounded once to bf16: at most half a
-// step off, as in any bf16 copy of the weights.
+// So a weight is held as w 2^-40 (the sums are multiplied by 2^40), rounded once to bf16: at most half a
+// step off, as in any bf16 copy of the weights (with fp32 scales 2^-17 of it more, as two bf16 numbers hold the scale to 2^-18).
+// That is 10 (shifted 11), 13 and 18 instructions a word, and each of them adds some 3 us to the FFN of 384 rows above.
 //
 // Every wait is bounded; a wait that runs out sets the timeout bit of the device error
 // word and an abort flag, after which every role stops, loads and MMAs in flight are
@@ -165,15 +165,11 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t both(float v) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(v, v);
-  return *reinterpret_cast<const uint32_t*>(&b);
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-__device__ __forceinline__ uint32_t pair(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
+__device__ __forceinline__ uint32_t both(float v) { return pack_bf16x2(v, v); }
 
 // Whether odd columns' codes are shifted into place, or taken where they lie, 16 times as large.  Shifted: with zero points,
 // which need the byte's upper bits, and in units of many rows without them (131072 rows through the FFN 862 to 868 us, 872 with the
@@ -189,7 +185,7 @@ template <int MODE, bool FEW>
 __device__ __forceinline__ Factors factors(float s, uint32_t z) {
   constexpr float k93 = 9903520314283042199192993792.0f, k89 = k93 / 16, k40 = 9.094947017729282379150390625e-13f,
                   k34 = 5.82076609134674072265625e-11f;  // 2^93, 2^-40, 2^-34
-  if (MODE == SYM) return Factors{{pair(s * k93, shifted<MODE, FEW>() ? s * k93 : s * k89), both(-8.0f * k40 * s), 0u}};
+  if (MODE == SYM) return Factors{{pack_bf16x2(s * k93, shifted<MODE, FEW>() ? s * k93 : s * k89), both(-8.0f * k40 * s), 0u}};
   if (MODE == ZEROS) return Factors{{both(s * k93), both(-16.0f * k40 * s), (16u - (z & 15u)) * 0x01010101u}};
   const uint32_t zero = both(-0.015625f * (float)(z & 15u));
   const float hi = __bfloat162float(__float2bfloat16_rn(s)), rest = s - hi;
@@ -262,10 +258,6 @@ __device__ __forceinline__ void store_pairs(const uint32_t (&v)[N], __nv_bfloat1
     asm volatile("{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %0, %3;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(mine),
                  "l"(first + 2 * i * stride), "r"(out[i]), "r"(2 * i)
                  : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <bool GLU, int ROWS, int MODE>
