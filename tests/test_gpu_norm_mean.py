@@ -73,3 +73,47 @@ def test_norms_of_a_combine_far_from_zero(T, H, maps):
     assert torch.equal(out, x)
     close(nxt, ref, err)
     assert abi().semmoe_check_errors() == 0
+
+
+CONSTANTS = [1e-40, 1e-20, 0.1, 100.0, 1234.5, -123456.7, 1e19, -3.3e25, 1e30, 3e38]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", SHAPES + [(20, 16384 // 2)])
+def test_constant_rows_are_zeros(T, H, dtype):
+    """The differences from the mean that fp32 has are equal and at most SUMS steps of the value, so their sum (below 2^24 such
+    steps) and its quotient by H are exact, and what is left is 0: the output is the bias."""
+    if dtype == torch.bfloat16:
+        H -= H % 8
+    x = cuda(np.resize(CONSTANTS, (T, 1)) * np.ones((1, H)), dtype)
+    bias = cuda(np.random.default_rng(H).standard_normal(H), dtype)
+    out, nxt = torch.empty_like(x), torch.empty_like(x)
+    abi().semmoe_norm(x, T, H, LAYER, None, bias, 0.0, 1e-6, out)
+    assert torch.equal(out, bias.expand(T, H))
+    abi().semmoe_combine_norm(x, None, None, None, T, H, 0, T, LAYER, None, bias, 0, None, None, 0.0, 1e-6, None, 0, 1.0, None, 1.0,
+                              out)
+    assert torch.equal(out, bias.expand(T, H))
+    zero = torch.zeros_like(x)
+    abi().semmoe_combine_norm(zero, None, None, None, T, H, 0, T, 0, None, None, LAYER, None, bias, 0.0, 1e-6, None, 0, 1.0, x, 1.0,
+                              out, nxt)
+    assert torch.equal(out, x) and torch.equal(nxt, bias.expand(T, H))
+    assert abi().semmoe_check_errors() == 0
+
+
+@pytest.mark.parametrize("value", [1e4, 1e19, 1e30, 3e38])
+@pytest.mark.parametrize("H", [64, 136, 520])
+def test_one_value_a_step_beside_the_others(H, value):
+    """Differences are k and k + 1 steps, |k| <= SUMS: sums exact, the variance (1 - 1 / H) / H of a step's square but for three
+    roundings of k^2, and the mean's rest off by one rounding of k."""
+    T, eps = 9, 1e-30
+    x = np.full((T, H), np.float32(value))
+    at = np.arange(T) * (H // T)
+    x[np.arange(T), at] = np.nextafter(np.float32(value), np.float32(np.inf))
+    out = torch.empty(T, H, device="cuda")
+    abi().semmoe_norm(cuda(x, torch.float32), T, H, LAYER, None, None, 0.0, eps, out)
+    ref = np.full((T, H), -1 / np.sqrt(H - 1))
+    ref[np.arange(T), at] = np.sqrt(H - 1)
+    rho = 3 * U * SUMS ** 2 * H
+    assert rho < 0.5
+    assert (np.abs(np_(out) - ref) <= rho * np.abs(ref) + SUMS * U * np.sqrt(H)).all()
+    assert abi().semmoe_check_errors() == 0

@@ -13,7 +13,7 @@
 // A row belongs to one warp while it fits 32 lanes x 4 pieces of 16 bytes, else to one CTA.
 // Measured (GB300, calls of a captured graph): the norm of 16384 x 2048 bf16, 22.9 us (5.9 TB/s); the combine of 8 rows a token
 // with both norms, a gate per channel and the residual, 16384 x 2048 bf16, 129 us (5.7 TB/s); a dense block's row with a gate a
-// token, the residual and one norm about the mean, 4096 x 2048 bf16, 17.0 us (4.9 TB/s).
+// token, the residual and one norm about the mean, 4096 x 2048 bf16, 17.1 us (4.9 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -33,7 +33,7 @@ static_assert(kMaxWarps == 16, "half of a warp's lanes add up one sum of the war
 
 // Threads of a CTA (plan below), and CTAs that an SM's registers have to hold: as many as come without spills that matter
 // (4 CTAs of the combine's two-piece form 129 us at 16384 x 2048, 3 of them 139, 5 142; 4 of the dense one's 27 us at
-// 4096 x 2048, 3 of them 17.0).
+// 4096 x 2048, 3 of them 17.1).
 template <bool WARP, int CH>
 constexpr int max_threads() { return WARP ? 32 * kWarpRows : CH == 4 ? 512 : 256; }
 template <bool WARP, int CH>
@@ -121,7 +121,9 @@ struct RowStats {
 // largest magnitude comes to [1, 2); the branch is the same for all its threads.
 // The mean, as a sum in fp32 has it, is off by some steps of the largest value, which may be more than the values
 // differ by.  So the differences from it are summed beside their squares: what they come to on average is taken off each of
-// them, and its square off theirs, and no error of the mean is left but that of numbers as small as the differences.
+// them, and its square off theirs, and no error of the mean is left but that of numbers as small as the differences.  In rows
+// that differ by a few steps of fp32 those are small multiples of one step, whose sums are exact, and the mean comes out
+// as a sum of two numbers: a constant row gives 0 whatever its value, with a variance that is kept above 0.
 template <bool WARP, int CH, int VEC>
 __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], bool about_mean, int H, float eps, int col0, int step,
                                               RowReduce& red) {
@@ -154,6 +156,7 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], bool ab
       if (about_mean) {
         const float2 both = red.pair<WARP>(ss, s);
         ss = both.x, off = both.y * inv;
+        off = fmaf(fmaf(-off, (float)H, both.y), inv, off);  // exact where a quotient is
       } else {
         ss = red.run<WARP, false>(ss);
       }
@@ -164,10 +167,16 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[CH][VEC], bool ab
         for (int i = 0; i < VEC; ++i) ss = fmaf(v[c][i], v[c][i], ss);
       ss = red.run<WARP, false>(ss);
     }
-    float var = fmaf(ss, inv, eps * scale * scale);
-    if (about_mean) var = fmaxf(fmaf(-off, off, var), eps * scale * scale);  // (NaN comes through b)
+    const float least = eps * scale * scale;
+    float var = fmaf(ss, inv, least);
+    if (about_mean) var = fmaxf(fmaf(-off, off, var), fmaxf(least, 1.17549435e-38f));  // (a NaN comes through b)
     const float rstd = rsqrtf(var);
-    const RowStats st{scale, mean, about_mean ? rstd : scale * rstd, -off * rstd};
+    RowStats st{scale, mean, scale * rstd, 0.f};
+    if (about_mean) {  // mean + off = st.mean + rest, exactly
+      st.mean = mean + off;
+      const float o = st.mean - mean, rest = (mean - (st.mean - o)) + (off - o);
+      st.a = rstd, st.b = -rest * rstd;
+    }
     if (pass || ((ss >= 1e-30f || eps >= 1e-20f) && ss <= 1e36f)) return st;
     float m = 0.f;
 #pragma unroll
@@ -318,7 +327,7 @@ __device__ __forceinline__ void finish_row(const CombineNorm& a, long long t, fl
 }
 
 // A dense block's row (no slots).  A token needs the same two or three rows each time, so they need no list and no ring: their
-// next pieces are fetched into registers as soon as this token's have been used (17.0 us at 4096 x 2048 bf16, 23.9 through
+// next pieces are fetched into registers as soon as this token's have been used (17.1 us at 4096 x 2048 bf16, 23.9 through
 // the ring below).  A shared row, which a dense block seldom has, is read where it is added.
 template <typename T, bool WARP, int CH, bool MEANS>
 __global__ void __launch_bounds__(max_threads<WARP, CH>(), dense_ctas<WARP, CH>())
